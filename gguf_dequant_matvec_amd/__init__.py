@@ -38,6 +38,13 @@ OP_MOE = 2
 OP_GEMM_N = 3
 OP_SHORT_CONV = 4
 OP_GEMM = 5
+# types of a key-value cache (the GGUF ids of F16, I8 and BF16)
+KV_F16 = 1
+KV_I8 = 24
+KV_BF16 = 30
+KV_TYPES = {"f16": KV_F16, "i8": KV_I8, "bf16": KV_BF16}
+MAX_ATTN_N = 16
+MAX_KV_ROWS = 1 << 27
 MAX_K = 32768
 MAX_SEGMENTS = 8
 MAX_N = 16
@@ -53,7 +60,9 @@ EXPORTS = ["qmv_q8_0", "qmv_q4_k", "qmv_q6_k", "qmv_q4_0", "qmv_q4_1", "qmv_q5_0
            "qmv_q8_1", "qmv_q5_k", "qmv_q2_k", "qmv_q3_k", "qmv_fused_rows", "qmv_fused_rows2",
            "qmv_gate_up_silu", "qmv_short_conv", "qmv_argmax", "qmv_argmax_noalloc", "moe_qmv_topk", "qmv_gemm_n", "qmv_gemm", "qmv_dequant",
            "qmv_quantize", "qmv_row_bytes", "qmv_workspace_bytes", "qmv_last_hip_error",
-           "qmv_status_str", "qmv_probe_stream_read", "qmv_time_next_launch"]
+           "qmv_status_str", "qmv_probe_stream_read", "qmv_time_next_launch",
+           "qmv_kv_page_bytes", "qmv_kv_append", "qmv_attn_decode", "qmv_attn_decode_workspace",
+           "qmv_attn_prefill", "qmv_attn_prefill_workspace", "qmv_kv_evict"]
 
 
 class QmvError(RuntimeError):
@@ -81,6 +90,7 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     P, i64, i32, ci, sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int,
                            ctypes.c_size_t)
+    cf = ctypes.c_float
     sig = {
         "qmv_q8_0": [P, i64, i64, P, P, P],
         "qmv_q4_k": [P, i64, i64, P, P, P],
@@ -106,6 +116,10 @@ def load():
         "qmv_quantize": [ci, P, i64, i64, P, P],
         "qmv_probe_stream_read": [P, sz, P, P],
         "qmv_time_next_launch": [P, P],
+        "qmv_kv_append": [P, i64, P, P, i64, P, i64, P],
+        "qmv_attn_decode": [P, i32, i32, P, i64, cf, i32, i32, P, i64, P, i64, P, sz, P],
+        "qmv_attn_prefill": [P, i64, P, i32, P, i64, cf, i32, i32, P, i64, P, sz, P],
+        "qmv_kv_evict": [P, P, i64, i32, i32, i32, P, i64, P, P, i64, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -115,6 +129,12 @@ def load():
     lib.qmv_row_bytes.restype = sz
     lib.qmv_workspace_bytes.argtypes = [ci, i64, i64, i32, i32]
     lib.qmv_workspace_bytes.restype = sz
+    lib.qmv_kv_page_bytes.argtypes = [i32, i32, i32, i32]
+    lib.qmv_kv_page_bytes.restype = sz
+    lib.qmv_attn_decode_workspace.argtypes = [P, i32, i32, i64, i32, i32, i32]
+    lib.qmv_attn_decode_workspace.restype = sz
+    lib.qmv_attn_prefill_workspace.argtypes = [P, i64, i32, i64, i32, i32]
+    lib.qmv_attn_prefill_workspace.restype = sz
     lib.qmv_last_hip_error.argtypes = []
     lib.qmv_last_hip_error.restype = ci
     lib.qmv_status_str.argtypes = [ci]
@@ -299,6 +319,156 @@ def qmv_dequant(t, blocks, M, K, w_out, stream=None):
 
 def qmv_quantize(t, w, M, K, blocks_out, stream=None):
     _call("qmv_quantize", _type(t), _ptr(w), M, K, _ptr(blocks_out), _stream(stream))
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("pages", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64),
+                ("seq_len", ctypes.c_void_p), ("n_seq", ctypes.c_int64)]
+
+
+class KvCache:
+    """A paged key-value cache (qmv_kv_cache): `pages` a byte buffer of whole
+    pages, `table` int32 [n_seq][table_ld], `seq_len` int32 [n_seq], all on the
+    device.  Tensors are checked and kept alive; with raw addresses the counts
+    have to be given.  Lengths and table are read when a call runs, so both
+    may be changed in place between calls."""
+
+    def __init__(self, t, n_kv_heads, head_dim, page_size, pages, table, seq_len, n_pages=None,
+                 n_seq=None, table_ld=None):
+        t = KV_TYPES[t] if isinstance(t, str) else int(t)
+        page_bytes = int(load().qmv_kv_page_bytes(t, n_kv_heads, head_dim, page_size))
+        if not isinstance(pages, int):
+            if not pages.is_contiguous():
+                raise ValueError("pages must be contiguous")
+            have = pages.numel() * pages.element_size() // max(page_bytes, 1)
+            if n_pages is not None and n_pages > have:
+                raise ValueError(f"pages holds {have} pages, not {n_pages}")
+            n_pages = have if n_pages is None else n_pages
+        if not isinstance(table, int):
+            if str(table.dtype) != "torch.int32" or table.dim() != 2 or \
+                    (table.shape[1] > 1 and table.stride(1) != 1):
+                raise ValueError("table must be an int32 matrix with contiguous rows")
+            if n_seq is not None and n_seq > table.shape[0]:
+                raise ValueError(f"table has {table.shape[0]} rows, not {n_seq}")
+            n_seq = table.shape[0] if n_seq is None else n_seq
+            if table.shape[0] > 1 and table.stride(0) != table.shape[1]:
+                raise ValueError("table must be contiguous")
+            if table_ld is not None and table_ld != table.shape[1]:
+                raise ValueError(f"table rows have {table.shape[1]} entries, not {table_ld}")
+            table_ld = table.shape[1]
+        if not isinstance(seq_len, int):
+            if str(seq_len.dtype) != "torch.int32" or not seq_len.is_contiguous() or \
+                    seq_len.numel() < n_seq:
+                raise ValueError("seq_len must be n_seq contiguous int32 values")
+        self.type, self.n_kv_heads, self.head_dim, self.page_size = t, n_kv_heads, head_dim, page_size
+        self.page_bytes, self.n_pages, self.n_seq, self.table_ld = page_bytes, n_pages, n_seq, table_ld
+        self.pages, self.table, self.seq_len = pages, table, seq_len
+        self._struct = _KvCacheStruct(t, n_kv_heads, head_dim, page_size, n_pages, _ptr(pages),
+                                      _ptr(table), table_ld, _ptr(seq_len), n_seq)
+        self._address = ctypes.addressof(self._struct)
+
+
+def qmv_kv_page_bytes(t, n_kv_heads, head_dim, page_size) -> int:
+    t = KV_TYPES[t] if isinstance(t, str) else int(t)
+    return int(load().qmv_kv_page_bytes(t, n_kv_heads, head_dim, page_size))
+
+
+def _f32_rows(name, a, ld, n, width):
+    """Leading dimension of n rows of `width` f32 values."""
+    if a is None or isinstance(a, int):
+        return width if ld is None else ld
+    if str(a.dtype) != "torch.float32":
+        raise ValueError(f"{name} must be float32")
+    if ld is None:
+        inner = width
+        for i in range(a.dim() - 1, 0, -1):       # every dimension but the first is one row
+            if a.shape[i] > 1 and a.stride(i) != width // inner:
+                raise ValueError(f"the rows of {name} must be contiguous")
+            inner //= max(a.shape[i], 1)
+        if a.dim() < 2 or a.shape[0] < n or inner != 1:
+            raise ValueError(f"{name} must be {n} rows of {width} values")
+        ld = a.stride(0) if n > 1 else width
+    return ld
+
+
+def _check_start(cache, start):
+    if start is not None and not isinstance(start, int):
+        if str(start.dtype) != "torch.int32" or not start.is_contiguous() or \
+                start.numel() < cache.n_seq + 1:
+            raise ValueError("start must be n_seq + 1 contiguous int32 values")
+
+
+def _check_dense(name, a, dtype, numel):
+    if a is not None and not isinstance(a, int):
+        if str(a.dtype) != "torch." + dtype or not a.is_contiguous() or a.numel() < numel:
+            raise ValueError(f"{name} must hold {numel} contiguous {dtype} values")
+
+
+def qmv_kv_append(cache, n, k, v, start=None, ldk=None, ldv=None, stream=None):
+    width = cache.n_kv_heads * cache.head_dim
+    ldk, ldv = _f32_rows("k", k, ldk, n, width), _f32_rows("v", v, ldv, n, width)
+    _check_start(cache, start)
+    _call("qmv_kv_append", cache._address, n, _ptr(start), _ptr(k), ldk, _ptr(v), ldv,
+          _stream(stream))
+
+
+def qmv_attn_decode_workspace(cache, n, n_heads, max_len, window=0, sinks=0, with_acc=False) -> int:
+    return int(load().qmv_attn_decode_workspace(cache._address, n, n_heads, max_len, window, sinks,
+                                                int(bool(with_acc))))
+
+
+def _head_rows(name, a, ld, cache):
+    """Leading dimension of a [n_seq][n_kv_heads][ld] f32 array."""
+    if a is None or isinstance(a, int):
+        return 0 if ld is None else ld
+    if str(a.dtype) != "torch.float32" or a.dim() != 3 or not a.is_contiguous() or \
+            a.shape[0] < cache.n_seq or a.shape[1] != cache.n_kv_heads:
+        raise ValueError(f"{name} must be contiguous float32 [n_seq][n_kv_heads][positions]")
+    return a.shape[2]
+
+
+def qmv_attn_decode(cache, n, n_heads, q, scale, out, max_len, window=0, sinks=0, acc=None,
+                    workspace=None, ldq=None, ld_acc=None, ws_bytes=None, stream=None):
+    ldq = _f32_rows("q", q, ldq, cache.n_seq * n, n_heads * cache.head_dim)
+    _check_dense("out", out, "float32", cache.n_seq * n * n_heads * cache.head_dim)
+    ld_acc = _head_rows("acc", acc, ld_acc, cache)
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call("qmv_attn_decode", cache._address, n, n_heads, _ptr(q), ldq, scale, window, sinks,
+          _ptr(out), max_len, _ptr(acc), ld_acc, _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def qmv_attn_prefill_workspace(cache, n, n_heads, max_len, window=0, sinks=0) -> int:
+    return int(load().qmv_attn_prefill_workspace(cache._address, n, n_heads, max_len, window, sinks))
+
+
+def qmv_attn_prefill(cache, n, n_heads, q, scale, out, max_len, start=None, window=0, sinks=0,
+                     workspace=None, ldq=None, ws_bytes=None, stream=None):
+    ldq = _f32_rows("q", q, ldq, n, n_heads * cache.head_dim)
+    _check_dense("out", out, "float32", n * n_heads * cache.head_dim)
+    _check_start(cache, start)
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call("qmv_attn_prefill", cache._address, n, _ptr(start), n_heads, _ptr(q), ldq, scale, window,
+          sinks, _ptr(out), max_len, _ptr(workspace), ws_bytes, _stream(stream))
+
+
+def qmv_kv_evict(cache, dst_table, keep, first, recent, acc, kept, acc_out, len_out, dst_ld=None,
+                 ld_acc=None, ld_out=None, stream=None):
+    if not isinstance(dst_table, int):
+        if dst_table is None or dst_table.dim() != 2 or dst_table.shape[0] < cache.n_seq:
+            raise ValueError("dst_table must be a matrix with a row per sequence")
+        _check_dense("dst_table", dst_table, "int32", 0)
+        dst_ld = dst_table.shape[1]
+    ld_acc = _head_rows("acc", acc, ld_acc, cache)
+    ld_out = _head_rows("acc_out", acc_out, ld_out, cache)
+    _check_dense("kept", kept, "int32", cache.n_seq * cache.n_kv_heads * max(keep, 0))
+    _check_dense("len_out", len_out, "int32", cache.n_seq)
+    _call("qmv_kv_evict", cache._address, _ptr(dst_table), dst_ld, keep, first, recent, _ptr(acc),
+          ld_acc, _ptr(kept), _ptr(acc_out), ld_out, _ptr(len_out), _stream(stream))
 
 
 def qmv_probe_stream_read(buf, nbytes, sink, stream=None):

@@ -50,6 +50,8 @@ qmv_status from_hip(hipError_t e) {
 
 }  // namespace
 
+void set_last_hip_error(hipError_t e) { g_last_hip_error = (int)e; }
+
 void set_timing_hook(hipEvent_t start, hipEvent_t stop) {
     g_timing_hook.start = start;
     g_timing_hook.stop = stop;

@@ -1,0 +1,132 @@
+// Device pieces shared by the decode and prefill attention kernels: operand
+// types, the exact splits of f32 values into 16-bit pieces, the list of
+// visible chunks of a cache.
+#pragma once
+
+#include "qmv_device.h"
+#include "qmv_kv.h"
+
+namespace qmv {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+// Probabilities are held as 2^kBias 2^(x - m), at most 2^(kBias + kSlack) =
+// 2^15 because m is moved as soon as a logit exceeds it by kSlack: f16 pieces
+// (largest 65504, smallest step 2^-24) then resolve weights down to 2^-36 of
+// the row's largest.
+constexpr float kBias = 11.f, kSlack = 4.f;
+constexpr float kNoMax = -1e30f;  // running maximum before any visible position: finite, so x - m never is inf - inf
+
+// 8-bit V rows carry their scale into the probabilities; `vmul`, a power of
+// two, keeps the largest scale so far at most 1.  Before the first row:
+constexpr float kVmulNone = 0x1p100f;
+
+// Matrix-core operands of a cache type.  f32 queries and probabilities are
+// split into 16-bit pieces whose sum is the f32 value to 2^-22 or better (two
+// f16 pieces of 11 bits, three bf16 pieces of 8), and each piece takes one
+// matrix instruction; cached values are exact in the operand type (8-bit
+// codes are integers up to 127).  So products are f32-exact and only the f32
+// accumulation rounds.
+struct OpF16 {
+    typedef f16x8 Vec;
+    static constexpr int kPieces = 2;
+    // to nearest even, one instruction for both: two pieces are off by at
+    // most 2^-22 (truncation would leave 2^-20, all to one side)
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const f32x2 v = {a, b};
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return half_bits_to_float(w); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return half_bits_to_float(w >> 16); }
+    static __device__ __forceinline__ f32x4 mfma16(Vec a, Vec b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(Vec a, Vec b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+struct OpBF16 {
+    typedef bf16x8 Vec;
+    static constexpr int kPieces = 3;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {  // truncation
+        return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+    static __device__ __forceinline__ f32x4 mfma16(Vec a, Vec b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(Vec a, Vec b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <int TYPE>
+struct KvOp { typedef OpF16 Op; };
+template <>
+struct KvOp<kKvBF16> { typedef OpBF16 Op; };
+
+struct U128 { uint32_t w[4]; };
+template <class V>
+__device__ __forceinline__ V as_vec(U128 u) { return __builtin_bit_cast(V, u); }
+
+// f[8] as Op::kPieces operand vectors.  f is used up.
+template <class Op>
+__device__ __forceinline__ void split8(float *f, U128 *piece) {
+#pragma unroll
+    for (int p = 0; p < Op::kPieces; p++) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t w = Op::pack(f[2 * j], f[2 * j + 1]);
+            piece[p].w[j] = w;
+            if (p + 1 < Op::kPieces) {
+                f[2 * j] -= Op::lo(w);
+                f[2 * j + 1] -= Op::hi(w);
+            }
+        }
+    }
+}
+
+// Four int8 codes of a dword as two dwords of f16 pairs, exactly: 1024 + 128 +
+// code is the f16 whose low byte is the code with its sign bit flipped.
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t v) {
+    const uint32_t u = v ^ 0x80808080u;
+    const f16x2_t bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+    const uint32_t a = __builtin_amdgcn_perm(0x64646464u, u, 0x07010700u);
+    const uint32_t b = __builtin_amdgcn_perm(0x64646464u, u, 0x07030702u);
+    return make_uint2(__builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) - bias),
+                      __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, b) - bias));
+}
+
+// The chunks of `ck` positions that hold every position some query with
+// pmin <= p <= pmax sees: first those of the sinks, then those of the window.
+struct Chunks {
+    int sink, win0, n;
+    __device__ __forceinline__ int at(int i) const { return i < sink ? i : win0 + (i - sink); }
+};
+__device__ __forceinline__ Chunks visible_chunks(int pmin, int pmax, int window, int sinks, int ck) {
+    Chunks v;
+    const int end = pmax < 0 ? 0 : pmax / ck + 1;
+    v.sink = 0;
+    v.win0 = 0;
+    if (window > 0) {
+        const int lo = pmin - window + 1;  // first position in some query's window
+        v.win0 = lo > 0 ? lo / ck : 0;
+        const int sc = sinks > pmax ? end : (sinks + ck - 1) / ck;
+        v.sink = sc < v.win0 ? sc : v.win0;
+        if (v.sink > end) v.sink = end;
+    }
+    v.n = v.sink + (end > v.win0 ? end - v.win0 : 0);
+    return v;
+}
+
+__device__ __forceinline__ bool sees(int p, int key, int window, int sinks) {
+    return key <= p && (window <= 0 || key > p - window || key < sinks);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+}  // namespace qmv

@@ -1,0 +1,506 @@
+// Attention of the last n tokens of each sequence over its paged cache, split
+// over the cache's length and joined.
+//
+// The operation streams K and V once per key-value head; everything else is
+// arranged so that this stream never waits:
+//  - The rows (tokens x query heads of one key-value head) are the columns of
+//    the matrix operands, 16 at a time.  S^T = K Q^T puts one query in each
+//    lane column and keys in the accumulator rows; with the K rows handed to
+//    the operand in the order key = 8 g + 4 b + i (lane group g, tile b, row
+//    i), each lane ends up holding 8 consecutive keys of its query, which is
+//    the layout the second product O^T = V^T P^T wants its P operand in.  No
+//    value moves between lanes from K to O.
+//  - K rows are stored as they are read; V is stored in blocks of 16
+//    positions, column-major, so its operand is a 16-byte load as well.  Both
+//    go from memory to registers with no LDS in the loop.
+//  - The softmax maximum is lazy: O and the sum are rescaled only when some
+//    logit exceeds the running maximum by 2^kSlack; the probabilities then
+//    are at most 2^(kBias + kSlack), which f16 pieces hold.
+// A wave takes every fourth chunk of its workgroup's piece of the length, the
+// four waves are joined through LDS, and the pieces by a second launch.
+#include "qmv_attn.h"
+#include "qmv_internal.h"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+template <int TYPE>
+constexpr int kChunk = TYPE == kKvI8 ? 64 : 32;  // positions a wave takes at a time (16 KB at 128 columns)
+
+// Column of element j of the operand of step t in lane group g: 8-bit rows are
+// read in 16-byte pieces of two steps where 64 divides the row.
+template <int TYPE, int HD>
+__device__ __forceinline__ constexpr int col_of(int t, int g) {
+    return TYPE == kKvI8 && HD % 64 == 0 ? 64 * (t / 2) + 16 * g + 8 * (t % 2) : 32 * t + 8 * g;
+}
+
+template <int TYPE, int HD>
+struct Tile {  // one chunk in registers
+    static constexpr int SUB = kChunk<TYPE> / 32;       // sub-chunks of 32 positions
+    static constexpr int KW = TYPE == kKvI8 ? HD / 8 : HD / 8 * 2;  // dwords: 2 * SUB rows of HD / 4 columns
+    static constexpr int VW = HD / 16 * 4;              // dwords: HD / 16 columns of 16 bytes
+    uint32_t k[2 * SUB][KW / 2];
+    uint32_t v[VW];
+    float ks[TYPE == kKvI8 ? 16 : 1], vs[TYPE == kKvI8 ? 16 : 1];
+    bool ok;  // the lane group's positions are in a page (not a hole)
+
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int kpage, int vpage,
+                                         int g, int m) {
+        constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
+        constexpr int PER = kChunk<TYPE> / 4;  // positions of a lane group
+        const int pmask = (1 << c.page_shift) - 1;
+        const int kslot = (chunk * kChunk<TYPE> + PER * (m >> 2)) & pmask;
+        const int vslot = (chunk * kChunk<TYPE> + PER * g) & pmask;
+        ok = vpage >= 0;
+        const uint8_t *kp = kv_head(c, kpage < 0 ? 0 : kpage, h) + (int64_t)(kslot + (m & 3)) * (HD * SZ);
+#pragma unroll
+        for (int r = 0; r < 2 * SUB; r++) {  // rows + 4 r: tile b = r % 2 of sub-chunk r / 2
+            const uint8_t *row = kp + r * 4 * HD * SZ;
+            if constexpr (TYPE == kKvI8 && HD % 64 != 0) {
+#pragma unroll
+                for (int t = 0; t < HD / 32; t++) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(row + 32 * t + 8 * g);
+                    k[r][2 * t] = w.x, k[r][2 * t + 1] = w.y;
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < HD * SZ / 64; t++) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(row + 64 * t + 16 * g);
+                    k[r][4 * t] = w.x, k[r][4 * t + 1] = w.y, k[r][4 * t + 2] = w.z, k[r][4 * t + 3] = w.w;
+                }
+            }
+        }
+        const uint8_t *vhead = kv_head(c, vpage < 0 ? 0 : vpage, h) + ((int64_t)HD * SZ << c.page_shift);
+        const uint8_t *vp = vhead + (int64_t)(vslot / kVBlock) * (HD * kVBlock * SZ) + m * (kVBlock * SZ) + (vslot % kVBlock) * SZ;
+#pragma unroll
+        for (int t = 0; t < HD / 16; t++) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(vp + t * 16 * kVBlock * SZ);
+            v[4 * t] = w.x, v[4 * t + 1] = w.y, v[4 * t + 2] = w.z, v[4 * t + 3] = w.w;
+        }
+        if constexpr (TYPE == kKvI8) {
+            const float *sc = reinterpret_cast<const float *>(vhead + ((int64_t)HD << c.page_shift)) + vslot;
+#pragma unroll
+            for (int j = 0; j < 16; j++) ks[j] = sc[j];
+            sc += pmask + 1;
+#pragma unroll
+            for (int j = 0; j < 16; j++) vs[j] = sc[j];
+        }
+    }
+    // operand of K: tile b of sub-chunk u, step t
+    template <class Vec>
+    __device__ __forceinline__ Vec kop(int u, int b, int t) const {
+        U128 o;
+        const uint32_t *r = k[2 * u + b];
+        if constexpr (TYPE == kKvI8) {
+            const uint2 x = codes_to_f16(r[2 * t]), y = codes_to_f16(r[2 * t + 1]);
+            o = U128{{x.x, x.y, y.x, y.y}};
+        } else {
+            o = U128{{r[4 * t], r[4 * t + 1], r[4 * t + 2], r[4 * t + 3]}};
+        }
+        return as_vec<Vec>(o);
+    }
+    template <class Vec>
+    __device__ __forceinline__ Vec vop(int u, int t) const {
+        U128 o;
+        if constexpr (TYPE == kKvI8) {
+            const uint2 x = codes_to_f16(v[4 * t + 2 * u]), y = codes_to_f16(v[4 * t + 2 * u + 1]);
+            o = U128{{x.x, x.y, y.x, y.y}};
+        } else {
+            o = U128{{v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]}};
+        }
+        return as_vec<Vec>(o);
+    }
+};
+
+template <int TYPE, int HD, int RT, bool ACC>
+__global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
+    typedef typename KvOp<TYPE>::Op Op;
+    typedef typename Op::Vec Vec;
+    constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
+    constexpr int KS = HD / 32, DT = HD / 16;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, g = lane >> 4;
+    const int split = blockIdx.x, s = blockIdx.z;
+    const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
+    const KvArgs &c = a.c;
+    const int len = kv_len(c, s, a.limit);
+    const int n = (int)a.n;
+    const int nrows = n * a.group;
+    const int r0 = tile * 16 * RT;
+
+    // the rows of this tile and what they see
+    int pos[RT];
+    float qscale[RT];
+    U128 qf[RT][KS][NP];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int rr = r0 + rt * 16 + m;
+        const bool live = rr < nrows;
+        const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
+        pos[rt] = live ? len - n + j : -1;
+        const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
+        float f[KS][8];
+        float big = 0.f;
+#pragma unroll
+        for (int t = 0; t < KS; t++) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
+            const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+            const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                f[t][e] = live ? w[e] : 0.f;
+                big = fmaxf(big, fabsf(f[t][e]));
+            }
+        }
+        // f16 pieces: scale the row by a power of two so that its largest
+        // value is in [2^14, 2^15)
+        int sh = 0;
+        if constexpr (TYPE != kKvBF16) {
+            big = fmaxf(big, __shfl_xor(big, 16));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            if (big > 0.f && big < __builtin_inff()) {
+                sh = 15 - __builtin_amdgcn_frexp_expf(big);
+                sh = sh > 100 ? 100 : sh;
+            }
+        }
+        qscale[rt] = ldexpf(a.scale_log2, -sh);
+#pragma unroll
+        for (int t = 0; t < KS; t++) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
+            split8<Op>(f[t], qf[rt][t]);
+        }
+    }
+    const int last = r0 + 16 * RT < nrows ? r0 + 16 * RT - 1 : nrows - 1;
+    const int pmin = len - n + r0 / a.group, pmax = len - n + last / a.group;
+    const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, CK);
+    const int begin = (int)((int64_t)ch.n * split / a.splits), end = (int)((int64_t)ch.n * (split + 1) / a.splits);
+
+    float mrun[RT], lrun[RT];
+    f32x4 o[RT][DT];
+    float vmul = kVmulNone;  // 8-bit: power of two that brings the row scales of V to at most 1
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        mrun[rt] = kNoMax;
+        lrun[rt] = 0.f;
+#pragma unroll
+        for (int t = 0; t < DT; t++) o[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
+    auto page_of = [&](int i, int grp) {  // page of a lane group's positions in chunk number i
+        int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
+        if (pi > last_page) return -1;
+        const int pg = c.table[(int64_t)s * c.table_ld + pi];
+        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
+    };
+    for (int i = begin + wave; i < end; i += kWaves) {
+        Tile<TYPE, HD> kv;
+        kv.load(c, h, ch.at(i), page_of(i, m >> 2), page_of(i, g), g, m);
+        const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
+        // a chunk that every row sees whole needs no masks
+        const int c0 = ch.at(i) * CK, c1 = c0 + CK - 1;
+        const bool whole = c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks) && __all(kv.ok);
+        if constexpr (TYPE == kKvI8) {
+            float big = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                if (!whole) {
+                    const bool any = kv.ok && key0 + e <= pmax && (a.window <= 0 || key0 + e > pmin - a.window || key0 + e < a.sinks);
+                    kv.vs[e] = any ? kv.vs[e] : 0.f;
+                }
+                big = fmaxf(big, fabsf(kv.vs[e]));
+            }
+            if (__any(big * vmul > 1.f && big < __builtin_inff())) {
+                for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
+                int ex = __builtin_amdgcn_frexp_expf(big);
+                ex = ex > 120 ? 120 : ex;
+                const float nm = ldexpf(1.f, -ex);
+                const float r = nm / vmul;
+                vmul = nm;
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int t = 0; t < DT; t++) o[rt][t] *= r;
+            }
+        } else if (!whole) {
+            // V of positions no row sees: zero, whatever the page holds there
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                uint32_t keep = 0;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int key = key0 + 2 * w + e;
+                    if (kv.ok && key <= pmax && (a.window <= 0 || key > pmin - a.window || key < a.sinks)) keep |= 0xFFFFu << (16 * e);
+                }
+#pragma unroll
+                for (int t = 0; t < DT; t++) kv.v[4 * t + w] &= keep;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; u++) {
+            f32x4 sacc[RT][2];
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) sacc[rt][0] = sacc[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < KS; t++) {
+#pragma unroll
+                for (int b = 0; b < 2; b++) {
+                    const Vec kx = kv.template kop<Vec>(u, b, t);
+#pragma unroll
+                    for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                        for (int p = 0; p < NP; p++) sacc[rt][b] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][b]);
+                }
+            }
+            U128 pf[RT][NP];
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    x[e] = sacc[rt][e >> 2][e & 3] * qscale[rt];
+                    if constexpr (TYPE == kKvI8) x[e] *= kv.ks[8 * u + e];
+                    if (!whole) x[e] = kv.ok && sees(pos[rt], key0 + 8 * u + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                }
+                if constexpr (ACC) {
+                    const int rr = r0 + rt * 16 + m;
+                    if (rr < nrows) {
+                        float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0 + 8 * u;
+                        *reinterpret_cast<float4 *>(lp) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4 *>(lp + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                    }
+                }
+                float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                if (__any(mx > mrun[rt] + kSlack)) {
+                    mx = fmaxf(mx, __shfl_xor(mx, 16));
+                    mx = fmaxf(mx, __shfl_xor(mx, 32));
+                    const float mnew = fmaxf(mrun[rt], mx);
+                    const float r = exp2_fast(mrun[rt] - mnew);
+                    mrun[rt] = mnew;
+                    lrun[rt] *= r;
+#pragma unroll
+                    for (int t = 0; t < DT; t++) o[rt][t] *= r;
+                }
+                const float off = kBias - mrun[rt];
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    x[e] = exp2_fast(x[e] + off);
+                    sum += x[e];
+                    if constexpr (TYPE == kKvI8) x[e] *= kv.vs[8 * u + e] * vmul;
+                }
+                lrun[rt] += sum;
+                split8<Op>(x, pf[rt]);
+            }
+#pragma unroll
+            for (int t = 0; t < DT; t++) {
+                const Vec vx = kv.template vop<Vec>(u, t);
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][p]), o[rt][t]);
+            }
+        }
+    }
+
+    // join the four waves: a common maximum, then the partial sums pairwise
+    __shared__ float s_m[kWaves][RT * 16], s_l[kWaves][RT * 16];
+    __shared__ f32x4 s_o[2][RT * DT * 64];
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        lrun[rt] += __shfl_xor(lrun[rt], 16);
+        lrun[rt] += __shfl_xor(lrun[rt], 32);
+        if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
+    }
+    __syncthreads();
+    const float back = 1.f / vmul;
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        float mm = kNoMax;
+        for (int w = 0; w < kWaves; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
+        // (a NaN maximum cannot be: fmaxf drops NaN; a NaN sum stays)
+        const float r = exp2_fast(mrun[rt] - mm);
+        mrun[rt] = mm;
+        lrun[rt] *= r;
+        if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
+        const float ro = TYPE == kKvI8 ? r * back : r;
+#pragma unroll
+        for (int t = 0; t < DT; t++) o[rt][t] *= ro;
+    }
+    for (int half = 2; half; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                for (int t = 0; t < DT; t++) s_o[wave - half][(rt * DT + t) * 64 + lane] = o[rt][t];
+        }
+        __syncthreads();
+        if (wave < half) {
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave][(rt * DT + t) * 64 + lane];
+        }
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    const bool direct = a.splits == 1 && !ACC;
+#pragma unroll
+    for (int rt = 0; rt < RT; rt++) {
+        const int rr = r0 + rt * 16 + m;
+        if (rr >= nrows) continue;
+        const float l = (s_l[0][rt * 16 + m] + s_l[1][rt * 16 + m]) + (s_l[2][rt * 16 + m] + s_l[3][rt * 16 + m]);
+        float *dst;
+        float mul = 1.f;
+        if (direct) {
+            const int j = rr / a.group, hg = rr % a.group;
+            dst = a.out + (((int64_t)s * n + j) * a.n_heads + h * a.group + hg) * HD;
+            mul = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
+        } else {
+            const int64_t prow = ((int64_t)s * n + rr / a.group) * a.n_heads + h * a.group + rr % a.group;
+            const int64_t at = (int64_t)split * a.part_rows + prow;
+            if (g == 0) a.part_ml[at] = make_float2(mrun[rt], l);
+            dst = a.part_o + at * HD;
+        }
+#pragma unroll
+        for (int t = 0; t < DT; t++) {
+            const f32x4 v = o[rt][t] * mul;
+            __builtin_memcpy(dst + 16 * t + 4 * g, &v, 16);
+        }
+    }
+}
+
+// acc[s][h][key] += sum over the rows of 2^(x - m) / l, rows in order.
+template <int TYPE>
+__global__ __launch_bounds__(256) void attn_weights(AttnArgs a, int rt16) {
+    constexpr int CK = kChunk<TYPE>;
+    const int s = blockIdx.z, h = blockIdx.y;
+    const int len = kv_len(a.c, s, a.limit);
+    const int n = (int)a.n, nrows = n * a.group;
+    if ((int64_t)blockIdx.x * 256 >= len) return;
+    const int key = blockIdx.x * 256 + threadIdx.x;
+    const int64_t head = (int64_t)s * a.c.n_kv + h;
+    __shared__ float s_m[16], s_r[16];
+    float sum = 0.f;
+    for (int r0 = 0; r0 < nrows; r0 += 16) {
+        __syncthreads();
+        const int row = threadIdx.x >> 4, l16 = threadIdx.x & 15;
+        if (r0 + row < nrows) {
+            const int rr = r0 + row;
+            const int64_t prow = ((int64_t)s * n + rr / a.group) * a.n_heads + h * a.group + rr % a.group;
+            float mm = kNoMax, l = 0.f;
+            for (int i = l16; i < a.splits; i += 16) mm = fmaxf(mm, a.part_ml[i * a.part_rows + prow].x);
+            for (int off = 8; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off, 16));
+            for (int i = l16; i < a.splits; i += 16) {
+                const float2 ml = a.part_ml[i * a.part_rows + prow];
+                l += exp2_fast(ml.x - mm) * ml.y;
+            }
+            for (int off = 8; off; off >>= 1) l += __shfl_xor(l, off, 16);
+            if (l16 == 0) {
+                s_m[row] = mm - kBias;  // l carries 2^kBias
+                s_r[row] = l == 0.f ? 0.f : 1.f / l;
+            }
+        }
+        __syncthreads();
+        if (key < len) {
+            for (int i = 0; i < 16 && r0 + i < nrows; i++) {
+                // what this row's tile read: other logits were not written
+                const int t0 = (r0 + i) / rt16 * rt16;
+                const int t1 = t0 + rt16 < nrows ? t0 + rt16 - 1 : nrows - 1;
+                const int pmin = len - n + t0 / a.group, pmax = len - n + t1 / a.group;
+                const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, CK);
+                const int k = key / CK;
+                const bool read = k < ch.sink || (k >= ch.win0 && k < ch.win0 + (ch.n - ch.sink));
+                if (read && s_r[i] != 0.f) {
+                    const float x = a.logits[(head * nrows + r0 + i) * a.ld_logits + key];
+                    sum += exp2_fast(x - s_m[i]) * s_r[i];
+                }
+            }
+        }
+    }
+    if (key < len) a.acc[head * a.ld_acc + key] += sum;
+}
+
+template <int TYPE, int HD, int RT>
+hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    const dim3 grid(p.splits, a.c.n_kv * p.tiles, a.c.n_seq);
+    hipError_t e;
+    if (a.acc)
+        e = launch_main(attn_decode<TYPE, HD, RT, true>, grid, dim3(kWaves * 64), 0, s, a);
+    else
+        e = launch_main(attn_decode<TYPE, HD, RT, false>, grid, dim3(kWaves * 64), 0, s, a);
+    if (e != hipSuccess || (p.splits == 1 && !a.acc)) return e;
+    e = launch_attn_join(a, s);
+    if (e != hipSuccess || !a.acc) return e;
+    return launch_aux(attn_weights<TYPE>, dim3((a.limit + 255) / 256, a.c.n_kv, a.c.n_seq), dim3(256), 0, s, a, 16 * RT);
+}
+
+template <int TYPE, int HD>
+hipError_t launch_hd(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    return p.rt == 2 ? launch_typed<TYPE, HD, 2>(a, p, s) : launch_typed<TYPE, HD, 1>(a, p, s);
+}
+
+template <int TYPE>
+hipError_t launch_type(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    switch (a.c.hd) {
+    case 64: return launch_hd<TYPE, 64>(a, p, s);
+    case 96: return launch_hd<TYPE, 96>(a, p, s);
+    case 128: return launch_hd<TYPE, 128>(a, p, s);
+    case 256: return launch_typed<TYPE, 256, 1>(a, p, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int n,
+                          int64_t max_len, int window, int sinks, bool with_acc) {
+    AttnPlan p{};
+    const int64_t rows = (int64_t)n * group;
+    p.rt = rows > 16 && hd <= 128 ? 2 : 1;
+    p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+    p.part_rows = n_seq * n_kv * rows;
+    // the most positions a tile reads, in chunks
+    const int ck = type == kKvI8 ? 64 : 32;
+    int64_t most = max_len;
+    if (window > 0) {
+        const int64_t w = (int64_t)window + n + sinks + 2 * ck;
+        if (w < most) most = w;
+    }
+    const int64_t chunks = (most + ck - 1) / ck;
+    const int64_t base = n_seq * n_kv * p.tiles;
+    int64_t splits = (1024 + base - 1) / base;       // two to four workgroups per compute unit
+    if (splits > chunks / 8) splits = chunks / 8;    // at least two chunks per wave
+    if (splits > 128) splits = 128;
+    p.splits = splits < 1 ? 1 : (int)splits;
+    size_t at = 0;
+    if (p.splits > 1 || with_acc) {
+        p.ml_off = at;
+        at = up256(at + sizeof(float2) * (size_t)p.splits * p.part_rows);
+        p.o_off = at;
+        at = up256(at + sizeof(float) * (size_t)p.splits * p.part_rows * hd);
+    }
+    if (with_acc) {
+        p.ld_logits = (max_len + ck - 1) / ck * ck;
+        p.logits_off = at;
+        at = up256(at + sizeof(float) * (size_t)p.part_rows * p.ld_logits);
+    }
+    p.bytes = at;
+    return p;
+}
+
+hipError_t launch_attn_decode(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    switch (type) {
+    case kKvF16: return launch_type<kKvF16>(a, p, s);
+    case kKvBF16: return launch_type<kKvBF16>(a, p, s);
+    case kKvI8: return launch_type<kKvI8>(a, p, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmv

@@ -1,0 +1,472 @@
+// Causal attention of prompts over a paged cache, with an optional sliding
+// window and first tokens that stay visible.
+//
+// Compute-bound: 4 * visible * head_dim operations a row, each product taking
+// two f16 (three bf16) matrix instructions because queries and probabilities
+// are f32.  A workgroup takes 128 rows (tokens x query heads of one key-value
+// head, so the heads of a group share every K and V tile), 32 per wave, and
+// walks over the visible chunks of 64 positions.  A chunk is staged through
+// two LDS buffers by all four waves, wave w taking positions 16 w .. 16 w + 15
+// (one page, one V block: 1 KB runs), while the previous chunk is computed.
+// The products are S^T = K Q^T and O^T = V^T P^T: K rows lie in LDS in the
+// order in which the 32x32 operand takes them so that each lane's
+// accumulators are 8 consecutive positions of its query, the operand layout
+// of P, and no value moves between lanes.  K rows are padded by 16 bytes and V
+// keeps the cache's block layout; both are read without bank conflicts.
+#include "qmv_attn.h"
+#include "qmv_internal.h"
+
+namespace qmv {
+
+namespace {
+
+constexpr int kBM = 128, kBK = 64;
+
+template <int HD>
+struct Lds {  // one buffer, bytes
+    static constexpr int kRow = HD * 2 + 16;            // K row
+    static constexpr int kV = kBK * kRow;               // V blocks
+    static constexpr int kScale = kV + kBK * HD * 2;    // row scales of K, then of V
+    static constexpr int kBytes = kScale + 2 * kBK * 4;
+    static constexpr int kOk = 2 * kBytes;              // per buffer: 4 flags, one a block
+    static constexpr int kTotal = kOk + 32;
+};
+
+// LDS row of position j (0..31) of a half chunk: operand row 8 b + 4 h + i
+// holds position 16 (b / 2) + 8 h + 4 (b % 2) + i.
+__device__ __forceinline__ int krow(int j) { return (j & 16) | ((j & 4) << 1) | ((j & 8) >> 1) | (j & 3); }
+
+template <int TYPE, int HD>
+struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
+    static constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
+    static constexpr int PIECES = HD * SZ;  // 16-byte pieces of 16 K rows, and of a V block
+    static constexpr int N = (PIECES + 63) / 64;
+    uint4 k[N], v[N];
+    float sc;
+    bool ok;
+
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int page, int pos, int lane) {
+        ok = page >= 0;
+        const uint8_t *base = kv_head(c, page < 0 ? 0 : page, h);
+        const int slot = pos & ((1 << c.page_shift) - 1);
+        const uint8_t *kp = base + (int64_t)slot * (HD * SZ);
+        const uint8_t *vp = base + ((int64_t)(HD * SZ) << c.page_shift) + (int64_t)slot * (HD * SZ);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            if (PIECES % 64 == 0 || lane + 64 * i < PIECES) {
+                k[i] = *reinterpret_cast<const uint4 *>(kp + (lane + 64 * i) * 16);
+                v[i] = *reinterpret_cast<const uint4 *>(vp + (lane + 64 * i) * 16);
+            }
+        }
+        if constexpr (TYPE == kKvI8) {
+            const float *s = reinterpret_cast<const float *>(base + ((int64_t)(2 * HD) << c.page_shift));
+            sc = lane < 32 ? s[((lane >> 4) << c.page_shift) + slot + (lane & 15)] : 0.f;
+        }
+    }
+    // live: positions of the 16 that some row may see; V of the others is zero
+    __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live) const {
+        if (!ok) live = 0;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int p = lane + 64 * i;
+            if (PIECES % 64 != 0 && p >= PIECES) break;
+            const int row = (p * 16) / (HD * SZ), at = (p * 16) % (HD * SZ);  // K: position, byte
+            const int j = 16 * w + row;
+            uint8_t *kd = buf + ((j & 32) + krow(j & 31)) * Lds<HD>::kRow;
+            if constexpr (TYPE == kKvI8) {
+                const uint2 a = codes_to_f16(k[i].x), b = codes_to_f16(k[i].y), c2 = codes_to_f16(k[i].z), d = codes_to_f16(k[i].w);
+                *reinterpret_cast<uint4 *>(kd + at * 2) = make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4 *>(kd + at * 2 + 16) = make_uint4(c2.x, c2.y, d.x, d.y);
+                const uint2 e = codes_to_f16(v[i].x), f = codes_to_f16(v[i].y), g = codes_to_f16(v[i].z), o = codes_to_f16(v[i].w);
+                uint8_t *vd = buf + Lds<HD>::kV + (w * HD + p) * 32;  // a piece is one column
+                *reinterpret_cast<uint4 *>(vd) = make_uint4(e.x, e.y, f.x, f.y);
+                *reinterpret_cast<uint4 *>(vd + 16) = make_uint4(g.x, g.y, o.x, o.y);
+            } else {
+                *reinterpret_cast<uint4 *>(kd + at) = k[i];
+                uint4 x = v[i];
+                if (live < 16) {
+                    const int e0 = live - 8 * (p & 1);  // positions of this piece that count
+                    x.x &= e0 >= 2 ? ~0u : e0 == 1 ? 0xFFFFu : 0u;
+                    x.y &= e0 >= 4 ? ~0u : e0 == 3 ? 0xFFFFu : 0u;
+                    x.z &= e0 >= 6 ? ~0u : e0 == 5 ? 0xFFFFu : 0u;
+                    x.w &= e0 >= 8 ? ~0u : e0 == 7 ? 0xFFFFu : 0u;
+                }
+                *reinterpret_cast<uint4 *>(buf + Lds<HD>::kV + w * HD * 32 + p * 16) = x;
+            }
+        }
+        if constexpr (TYPE == kKvI8) {
+            if (lane < 32)
+                reinterpret_cast<float *>(buf + Lds<HD>::kScale)[(lane >> 4) * kBK + 16 * w + (lane & 15)] = (lane & 15) < live ? sc : 0.f;
+        }
+        if (lane == 0) flag[w] = ok;
+    }
+};
+
+template <int TYPE, int HD>
+__global__ __launch_bounds__(256) void attn_prefill(AttnArgs a) {
+    typedef typename KvOp<TYPE>::Op Op;
+    typedef typename Op::Vec Vec;
+    constexpr int KS = HD / 16, DT = HD / 32, NP = Op::kPieces;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int col = lane & 31, hh = lane >> 5;
+    const int h = blockIdx.x, split = blockIdx.z;
+    const KvArgs &c = a.c;
+
+    // which sequence and tile: the last tiles, which see the most, first
+    int slot = gridDim.y - 1 - blockIdx.y;
+    int s, tile;
+    int64_t row0, n;
+    if (!a.start) {
+        n = a.n;
+        const int per = (int)((n * a.group + kBM - 1) / kBM);
+        s = slot / per;
+        tile = slot % per;
+        row0 = (int64_t)s * n;
+    } else {
+        s = -1;
+        for (int base = 0; base < c.n_seq; base += 64) {
+            int64_t cnt = 0;
+            if (base + lane < c.n_seq) {
+                const int64_t len = (int64_t)a.start[base + lane + 1] - a.start[base + lane];
+                cnt = len > 0 ? (len * a.group + kBM - 1) / kBM : 0;
+            }
+            int64_t upto = cnt;
+            for (int off = 1; off < 64; off <<= 1) {
+                const int64_t x = __shfl_up(upto, off);
+                if (lane >= off) upto += x;
+            }
+            const int64_t all = __shfl(upto, 63);
+            if (slot < all) {
+                const int who = __builtin_ctzll(__ballot(upto > slot));
+                s = base + who;
+                tile = slot - (int)__shfl(upto - cnt, who);
+                break;
+            }
+            slot -= (int)all;
+        }
+        if (s < 0) return;
+        s = __builtin_amdgcn_readfirstlane(s);
+        tile = __builtin_amdgcn_readfirstlane(tile);
+        row0 = a.start[s];
+        n = (int64_t)a.start[s + 1] - row0;
+    }
+    const int len = kv_len(c, s, a.limit);
+    const int64_t nrows = n * a.group;
+    const int64_t r0 = (int64_t)tile * kBM;
+
+    // this wave's rows
+    const int64_t rr = r0 + 32 * wave + col;
+    const int64_t tok = rr / a.group;
+    const int hg = (int)(rr % a.group);
+    const int64_t row = row0 + tok;
+    const bool live = rr < nrows && row >= 0 && row < a.rows;
+    const int64_t pos64 = (int64_t)len - n + tok;
+    const int pos = live && pos64 >= 0 ? (int)pos64 : -1;
+    U128 qf[KS][NP];
+    float qscale;
+    {
+        const float *qp = a.q + (live ? row : 0) * a.ldq + (int64_t)(h * a.group + (live ? hg : 0)) * HD + 8 * hh;
+        float big = 0.f;
+        int sh = 0;
+        if constexpr (TYPE != kKvBF16) {
+#pragma unroll
+            for (int t = 0; t < KS; t++) {
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
+                const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+                big = fmaxf(big, fmaxf(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))),
+                                       fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)))));
+            }
+            big = fmaxf(big, __shfl_xor(big, 32));
+            if (big > 0.f && big < __builtin_inff()) {
+                sh = 15 - __builtin_amdgcn_frexp_expf(big);
+                sh = sh > 100 ? 100 : sh;
+            }
+        }
+        qscale = ldexpf(a.scale_log2, -sh);
+#pragma unroll
+        for (int t = 0; t < KS; t++) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
+            const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+            float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; e++) f[e] = live ? ldexpf(f[e], sh) : 0.f;
+            split8<Op>(f, qf[t]);
+        }
+    }
+    // what the tile's and this wave's rows see
+    auto pos_of = [&](int64_t r) {
+        const int64_t p = (int64_t)len - n + (r < nrows ? r : nrows - 1) / a.group;
+        return p < -1 ? -1 : (int)p;
+    };
+    const int pmin = pos_of(r0), pmax = pos_of(r0 + kBM - 1);
+    const bool wave_live = r0 + 32 * wave < nrows;
+    const int wmin = pos_of(r0 + 32 * wave), wmax = wave_live ? pos_of(r0 + 32 * wave + 31) : -1;
+    const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, kBK);
+    const int begin = (int)((int64_t)ch.n * split / a.splits), end = (int)((int64_t)ch.n * (split + 1) / a.splits);
+
+    float mrun = kNoMax, lrun = 0.f, vmul = kVmulNone;
+    f32x16 o[DT];
+#pragma unroll
+    for (int t = 0; t < DT; t++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[t][e] = 0.f;
+
+    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
+    auto page_of = [&](int i) {  // page of this wave's 16 positions of chunk number i
+        if (i >= end) return -1;
+        const int pi = (ch.at(i) * kBK + 16 * wave) >> c.page_shift;
+        if (pi > last_page) return -1;
+        const int pg = c.table[(int64_t)s * c.table_ld + pi];
+        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
+    };
+    auto live_of = [&](int i) {  // how many of its 16 positions some row of the tile sees
+        const int left = pmax + 1 - (ch.at(i) * kBK + 16 * wave);
+        return left > 16 ? 16 : left < 0 ? 0 : left;
+    };
+    Stage<TYPE, HD> st;
+    int page = __builtin_amdgcn_readfirstlane(page_of(begin));
+    if (begin < end) {
+        st.load(c, h, page, ch.at(begin) * kBK + 16 * wave, lane);
+        st.store(lds + (begin & 1) * Lds<HD>::kBytes, lds + Lds<HD>::kOk + (begin & 1) * 4, wave, lane, live_of(begin));
+    }
+    page = __builtin_amdgcn_readfirstlane(page_of(begin + 1));
+    for (int i = begin; i < end; i++) {
+        uint8_t *buf = lds + (i & 1) * Lds<HD>::kBytes;
+        const bool more = i + 1 < end;
+        if (more) st.load(c, h, page, ch.at(i + 1) * kBK + 16 * wave, lane);
+        const int next_page = page_of(i + 2);
+        __syncthreads();  // buffer i is written; everyone is done with buffer i - 1
+        const uint32_t okf = *reinterpret_cast<const uint32_t *>(lds + Lds<HD>::kOk + (i & 1) * 4);
+        const float *ksc = reinterpret_cast<const float *>(buf + Lds<HD>::kScale);
+        const float *vsc = ksc + kBK;
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            const int c0 = ch.at(i) * kBK + 32 * half, c1 = c0 + 31;
+            // nothing for this wave's rows here?
+            if (c0 > wmax || (a.window > 0 && c1 <= wmin - a.window && c0 >= a.sinks)) continue;
+            const uint32_t ok2 = __builtin_amdgcn_readfirstlane((okf >> (16 * half)) & 0x0101u);
+            const bool whole = c1 <= wmin && (a.window <= 0 || c0 > wmax - a.window || c1 < a.sinks) && ok2 == 0x0101u;
+            f32x16 sa;
+#pragma unroll
+            for (int e = 0; e < 16; e++) sa[e] = 0.f;
+            const uint8_t *kp = buf + (32 * half + col) * Lds<HD>::kRow + 16 * hh;
+#pragma unroll
+            for (int t = 0; t < KS; t++) {
+                const Vec kx = *reinterpret_cast<const Vec *>(kp + 32 * t);
+#pragma unroll
+                for (int p = 0; p < NP; p++) sa = Op::mfma32(kx, as_vec<Vec>(qf[t][p]), sa);
+            }
+            float x[16];
+            float mx = -__builtin_inff(), vbig = 0.f;
+            f32x4 vs[4];
+#pragma unroll
+            for (int e = 0; e < 16; e++) x[e] = sa[e] * qscale;
+            if constexpr (TYPE == kKvI8) {
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    const int at = 32 * half + 16 * (u >> 1) + 8 * hh + 4 * (u & 1);
+                    const f32x4 ks = *reinterpret_cast<const f32x4 *>(ksc + at);
+                    vs[u] = *reinterpret_cast<const f32x4 *>(vsc + at);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        x[4 * u + e] *= ks[e];
+                        vbig = fmaxf(vbig, fabsf(vs[u][e]));
+                    }
+                }
+            }
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const int key = c0 + 16 * (e >> 3) + 8 * hh + (e & 7);
+                    const bool in = (ok2 >> (8 * (e >> 3))) & 1;
+                    x[e] = in && sees(pos, key, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e++) mx = fmaxf(mx, x[e]);
+            if (__any(mx > mrun + kSlack)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 32));
+                const float mnew = fmaxf(mrun, mx);
+                const float r = exp2_fast(mrun - mnew);
+                mrun = mnew;
+                lrun *= r;
+#pragma unroll
+                for (int t = 0; t < DT; t++) o[t] *= r;
+            }
+            if constexpr (TYPE == kKvI8) {
+                if (__any(vbig * vmul > 1.f && vbig < __builtin_inff())) {
+                    for (int off = 32; off; off >>= 1) vbig = fmaxf(vbig, __shfl_xor(vbig, off));
+                    int ex = __builtin_amdgcn_frexp_expf(vbig);
+                    ex = ex > 120 ? 120 : ex;
+                    const float nm = ldexpf(1.f, -ex);
+                    const float r = nm / vmul;
+                    vmul = nm;
+#pragma unroll
+                    for (int t = 0; t < DT; t++) o[t] *= r;
+                }
+            }
+            const float off = kBias - mrun;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                x[e] = exp2_fast(x[e] + off);
+                sum += x[e];
+                if constexpr (TYPE == kKvI8) x[e] *= vs[e >> 2][e & 3] * vmul;
+            }
+            lrun += sum;
+            U128 pf[2][NP];
+            split8<Op>(x, pf[0]);
+            split8<Op>(x + 8, pf[1]);
+            const uint8_t *vp = buf + Lds<HD>::kV + (2 * half * HD + col) * 32 + 16 * hh;
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+#pragma unroll
+                for (int t = 0; t < DT; t++) {
+                    const Vec vx = *reinterpret_cast<const Vec *>(vp + u * HD * 32 + t * 32 * 32);
+#pragma unroll
+                    for (int p = 0; p < NP; p++) o[t] = Op::mfma32(vx, as_vec<Vec>(pf[u][p]), o[t]);
+                }
+            }
+        }
+        if (more)
+            st.store(lds + ((i + 1) & 1) * Lds<HD>::kBytes, lds + Lds<HD>::kOk + ((i + 1) & 1) * 4, wave, lane, live_of(i + 1));
+        page = __builtin_amdgcn_readfirstlane(next_page);
+    }
+
+    lrun += __shfl_xor(lrun, 32);
+    if (!live) return;
+    const int64_t orow = row * a.n_heads + h * a.group + hg;
+    float mul = TYPE == kKvI8 ? 1.f / vmul : 1.f;
+    float *dst;
+    if (a.splits == 1) {
+        mul = lrun == 0.f ? 0.f : mul / lrun;  // a row that sees nothing: zeros
+        dst = a.out + orow * HD;
+    } else {
+        const int64_t at = (int64_t)split * a.part_rows + orow;
+        if (hh == 0) a.part_ml[at] = make_float2(mrun, lrun);
+        dst = a.part_o + at * HD;
+    }
+#pragma unroll
+    for (int t = 0; t < DT; t++) {
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+            const f32x4 v = f32x4{o[t][4 * b], o[t][4 * b + 1], o[t][4 * b + 2], o[t][4 * b + 3]} * mul;
+            __builtin_memcpy(dst + 32 * t + 8 * b + 4 * hh, &v, 16);
+        }
+    }
+}
+
+// Joins the pieces of a row: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// One workgroup a row; its four waves take every fourth piece.
+template <int HD>
+__global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
+    constexpr int PER = (HD + 63) / 64;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int64_t prow = blockIdx.x;
+    if (a.start) {  // rows of no sequence stay as they were
+        const int64_t row = prow / a.n_heads;
+        if (row < a.start[0] || row >= a.start[a.c.n_seq]) return;
+    }
+    float mm = kNoMax;
+    for (int i = lane; i < a.splits; i += 64) mm = fmaxf(mm, a.part_ml[i * a.part_rows + prow].x);
+    for (int off = 32; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
+    float l = 0.f, o[PER];
+    for (int e = 0; e < PER; e++) o[e] = 0.f;
+    for (int i = wave; i < a.splits; i += 4) {
+        const int64_t at = i * a.part_rows + prow;
+        const float2 ml = a.part_ml[at];
+        const float r = exp2_fast(ml.x - mm);
+        l += r * ml.y;
+        for (int e = 0; e < PER; e++)
+            if (HD % 64 == 0 || lane + 64 * e < HD) o[e] += r * a.part_o[at * HD + lane + 64 * e];
+    }
+    __shared__ float s_l[4], s_o[4][PER * 64];
+    if (lane == 0) s_l[wave] = l;
+    for (int e = 0; e < PER; e++) s_o[wave][lane + 64 * e] = o[e];
+    __syncthreads();
+    if (tid >= HD) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    const float v = (s_o[0][tid] + s_o[1][tid]) + (s_o[2][tid] + s_o[3][tid]);
+    a.out[prow * HD + tid] = l == 0.f ? 0.f : v / l;
+}
+
+template <int TYPE, int HD>
+hipError_t launch_typed(const AttnArgs &a, int64_t slots, hipStream_t s) {
+    const void *fn = (const void *)attn_prefill<TYPE, HD>;
+    hipError_t e = ensure_lds(fn, Lds<HD>::kTotal);
+    if (e != hipSuccess) return e;
+    const dim3 grid(a.c.n_kv, (uint32_t)slots, a.splits);
+    e = launch_main(attn_prefill<TYPE, HD>, grid, dim3(256), Lds<HD>::kTotal, s, a);
+    if (e != hipSuccess || a.splits == 1) return e;
+    return launch_attn_join(a, s);
+}
+
+template <int TYPE>
+hipError_t launch_type(const AttnArgs &a, int64_t slots, hipStream_t s) {
+    switch (a.c.hd) {
+    case 64: return launch_typed<TYPE, 64>(a, slots, s);
+    case 96: return launch_typed<TYPE, 96>(a, slots, s);
+    case 128: return launch_typed<TYPE, 128>(a, slots, s);
+    case 256: return launch_typed<TYPE, 256>(a, slots, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+hipError_t launch_attn_join(const AttnArgs &a, hipStream_t s) {
+    const dim3 grid((uint32_t)a.part_rows);
+    switch (a.c.hd) {
+    case 64: return launch_aux(attn_join<64>, grid, dim3(256), 0, s, a);
+    case 96: return launch_aux(attn_join<96>, grid, dim3(256), 0, s, a);
+    case 128: return launch_aux(attn_join<128>, grid, dim3(256), 0, s, a);
+    case 256: return launch_aux(attn_join<256>, grid, dim3(256), 0, s, a);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+AttnPlan attn_prefill_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int64_t rows,
+                           int64_t max_len, int window, int sinks) {
+    AttnPlan p{};
+    (void)type;
+    // row tiles: at least these; with prompts of different lengths each
+    // sequence may add a partly filled one
+    const int64_t tiles = (rows * group + kBM - 1) / kBM;
+    p.tiles = (int)(tiles + n_seq);
+    p.part_rows = rows * n_kv * group;
+    int64_t most = max_len;
+    if (window > 0) {
+        const int64_t w = (int64_t)window + kBM / group + sinks + 2 * kBK;
+        if (w < most) most = w;
+    }
+    const int64_t chunks = (most + kBK - 1) / kBK;
+    const int64_t base = tiles * n_kv;
+    int64_t splits = 512 / base;                      // two workgroups per compute unit
+    if (splits > chunks / 4) splits = chunks / 4;     // at least four chunks each
+    if (splits > 64) splits = 64;
+    p.splits = splits < 1 ? 1 : (int)splits;
+    size_t at = 0;
+    if (p.splits > 1) {
+        p.ml_off = at;
+        at = up256(at + sizeof(float2) * (size_t)p.splits * p.part_rows);
+        p.o_off = at;
+        at = up256(at + sizeof(float) * (size_t)p.splits * p.part_rows * hd);
+    }
+    p.bytes = at;
+    return p;
+}
+
+hipError_t launch_attn_prefill(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    const int64_t slots = a.start ? p.tiles : a.c.n_seq * ((a.n * a.group + kBM - 1) / kBM);
+    switch (type) {
+    case kKvF16: return launch_type<kKvF16>(a, slots, s);
+    case kKvBF16: return launch_type<kKvBF16>(a, slots, s);
+    case kKvI8: return launch_type<kKvI8>(a, slots, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmv

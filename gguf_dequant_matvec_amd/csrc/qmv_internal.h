@@ -53,6 +53,8 @@ struct TimingHook {
     hipEvent_t start = nullptr, stop = nullptr;
 };
 void set_timing_hook(hipEvent_t start, hipEvent_t stop);
+// The code qmv_last_hip_error() reports on this thread.
+void set_last_hip_error(hipError_t e);
 TimingHook take_timing_hook();
 
 // Enqueue `kernel` and return the status of this enqueue itself (not a

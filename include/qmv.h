@@ -54,6 +54,12 @@
  *    the timing hook below).  Calls on one stream run in order; calls on
  *    different streams must not share an output or a workspace.
  *  - Shapes: M >= 1, K >= 1, K a multiple of B, K <= QMV_MAX_K.
+ *  - Attention: between the QKV product and the O product of a layer stand a
+ *    paged key-value cache (qmv_kv_append), attention over it for one to 16
+ *    new tokens (qmv_attn_decode) and for prompts (qmv_attn_prefill), and the
+ *    cache's eviction (qmv_kv_evict).  BebeLM page, section "核心算子" (GQA
+ *    with 32 query and 8 key-value heads, causal mask, KV cache); FlareLLM
+ *    page, section "推理层面的深度优化" (online softmax in one pass).
  */
 #ifndef QMV_H
 #define QMV_H
@@ -334,6 +340,150 @@ qmv_status qmv_dequant(qmv_type t, const void *blocks, int64_t M, int64_t K, flo
  * Q6_K s = max|w|/31, d = max s/126; codes rounded half away from zero. */
 qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *blocks_out,
                         hipStream_t stream);
+
+/* ---- paged key-value cache -------------------------------------------------
+ * A cache is a pool of equal pages in one device buffer and a table that says
+ * which page holds which positions of which sequence.  Nefm page, section
+ * "KV-cache机制详解" (keys and values of earlier tokens are kept).
+ *
+ * Types of the cached values:
+ *   QMV_KV_F16, QMV_KV_BF16: the value rounded to nearest even (beyond the
+ *     type's range: infinity);
+ *   QMV_KV_I8: int8 codes with one f32 scale per row (the head_dim values of
+ *     one position and head): scale = max|x| / 127, code = round(x / scale)
+ *     (to nearest even), 0 if the row is zero; value = scale * code.
+ *
+ * A page holds, for each key-value head in turn, the bytes
+ *   K  [page_size][head_dim]            rows of the positions,
+ *   V  [page_size / 16][head_dim][16]   blocks of 16 positions, each column's
+ *                                       16 values next to each other,
+ *   QMV_KV_I8 only: f32 K scale[page_size], f32 V scale[page_size];
+ * qmv_kv_page_bytes() bytes in all.  Position p of sequence s is slot
+ * p % page_size of page table[s * table_ld + p / page_size].  A table entry
+ * outside 0 .. n_pages - 1 is a hole: appending there writes nothing, and
+ * attention does not see its positions (a sliding window's pages can be given
+ * back that way).
+ *
+ * Positions 0 .. seq_len[s] - 1 of sequence s exist, the new tokens of the
+ * call among them: the last n positions are its n new tokens, and a new token
+ * at a negative position (seq_len[s] < n, as for padding sequences with
+ * seq_len 0) has no place in the cache and sees nothing.  Values at
+ * positions that exist must be finite; what slots behind the last position
+ * hold does not matter.  Lengths and table are read on the device when the
+ * call runs, so a captured call follows them from replay to replay. */
+typedef enum {
+    QMV_KV_F16 = 1,   /* the GGUF ids of F16, I8 and BF16 */
+    QMV_KV_I8 = 24,
+    QMV_KV_BF16 = 30
+} qmv_kv_type;
+
+/* A cache.  The struct is in HOST memory and read during the call only; its
+ * pointers are device memory: pages 16-byte aligned (n_pages *
+ * qmv_kv_page_bytes() bytes), table int32[n_seq][table_ld] and seq_len
+ * int32[n_seq] 4-byte aligned.  head_dim is 64, 96, 128 or 256; page_size a
+ * power of two from 16 to 4096; table_ld * page_size <= 2^30;
+ * n_seq, n_kv_heads <= 65535. */
+typedef struct {
+    int32_t type;         /* qmv_kv_type */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int64_t n_pages;
+    void *pages;
+    const int32_t *table;
+    int64_t table_ld;     /* table entries per sequence */
+    const int32_t *seq_len;
+    int64_t n_seq;
+} qmv_kv_cache;
+
+/* Most rows (new tokens of all sequences) in one call.  qmv_attn_prefill takes
+ * at most 65535 tiles of 128 rows x (n_heads / n_kv_heads), one more for each
+ * sequence included. */
+#define QMV_MAX_KV_ROWS (1 << 27)
+
+/* Bytes of one page; 0 if an argument is out of range. */
+size_t qmv_kv_page_bytes(int32_t type, int32_t n_kv_heads, int32_t head_dim, int32_t page_size);
+
+/* ---- append new tokens' K and V to the cache -------------------------------
+ * k, v: f32, row r at k + r * ldk (v + r * ldv), n_kv_heads * head_dim values
+ * (ldk, ldv >= that: K and V may be column ranges of a stacked QKV product).
+ * n rows in all, n <= QMV_MAX_KV_ROWS.  start: device int32[n_seq + 1], not
+ * decreasing: rows start[s] .. start[s + 1] - 1 are sequence s's new tokens
+ * (rows outside start[0] .. start[n_seq] - 1 are left out); NULL: n / n_seq
+ * rows each (n a multiple of n_seq).  The j-th of a sequence's m new rows
+ * goes to position seq_len[s] - m + j.  One launch. */
+qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *start,
+                         const float *k, int64_t ldk, const float *v, int64_t ldv,
+                         hipStream_t stream);
+
+/* Most new tokens per sequence in one qmv_attn_decode call. */
+#define QMV_MAX_ATTN_N 16
+
+/* ---- attention of each sequence's last n tokens over its cache -------------
+ * The decode step (n = 1) and the check of drafted tokens (n <=
+ * QMV_MAX_ATTN_N).  For row r = s * n + j, whose position is p = seq_len[s] -
+ * n + j, and query head i (key-value head i / (n_heads / n_kv_heads)):
+ *   out[r][i] = sum_t w_t V_t,  w = softmax over the visible t of
+ *               scale * <q[r][i], K_t>
+ * t is visible if t <= p and, with window > 0, t > p - window or t < sinks
+ * (a sliding window and the first `sinks` positions); window 0: no window.
+ * A row that sees nothing gives zeros.
+ * q: f32, row r at q + r * ldq, n_heads * head_dim values.  out: f32
+ * [n_seq * n][n_heads * head_dim].  n_heads a multiple of n_kv_heads.
+ * max_len: the longest seq_len of the call (longer ones are taken as max_len,
+ * or as what a table row addresses); it sizes the workspace and decides into
+ * how many pieces the length is split.  With acc, n_seq * n * n_heads < 2^24.
+ * acc: NULL, or f32 [n_seq][n_kv_heads][ld_acc], ld_acc >= max_len: position
+ * t of key-value head h gets, added, the weights w_t of the n tokens and of the
+ * query heads that share h (what qmv_kv_evict ranks by).
+ * f32 throughout: queries and weights enter the matrix cores as exact sums of
+ * 16-bit pieces (f16 hi + lo, bf16 in three), maximum, sum and output are
+ * f32.  Results do not depend on anything but the arguments.
+ * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is
+ * 0), 16-byte aligned, no initial contents needed.  One launch, a second one
+ * to join the pieces when the length is split, a third for acc. */
+qmv_status qmv_attn_decode(const qmv_kv_cache *cache, int32_t n, int32_t n_heads, const float *q,
+                           int64_t ldq, float scale, int32_t window, int32_t sinks, float *out,
+                           int64_t max_len, float *acc, int64_t ld_acc, void *workspace,
+                           size_t ws_bytes, hipStream_t stream);
+/* 0 also where an argument is out of range.  with_acc: acc is not NULL. */
+size_t qmv_attn_decode_workspace(const qmv_kv_cache *cache, int32_t n, int32_t n_heads,
+                                 int64_t max_len, int32_t window, int32_t sinks, int32_t with_acc);
+
+/* ---- causal attention of prompts over the cache -----------------------------
+ * The same definition for any number of new tokens per sequence, whole
+ * prompts or later parts of them: n rows in all, divided by `start` as in
+ * qmv_kv_append (rows of no sequence leave out as it was).  The keys and
+ * values of the new tokens have to be in the cache already.  out: f32
+ * [n][n_heads * head_dim].  workspace: >= qmv_attn_prefill_workspace() bytes
+ * (NULL when that is 0; only few rows over a long cache need one). */
+qmv_status qmv_attn_prefill(const qmv_kv_cache *cache, int64_t n, const int32_t *start,
+                            int32_t n_heads, const float *q, int64_t ldq, float scale,
+                            int32_t window, int32_t sinks, float *out, int64_t max_len,
+                            void *workspace, size_t ws_bytes, hipStream_t stream);
+size_t qmv_attn_prefill_workspace(const qmv_kv_cache *cache, int64_t n, int32_t n_heads,
+                                  int64_t max_len, int32_t window, int32_t sinks);
+
+/* ---- evict from the cache by accumulated attention weight --------------------
+ * Cuts every sequence to its `keep` most useful positions, for each key-value
+ * head by itself: the first `first` and the last `recent` positions stay, and
+ * of those between the ones with the largest acc (equal ones: the lowest
+ * positions; a NaN ranks above everything).  first + recent <= keep.  The
+ * kept rows go, in their old order, to positions 0, 1, ... of the pages of
+ * dst_table (int32 [n_seq][dst_ld], device; same pool, keep <= dst_ld *
+ * page_size), which must share no page with the live ones; a hole there
+ * drops what would go to it, and a row kept from a hole becomes zeros.  A
+ * sequence with seq_len <= keep is copied whole.  Afterwards the caller makes
+ * dst_table the cache's table.
+ * acc: f32 [n_seq][n_kv_heads][ld_acc]; seq_len is taken as at most ld_acc.
+ * Outputs: kept int32 [n_seq][n_kv_heads][keep], the old positions (-1 past
+ * the new length); acc_out f32 [n_seq][n_kv_heads][ld_out], ld_out >= keep,
+ * their acc (0 past the new length, up to keep); len_out int32[n_seq],
+ * min(seq_len, keep).  Two launches, no workspace. */
+qmv_status qmv_kv_evict(const qmv_kv_cache *cache, const int32_t *dst_table, int64_t dst_ld,
+                        int32_t keep, int32_t first, int32_t recent, const float *acc,
+                        int64_t ld_acc, int32_t *kept, float *acc_out, int64_t ld_out,
+                        int32_t *len_out, hipStream_t stream);
 
 /* ---- helpers -------------------------------------------------------------- */
 /* Bytes of one row of K weights in format t; 0 if K is not a multiple of B. */

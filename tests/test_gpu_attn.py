@@ -1,0 +1,542 @@
+"""GPU parity of the paged key-value cache calls (append, decode and prompt
+attention, eviction) with the 64-bit implementation in attn_ref.py, whose
+docstring derives the bounds.  Cached bytes and kept positions have to be equal."""
+import numpy as np
+import pytest
+
+import synth
+from tests import attn_ref as ref
+from tests.gpu_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+import gguf_dequant_matvec_amd as q  # noqa: E402
+
+NAN_FILL = {"f16": 0xFF, "bf16": 0xFF, "i8": 0xFF}   # 0xFFFF is a NaN in f16, bf16 and f32
+
+
+def make_cache(t, kv, hd, page, lens, seed, extra_pages=3, cap_pages=None, spare=0):
+    """A host cache with the pages scattered over the pool, every slot NaN, then
+    positions 0 .. len - 1 of every sequence written with random rows."""
+    rng = synth.rng(seed, synth.T_X)
+    per = cap_pages or max(1, -(-max(max(lens), 1) // page))
+    n_pages = len(lens) * per + extra_pages + spare
+    ids = rng.permutation(n_pages - spare)[:len(lens) * per]
+    c = ref.Cache(t, kv, hd, page, n_pages, ids.reshape(len(lens), per), lens, fill=NAN_FILL[t])
+    for s, length in enumerate(lens):
+        if length <= 0:
+            continue
+        k = rng.standard_normal((length, kv, hd), dtype=np.float32)
+        v = rng.standard_normal((length, kv, hd), dtype=np.float32) * np.float32(0.5)
+        _fill(c, s, k, v)
+    return c, rng
+
+
+def _fill(c, s, k, v):
+    """Rows 0 .. of sequence s, page by page (the row-by-row append is slow in numpy)."""
+    length = len(k)
+    for p0 in range(0, length, c.page):
+        pg, _ = c.where(s, p0)
+        m = min(c.page, length - p0)
+        for h in range(c.kv):
+            kk, vv, sc = c.parts(pg, h)
+            for x, put in ((k, 0), (v, 1)):
+                rows = x[p0:p0 + m, h]
+                if c.t == "i8":
+                    d = (np.abs(rows).max(1) / np.float32(127)).astype(np.float32)
+                    code = np.clip(np.rint(rows / np.where(d == 0, 1, d)[:, None]), -127, 127).astype(np.int8)
+                    sc[put, :m] = d
+                else:
+                    code = rows.astype(np.float16) if c.t == "f16" else ref.round_bf16(rows)
+                if put == 0:
+                    kk[:m] = code
+                else:
+                    slots = np.arange(m)
+                    vv[slots // 16, :, slots % 16] = code
+
+
+class Dev:
+    """A host cache's copy on the device."""
+
+    def __init__(self, c):
+        self.c = c
+        self.pages, self.table, self.lens = dev(c.pool.reshape(-1)), dev(c.table), dev(c.seq_len)
+        self.h = q.KvCache(c.t, c.kv, c.hd, c.page, self.pages, self.table, self.lens)
+        assert self.h.n_pages == c.n_pages
+
+    def pool(self):
+        return host(self.pages).reshape(self.c.pool.shape)
+
+
+def workspace(nbytes):
+    return torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda") if nbytes else None
+
+
+def close(got, want, tol, what):
+    got = got.astype(np.float64)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} off; first {np.argwhere(bad)[:3].tolist()}, "
+                           f"worst {np.nanmax(np.abs(got - want) / tol):.3g} of the bound, NaN {np.isnan(got).sum()}")
+
+
+def run_decode(c, n, heads, window=0, sinks=0, max_len=None, with_acc=False, seed=5, qstd=1.5, ld_extra=0, d=None):
+    d = d or Dev(c)
+    n_seq = len(c.seq_len)
+    max_len = max_len or c.cap
+    scale = c.hd ** -0.5
+    width = heads * c.hd
+    qh = synth.normal(seed, synth.T_X, (n_seq * n, width + ld_extra), qstd)
+    qd = dev(qh)[:, ld_extra // 2:ld_extra // 2 + width] if ld_extra else dev(qh)
+    qh = qh[:, ld_extra // 2:ld_extra // 2 + width].reshape(n_seq * n, heads, c.hd)
+    out = torch.full((n_seq * n * heads * c.hd,), float("nan"), device="cuda")
+    acc0 = np.abs(synth.normal(seed + 1, synth.T_X, (n_seq, c.kv, max_len), 1.0)) if with_acc else None
+    acc = dev(acc0) if with_acc else None
+    ws = workspace(q.qmv_attn_decode_workspace(d.h, n, heads, max_len, window, sinks, with_acc))
+    q.qmv_attn_decode(d.h, n, heads, qd, scale, out, max_len, window=window, sinks=sinks, acc=acc, workspace=ws)
+    start = np.arange(n_seq + 1) * n
+    want, tol, acc1, acc_tol = ref.attention(c, start, qh, scale, max_len, window, sinks, acc0)
+    what = f"decode {c.t} hd{c.hd} page{c.page} lens{list(c.seq_len)[:4]} n{n} w{window}+{sinks}"
+    close(host(out).reshape(want.shape), want, tol, what)
+    if with_acc:
+        close(host(acc), acc1, acc_tol, what + " acc")
+        t = np.arange(max_len)
+        for s in range(n_seq):                      # positions that do not exist keep their bits
+            keep = t >= c.length(s, max_len)
+            assert np.array_equal(host(acc)[s][:, keep], acc0[s][:, keep])
+    return host(out)
+
+
+def run_prefill(c, news, heads, window=0, sinks=0, max_len=None, before=0, after=0, seed=7, use_start=True, qstd=1.5):
+    d = Dev(c)
+    max_len = max_len or c.cap
+    scale = c.hd ** -0.5
+    start = before + np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    n = int(start[-1]) + after
+    qh = synth.normal(seed, synth.T_X, (n, heads, c.hd), qstd)
+    out = torch.full((n, heads, c.hd), -77.0, device="cuda")
+    ws = workspace(q.qmv_attn_prefill_workspace(d.h, n, heads, max_len, window, sinks))
+    q.qmv_attn_prefill(d.h, n, heads, dev(qh), scale, out, max_len, start=dev(start) if use_start else None,
+                       window=window, sinks=sinks, workspace=ws)
+    want, tol, _, _ = ref.attention(c, start, qh, scale, max_len, window, sinks)
+    got = host(out)
+    none = np.isnan(want)
+    assert np.all(got[none] == -77.0), "rows of no sequence were written"
+    what = f"prefill {c.t} hd{c.hd} page{c.page} lens{list(c.seq_len)[:4]} new{list(news)[:4]} w{window}+{sinks}"
+    close(np.where(none, 0, got), np.where(none, 0, want), np.where(none, 1, tol), what)
+    return got, ws
+
+
+# ---- append -----------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,kv,page", [(64, 3, 16), (96, 1, 32), (128, 2, 64), (256, 1, 16)])
+def test_append(t, hd, kv, page):
+    lens = [1, 0, 40, 23, 100]
+    news = [1, 0, 17, 40, 3]          # the fourth has more rows than positions: its first 17 have no place
+    c, rng = make_cache(t, kv, hd, page, lens, 11)
+    if page < 64:
+        c.table[4, 98 // page] = -1   # the fifth's last rows but one fall into a hole
+    d = Dev(c)
+    before, after = 2, 5
+    start = (before + np.concatenate([[0], np.cumsum(news)])).astype(np.int32)
+    n = int(start[-1]) + after
+    w = kv * hd
+    k = rng.standard_normal((n, w + 8), dtype=np.float32) * 3
+    v = rng.standard_normal((n, 2 * w), dtype=np.float32)
+    k[before, :w] = 0                 # a zero row
+    kd, vd = dev(k)[:, :w], dev(v)[:, w:]
+    q.qmv_kv_append(d.h, n, kd, vd, start=dev(start))
+    c.append(start, np.ascontiguousarray(k[:, :w]).reshape(n, kv, hd), np.ascontiguousarray(v[:, w:]).reshape(n, kv, hd))
+    assert np.array_equal(d.pool(), c.pool)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+def test_append_even_rows(t):
+    """start = None: n / n_seq rows each; positions that wrap from page to page."""
+    kv, hd, page, lens, m = 2, 64, 16, [64, 33, 16, 200], 15
+    c, rng = make_cache(t, kv, hd, page, lens, 12)
+    d = Dev(c)
+    n = m * len(lens)
+    k, v = (rng.standard_normal((n, kv, hd), dtype=np.float32) for _ in range(2))
+    q.qmv_kv_append(d.h, n, dev(k), dev(v))
+    c.append(np.arange(len(lens) + 1) * m, k, v)
+    assert np.array_equal(d.pool(), c.pool)
+
+
+# ---- decode -----------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,heads,kv,page", [(64, 9, 3, 16), (96, 4, 2, 32), (128, 8, 2, 64), (256, 5, 1, 16),
+                                              (64, 17, 1, 128), (128, 2, 2, 16)])
+def test_decode_lengths(t, hd, heads, kv, page):
+    """From an empty sequence to several chunks, ends inside pages and chunks."""
+    lens = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 130, 257]
+    c, _ = make_cache(t, kv, hd, page, lens, 21)
+    run_decode(c, 1, heads)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("n,heads,kv,hd", [(2, 4, 2, 64), (5, 6, 2, 128), (8, 8, 2, 64), (16, 3, 1, 96), (16, 8, 1, 256),
+                                           (3, 32, 1, 64)])
+def test_decode_several_tokens(t, n, heads, kv, hd):
+    """n > 1, some sequences shorter than n: tokens without a position give zeros."""
+    c, _ = make_cache(t, kv, hd, 32, [0, 1, n - 1, n, 40, 129, 300], 22)
+    run_decode(c, n, heads, with_acc=True, ld_extra=12)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (33, 0), (100, 70), (5000, 3), (64, 1000)])
+@pytest.mark.parametrize("n", [1, 7])
+def test_decode_window(t, window, sinks, n):
+    c, _ = make_cache(t, 2, 64, 16, [1, 20, 150, 333, 600], 23)
+    run_decode(c, n, 6, window=window, sinks=sinks, with_acc=n == 7)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
+def test_decode_split(t, window, sinks):
+    """One long sequence: many pieces and their join; max_len beyond the length."""
+    c, _ = make_cache(t, 2, 128, 64, [5003], 24, cap_pages=100)
+    if window == 0:                   # a window may leave too little to split
+        assert q.qmv_attn_decode_workspace(Dev(c).h, 1, 8, c.cap) > 0
+    run_decode(c, 1, 8, window=window, sinks=sinks)
+    run_decode(c, 4, 8, window=window, sinks=sinks, with_acc=True)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+def test_decode_holes(t):
+    """Positions in holes are not seen: released pages of a window, a row whose
+    every page is a hole."""
+    c, _ = make_cache(t, 1, 64, 16, [300, 300, 40], 25)
+    c.table[0, 2:14] = -1
+    c.table[1, 5] = c.n_pages
+    c.table[1, 18] = 2 ** 31 - 1
+    c.table[2, :] = -5
+    run_decode(c, 1, 4, with_acc=True)
+    run_decode(c, 3, 4, window=70, sinks=20)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+def test_decode_large_logits(t):
+    """Logits that grow along the sequence: the running maximum moves often."""
+    c, _ = make_cache(t, 1, 64, 64, [700, 64], 26)
+    run_decode(c, 2, 4, qstd=40.0, with_acc=True)
+
+
+@pytest.mark.parametrize("t", ["f16", "i8"])
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e9, 1e30])
+def test_decode_query_range(t, size):
+    """Queries far outside f16's range (the f16 pieces are taken of scaled rows)."""
+    c, _ = make_cache(t, 1, 64, 64, [90], 27)
+    d = Dev(c)
+    qh = synth.normal(3, synth.T_X, (1, 4, 64), 1.0) * np.float32(size)
+    out = torch.empty(4 * 64, device="cuda")
+    scale = 0.2 / size
+    q.qmv_attn_decode(d.h, 1, 4, dev(qh.reshape(1, -1)), scale, out, 128)
+    want, tol, _, _ = ref.attention(c, [0, 1], qh, float(np.float32(scale)), 128)
+    close(host(out).reshape(want.shape), want, tol, f"query size {size}")
+
+
+@pytest.mark.parametrize("size", [1e-20, 1e-7, 3e4, 1e20])
+def test_decode_i8_value_range(size):
+    """8-bit V rows of any scale, and of very different scales in one sequence."""
+    c, rng = make_cache("i8", 1, 64, 16, [150], 28)
+    for p in range(150):
+        pg, slot = c.where(0, p)
+        c.parts(pg, 0)[2][1, slot] *= np.float32(size * 10.0 ** (p % 5 - 4))
+    run_decode(c, 1, 4)
+
+
+def test_decode_far_pages():
+    """Pages beyond 4 GiB of the pool."""
+    t, kv, hd, page = "f16", 2, 128, 64
+    c, _ = make_cache(t, kv, hd, page, [500], 29)
+    pb = q.qmv_kv_page_bytes(t, kv, hd, page)
+    n_pages = (9 << 30) // (2 * pb)                 # 4.5 GiB
+    pool = torch.zeros(n_pages * pb, dtype=torch.uint8, device="cuda")
+    far = np.array([[n_pages - 1 - 3 * i for i in range(c.table.shape[1])]], np.int32)
+    view = pool.view(n_pages, pb)
+    for i, pg in enumerate(c.table[0]):
+        view[int(far[0, i])] = dev(c.pool[pg].reshape(-1))
+    cache = q.KvCache(t, kv, hd, page, pool, dev(far), dev(c.seq_len))
+    qh = synth.normal(4, synth.T_X, (20, 8, hd), 1.0)
+    want, tol, _, _ = ref.attention(c, [0, 1], qh[:1], hd ** -0.5, 512)
+    out = torch.empty(20, 8, hd, device="cuda")
+    q.qmv_attn_decode(cache, 1, 8, dev(qh[:1].reshape(1, -1)), hd ** -0.5, out[:1], 512,
+                      workspace=workspace(q.qmv_attn_decode_workspace(cache, 1, 8, 512)))
+    close(host(out[:1]), want, tol, "far pages, decode")
+    want, tol, _, _ = ref.attention(c, [0, 20], qh, hd ** -0.5, 512)
+    q.qmv_attn_prefill(cache, 20, 8, dev(qh.reshape(20, -1)), hd ** -0.5, out, 512,
+                       workspace=workspace(q.qmv_attn_prefill_workspace(cache, 20, 8, 512)))
+    close(host(out), want, tol, "far pages, prefill")
+    k, v = (synth.normal(i, synth.T_X, (3, kv, hd)) for i in (5, 6))
+    q.qmv_kv_append(cache, 3, dev(k), dev(v))
+    c.append([0, 3], k, v)
+    for i, pg in enumerate(c.table[0]):
+        assert np.array_equal(host(view[int(far[0, i])]), c.pool[pg].reshape(-1))
+
+
+# ---- prefill ----------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,heads,kv,page", [(64, 9, 3, 16), (96, 4, 2, 32), (128, 8, 2, 64), (256, 5, 1, 16),
+                                              (64, 17, 1, 128)])
+def test_prefill_ragged(t, hd, heads, kv, page):
+    """Whole prompts and later parts, empty sequences, rows of no sequence."""
+    lens = [0, 1, 33, 64, 130, 200]
+    news = [0, 1, 33, 20, 130, 97]
+    c, _ = make_cache(t, kv, hd, page, lens, 31)
+    run_prefill(c, news, heads, before=3, after=4)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("n,length", [(1, 1), (16, 16), (17, 40), (150, 150), (64, 300)])
+def test_prefill_even(t, n, length):
+    c, _ = make_cache(t, 2, 64, 32, [length, max(0, length - 9), length], 32)
+    run_prefill(c, [n] * 3, 6, use_start=False)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 2), (17, 4), (64, 0), (100, 70), (250, 1000)])
+def test_prefill_window(t, window, sinks):
+    c, _ = make_cache(t, 1, 64, 16, [400, 90, 300], 33)
+    run_prefill(c, [400, 90, 40], 4, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd", [128, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (900, 5)])
+def test_prefill_split(t, hd, window, sinks):
+    """Few new rows after a long context: pieces and their join."""
+    c, _ = make_cache(t, 1, hd, 64, [3000, 2100], 34)
+    _, ws = run_prefill(c, [40, 19], 3, window=window, sinks=sinks, before=1, after=2)
+    assert ws is not None or window > 0
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+def test_prefill_holes_and_large_logits(t):
+    c, _ = make_cache(t, 1, 64, 16, [300, 40], 35)
+    c.table[0, 2:14] = -1
+    c.table[0, 17] = c.n_pages
+    c.table[1, :] = -5
+    run_prefill(c, [60, 40], 4)
+    run_prefill(c, [60, 40], 4, window=90, sinks=20, qstd=40.0)
+
+
+def test_prefill_matches_decode():
+    """Both calls compute the same rows (n <= 16), each within its bound."""
+    c, _ = make_cache("f16", 2, 128, 64, [700, 16, 31], 36)
+    a = run_decode(c, 16, 8, seed=9).reshape(48, 8, 128)
+    b, _ = run_prefill(c, [16] * 3, 8, seed=9, use_start=False)
+    assert np.max(np.abs(a - b)) < 1e-4
+
+
+# ---- eviction ----------------------------------------------------------------
+
+def run_evict(c, keep, first, recent, acc, dst=None):
+    n_seq = len(c.seq_len)
+    per = -(-keep // c.page)
+    if dst is None:
+        dst = np.arange(c.n_pages - n_seq * per, c.n_pages, dtype=np.int32)[::-1].reshape(n_seq, per)
+    d = Dev(c)
+    kept = torch.full((n_seq, c.kv, keep), -9, dtype=torch.int32, device="cuda")
+    out = torch.full((n_seq, c.kv, keep + 5), -9.0, device="cuda")
+    lens = torch.full((n_seq,), -9, dtype=torch.int32, device="cuda")
+    q.qmv_kv_evict(d.h, dev(dst), keep, first, recent, dev(acc), kept, out, lens)
+    k, a, n = ref.evict(c, dst, keep, first, recent, acc)
+    assert np.array_equal(host(kept), k)
+    assert np.array_equal(host(out)[..., :keep].view(np.uint32), a.view(np.uint32))
+    assert np.all(host(out)[..., keep:] == -9.0)
+    assert np.array_equal(host(lens), n)
+    assert np.array_equal(d.pool(), c.pool)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,kv,page", [(64, 3, 16), (96, 1, 32), (128, 2, 64), (256, 1, 16)])
+@pytest.mark.parametrize("keep,first,recent", [(1, 0, 0), (33, 4, 20), (64, 0, 64), (100, 4, 17), (100, 100, 0)])
+def test_evict(t, hd, kv, page, keep, first, recent):
+    lens = [0, 1, 63, 100, 101, 300]
+    c, rng = make_cache(t, kv, hd, page, lens, 41, spare=len(lens) * -(-keep // page))
+    run_evict(c, keep, first, recent, rng.random((len(lens), kv, 310), dtype=np.float32) ** 2)
+
+
+@pytest.mark.parametrize("case", ["equal", "two", "signs", "special", "tiny"])
+def test_evict_scores(case):
+    """Equal scores, few distinct ones, negative ones and zeros of both signs,
+    infinities and NaN, differences in the last bit."""
+    n, kv = 2500, 2
+    c, rng = make_cache("f16", kv, 64, 64, [n], 42, spare=20)
+    x = {"equal": np.ones((1, kv, n)), "two": rng.integers(0, 2, (1, kv, n)),
+         "signs": rng.integers(-2, 3, (1, kv, n)) * rng.choice([1.0, 0.0, -0.0], (1, kv, n)),
+         "special": rng.choice([np.inf, -np.inf, np.nan, 0.5, 1e-40], (1, kv, n)),
+         "tiny": np.float32(1) + rng.integers(0, 40, (1, kv, n)).astype(np.float32) * np.float32(2.0 ** -23)}[case]
+    run_evict(c, 1203, 4, 100, x.astype(np.float32))
+
+
+def test_evict_holes():
+    """A destination hole drops its rows, a source hole gives zeros."""
+    c, rng = make_cache("i8", 2, 64, 16, [200, 90], 43, spare=20)
+    c.table[0, 3] = -1
+    c.table[1, 0] = c.n_pages + 7
+    per = 5
+    dst = np.arange(c.n_pages - 2 * per, c.n_pages, dtype=np.int32).reshape(2, per)
+    dst[0, 2] = -1
+    dst[1, 4] = c.n_pages
+    run_evict(c, 70, 4, 10, rng.random((2, 2, 200), dtype=np.float32), dst)
+
+
+# ---- together -----------------------------------------------------------------
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+def test_prompt_decode_evict_decode(t):
+    """As a program uses them: prompts appended and attended, tokens decoded one
+    by one with their weights collected, drafted tokens checked, the cache cut,
+    decoding again from the cut cache."""
+    kv, heads, hd, page, prompts = 2, 6, 64, 16, [50, 7, 33]
+    n_seq, per, keep = 3, 8, 40
+    rng = synth.rng(51, synth.T_X)
+    n_pages = 2 * n_seq * per
+    ids = rng.permutation(n_pages).astype(np.int32)
+    c = ref.Cache(t, kv, hd, page, n_pages, ids[:n_seq * per].reshape(n_seq, per), prompts, fill=0xFF)
+    d = Dev(c)
+    acc_ref = np.zeros((n_seq, kv, c.cap), np.float32)
+    acc = dev(acc_ref)
+    scale, max_len = hd ** -0.5, c.cap
+    ws = workspace(max(q.qmv_attn_decode_workspace(d.h, n, heads, max_len, 0, 0, True) for n in (1, 4)))
+
+    def qkv(n):
+        x = rng.standard_normal((n, (heads + 2 * kv) * hd), dtype=np.float32)
+        xd = dev(x)
+        a, b = heads * hd, (heads + kv) * hd
+        return (x[:, :a].reshape(n, heads, hd), x[:, a:b].reshape(n, kv, hd), x[:, b:].reshape(n, kv, hd),
+                xd[:, :a], xd[:, a:b], xd[:, b:])
+
+    # prompts
+    start = np.concatenate([[0], np.cumsum(prompts)]).astype(np.int32)
+    n = int(start[-1])
+    qh, kh, vh, qd, kd, vd = qkv(n)
+    sd = dev(start)
+    q.qmv_kv_append(d.h, n, kd, vd, start=sd)
+    c.append(start, kh, vh)
+    out = torch.empty(n, heads * hd, device="cuda")
+    assert q.qmv_attn_prefill_workspace(d.h, n, heads, max_len) == 0
+    q.qmv_attn_prefill(d.h, n, heads, qd, scale, out, max_len, start=sd)
+    want, tol, _, _ = ref.attention(c, start, qh, scale, max_len)
+    close(host(out).reshape(want.shape), want, tol, "prompt")
+
+    def step(n, what):
+        nonlocal acc_ref
+        c.seq_len += n
+        d.lens.add_(n)
+        rows = n_seq * n
+        qh, kh, vh, qd, kd, vd = qkv(rows)
+        q.qmv_kv_append(d.h, rows, kd, vd)
+        st = np.arange(n_seq + 1) * n
+        c.append(st, kh, vh)
+        out = torch.empty(rows, heads * hd, device="cuda")
+        q.qmv_attn_decode(d.h, n, heads, qd, scale, out, max_len, acc=acc, workspace=ws)
+        want, tol, a1, at = ref.attention(c, st, qh, scale, max_len, acc=acc_ref)
+        close(host(out).reshape(want.shape), want, tol, what)
+        close(host(acc), a1, at, what + " acc")
+        acc_ref = host(acc).copy()
+
+    for i in range(5):
+        step(1, f"step {i}")
+    step(4, "draft")
+    assert np.array_equal(d.pool(), c.pool)
+
+    # cut to `keep` positions and go on
+    dst = np.full((n_seq, per), -1, np.int32)
+    dst[:] = ids[n_seq * per:].reshape(n_seq, per)
+    kept = torch.empty(n_seq, kv, keep, dtype=torch.int32, device="cuda")
+    acc2 = torch.zeros(n_seq, kv, max_len, device="cuda")
+    lens2 = torch.empty(n_seq, dtype=torch.int32, device="cuda")
+    q.qmv_kv_evict(d.h, dev(dst), keep, 4, 16, acc, kept, acc2, lens2)
+    k, a, n2 = ref.evict(c, dst, keep, 4, 16, acc_ref)
+    assert np.array_equal(host(kept), k) and np.array_equal(host(lens2), n2)
+    d.table.copy_(dev(dst))
+    d.lens.copy_(lens2)
+    acc.copy_(acc2)
+    c.table, c.seq_len = dst, n2
+    acc_ref = np.zeros_like(acc_ref)
+    acc_ref[..., :keep] = a
+    for i in range(3):
+        step(1, f"step {i} after the cut")
+    assert np.array_equal(d.pool(), c.pool)
+
+
+@pytest.mark.parametrize("window", [0, 90])
+def test_graph_replay_follows_lengths(window):
+    """Append and decode captured once; every replay follows the lengths and the
+    inputs in place, with eager work between replays, and equals the eager call
+    bit for bit."""
+    kv, heads, hd, page = 2, 8, 128, 64
+    c, rng = make_cache("f16", kv, hd, page, [900, 130], 61, cap_pages=20)
+    d = Dev(c)
+    max_len = c.cap
+    acc = torch.zeros(2, kv, max_len, device="cuda")
+    qd, kd, vd = (torch.zeros(2, w, device="cuda") for w in (heads * hd, kv * hd, kv * hd))
+    out = torch.empty(2, heads * hd, device="cuda")
+    ws = workspace(q.qmv_attn_decode_workspace(d.h, 1, heads, max_len, window, 4, True))
+
+    def fn():
+        q.qmv_kv_append(d.h, 2, kd, vd)
+        q.qmv_attn_decode(d.h, 1, heads, qd, hd ** -0.5, out, max_len, window=window, sinks=4, acc=acc, workspace=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fn()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fn()
+    for rep in range(4):
+        for x, w in ((qd, 1.5), (kd, 1.0), (vd, 1.0)):
+            x.copy_(dev(rng.standard_normal(x.shape, dtype=np.float32) * np.float32(w)))
+        d.lens.add_(1)
+        acc.zero_()
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        got, got_acc, pool = host(out).copy(), host(acc).copy(), d.pool().copy()
+        acc.zero_()
+        fn()                                         # the same again, eagerly
+        torch.cuda.synchronize()
+        assert np.array_equal(got, host(out)) and np.array_equal(got_acc, host(acc)), rep
+        assert np.array_equal(pool, d.pool())
+        assert np.isfinite(got).all()
+
+
+def test_other_stream():
+    """On a stream of its own, ordered by the caller; two streams at once with a
+    workspace each."""
+    c, _ = make_cache("f16", 2, 64, 64, [2000], 62)
+    d = Dev(c)
+    qd = dev(synth.normal(1, synth.T_X, (1, 8 * 64)))
+    need = q.qmv_attn_decode_workspace(d.h, 1, 8, c.cap)
+    base = torch.empty(1, 8 * 64, device="cuda")
+    q.qmv_attn_decode(d.h, 1, 8, qd, 0.125, base, c.cap, workspace=workspace(need))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros(1, 8 * 64, device="cuda") for _ in streams]
+    wss = [workspace(need) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o, w in zip(streams, outs, wss):
+            q.qmv_attn_decode(d.h, 1, 8, qd, 0.125, o, c.cap, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, base)
+
+
+def test_results_repeat():
+    """The same call twice gives the same bits (no order-dependent sums)."""
+    c, _ = make_cache("bf16", 2, 64, 32, [3000, 411], 63)
+    a = run_decode(c, 5, 8, with_acc=True)
+    assert np.array_equal(a, run_decode(c, 5, 8, with_acc=True))
