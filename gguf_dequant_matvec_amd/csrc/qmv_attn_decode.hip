@@ -37,27 +37,21 @@ __device__ __forceinline__ constexpr int col_of(int t, int g) {
     return TYPE == kKvI8 && HD % 64 == 0 ? 64 * (t / 2) + 16 * g + 8 * (t % 2) : 32 * t + 8 * g;
 }
 
+// K rows of a chunk in registers: rows + 4 r of a lane's positions, r = 2 u + b
+// for tile b of sub-chunk u.
 template <int TYPE, int HD>
-struct Tile {  // one chunk in registers
-    static constexpr int SUB = kChunk<TYPE> / 32;       // sub-chunks of 32 positions
-    static constexpr int KW = TYPE == kKvI8 ? HD / 8 : HD / 8 * 2;  // dwords: 2 * SUB rows of HD / 4 columns
-    static constexpr int VW = HD / 16 * 4;              // dwords: HD / 16 columns of 16 bytes
-    uint32_t k[2 * SUB][KW / 2];
-    uint32_t v[VW];
-    float ks[TYPE == kKvI8 ? 16 : 1], vs[TYPE == kKvI8 ? 16 : 1];
-    bool ok;  // the lane group's positions are in a page (not a hole)
+struct KTile {
+    static constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
+    static constexpr int R = kChunk<TYPE> / 16;
+    static constexpr int W = HD * SZ / 16;  // dwords of a lane's quarter row
+    uint32_t k[R][W];
 
-    __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int kpage, int vpage,
-                                         int g, int m) {
-        constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
-        constexpr int PER = kChunk<TYPE> / 4;  // positions of a lane group
-        const int pmask = (1 << c.page_shift) - 1;
-        const int kslot = (chunk * kChunk<TYPE> + PER * (m >> 2)) & pmask;
-        const int vslot = (chunk * kChunk<TYPE> + PER * g) & pmask;
-        ok = vpage >= 0;
-        const uint8_t *kp = kv_head(c, kpage < 0 ? 0 : kpage, h) + (int64_t)(kslot + (m & 3)) * (HD * SZ);
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
+        const int pos = chunk * kChunk<TYPE> + kChunk<TYPE> / 4 * (m >> 2);
+        const int slot = (pos & ((1 << c.page_shift) - 1)) + (m & 3);
+        const uint8_t *kp = kv_head(c, page < 0 ? 0 : page, h) + (int64_t)slot * (HD * SZ);
 #pragma unroll
-        for (int r = 0; r < 2 * SUB; r++) {  // rows + 4 r: tile b = r % 2 of sub-chunk r / 2
+        for (int r = 0; r < R; r++) {
             const uint8_t *row = kp + r * 4 * HD * SZ;
             if constexpr (TYPE == kKvI8 && HD % 64 != 0) {
 #pragma unroll
@@ -73,15 +67,40 @@ struct Tile {  // one chunk in registers
                 }
             }
         }
-        const uint8_t *vhead = kv_head(c, vpage < 0 ? 0 : vpage, h) + ((int64_t)HD * SZ << c.page_shift);
-        const uint8_t *vp = vhead + (int64_t)(vslot / kVBlock) * (HD * kVBlock * SZ) + m * (kVBlock * SZ) + (vslot % kVBlock) * SZ;
+    }
+    template <class Vec>
+    __device__ __forceinline__ Vec op(int u, int b, int t) const {
+        const uint32_t *r = k[2 * u + b];
+        if constexpr (TYPE == kKvI8) {
+            const uint2 x = codes_to_f16(r[2 * t]), y = codes_to_f16(r[2 * t + 1]);
+            return as_vec<Vec>(U128{{x.x, x.y, y.x, y.y}});
+        } else {
+            return as_vec<Vec>(U128{{r[4 * t], r[4 * t + 1], r[4 * t + 2], r[4 * t + 3]}});
+        }
+    }
+};
+
+// V columns of a chunk in registers (8 or 16 positions of a lane group in 16
+// bytes), and the row scales of an 8-bit cache at those positions.
+template <int TYPE, int HD>
+struct VTile {
+    static constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
+    static constexpr int DT = HD / 16;
+    uint32_t v[DT][4];
+    float ks[TYPE == kKvI8 ? 16 : 1], vs[TYPE == kKvI8 ? 16 : 1];
+
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
+        const int pmask = (1 << c.page_shift) - 1;
+        const int slot = (chunk * kChunk<TYPE> + kChunk<TYPE> / 4 * g) & pmask;
+        const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h) + ((int64_t)(HD * SZ) << c.page_shift);
+        const uint8_t *vp = head + (int64_t)(slot / kVBlock) * (HD * kVBlock * SZ) + (m * kVBlock + slot % kVBlock) * SZ;
 #pragma unroll
-        for (int t = 0; t < HD / 16; t++) {
+        for (int t = 0; t < DT; t++) {
             const uint4 w = *reinterpret_cast<const uint4 *>(vp + t * 16 * kVBlock * SZ);
-            v[4 * t] = w.x, v[4 * t + 1] = w.y, v[4 * t + 2] = w.z, v[4 * t + 3] = w.w;
+            v[t][0] = w.x, v[t][1] = w.y, v[t][2] = w.z, v[t][3] = w.w;
         }
         if constexpr (TYPE == kKvI8) {
-            const float *sc = reinterpret_cast<const float *>(vhead + ((int64_t)HD << c.page_shift)) + vslot;
+            const float *sc = reinterpret_cast<const float *>(head + ((int64_t)HD << c.page_shift)) + slot;
 #pragma unroll
             for (int j = 0; j < 16; j++) ks[j] = sc[j];
             sc += pmask + 1;
@@ -89,29 +108,14 @@ struct Tile {  // one chunk in registers
             for (int j = 0; j < 16; j++) vs[j] = sc[j];
         }
     }
-    // operand of K: tile b of sub-chunk u, step t
     template <class Vec>
-    __device__ __forceinline__ Vec kop(int u, int b, int t) const {
-        U128 o;
-        const uint32_t *r = k[2 * u + b];
+    __device__ __forceinline__ Vec op(int u, int t) const {
         if constexpr (TYPE == kKvI8) {
-            const uint2 x = codes_to_f16(r[2 * t]), y = codes_to_f16(r[2 * t + 1]);
-            o = U128{{x.x, x.y, y.x, y.y}};
+            const uint2 x = codes_to_f16(v[t][2 * u]), y = codes_to_f16(v[t][2 * u + 1]);
+            return as_vec<Vec>(U128{{x.x, x.y, y.x, y.y}});
         } else {
-            o = U128{{r[4 * t], r[4 * t + 1], r[4 * t + 2], r[4 * t + 3]}};
+            return as_vec<Vec>(U128{{v[t][0], v[t][1], v[t][2], v[t][3]}});
         }
-        return as_vec<Vec>(o);
-    }
-    template <class Vec>
-    __device__ __forceinline__ Vec vop(int u, int t) const {
-        U128 o;
-        if constexpr (TYPE == kKvI8) {
-            const uint2 x = codes_to_f16(v[4 * t + 2 * u]), y = codes_to_f16(v[4 * t + 2 * u + 1]);
-            o = U128{{x.x, x.y, y.x, y.y}};
-        } else {
-            o = U128{{v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]}};
-        }
-        return as_vec<Vec>(o);
     }
 };
 
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
     typedef typename Op::Vec Vec;
     constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
     constexpr int KS = HD / 32, DT = HD / 16;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, m = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, g = lane >> 4;
     const int split = blockIdx.x, s = blockIdx.z;
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
     const KvArgs &c = a.c;
@@ -130,54 +134,20 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
     const int nrows = n * a.group;
     const int r0 = tile * 16 * RT;
 
-    // the rows of this tile and what they see
-    int pos[RT];
-    float qscale[RT];
-    U128 qf[RT][KS][NP];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        const int rr = r0 + rt * 16 + m;
-        const bool live = rr < nrows;
-        const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
-        pos[rt] = live ? len - n + j : -1;
-        const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
-        float f[KS][8];
-        float big = 0.f;
-#pragma unroll
-        for (int t = 0; t < KS; t++) {
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
-            const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
-            const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                f[t][e] = live ? w[e] : 0.f;
-                big = fmaxf(big, fabsf(f[t][e]));
-            }
-        }
-        // f16 pieces: scale the row by a power of two so that its largest
-        // value is in [2^14, 2^15)
-        int sh = 0;
-        if constexpr (TYPE != kKvBF16) {
-            big = fmaxf(big, __shfl_xor(big, 16));
-            big = fmaxf(big, __shfl_xor(big, 32));
-            if (big > 0.f && big < __builtin_inff()) {
-                sh = 15 - __builtin_amdgcn_frexp_expf(big);
-                sh = sh > 100 ? 100 : sh;
-            }
-        }
-        qscale[rt] = ldexpf(a.scale_log2, -sh);
-#pragma unroll
-        for (int t = 0; t < KS; t++) {
-#pragma unroll
-            for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
-            split8<Op>(f[t], qf[rt][t]);
-        }
-    }
+    // what the rows of this tile see, and the first chunk on its way
     const int last = r0 + 16 * RT < nrows ? r0 + 16 * RT - 1 : nrows - 1;
     const int pmin = len - n + r0 / a.group, pmax = len - n + last / a.group;
     const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, CK);
     const int begin = (int)((int64_t)ch.n * split / a.splits), end = (int)((int64_t)ch.n * (split + 1) / a.splits);
-
+    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
+    const int32_t *table = c.table + (int64_t)s * c.table_ld;
+    auto page_of = [&](int i, int grp) {  // page of a lane group's positions in chunk number i
+        if (i >= end) return -1;
+        const int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
+        if (pi > last_page) return -1;
+        const int pg = table[pi];
+        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
+    };
     float mrun[RT], lrun[RT];
     f32x4 o[RT][DT];
     float vmul = kVmulNone;  // 8-bit: power of two that brings the row scales of V to at most 1
@@ -189,91 +159,146 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
         for (int t = 0; t < DT; t++) o[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
-    auto page_of = [&](int i, int grp) {  // page of a lane group's positions in chunk number i
-        int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
-        if (pi > last_page) return -1;
-        const int pg = c.table[(int64_t)s * c.table_ld + pi];
-        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
-    };
-    for (int i = begin + wave; i < end; i += kWaves) {
-        Tile<TYPE, HD> kv;
-        kv.load(c, h, ch.at(i), page_of(i, m >> 2), page_of(i, g), g, m);
-        const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
-        // a chunk that every row sees whole needs no masks
-        const int c0 = ch.at(i) * CK, c1 = c0 + CK - 1;
-        const bool whole = c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks) && __all(kv.ok);
-        if constexpr (TYPE == kKvI8) {
+    if (begin + wave < end) {
+        int i = begin + wave;
+        int kpage = page_of(i, m >> 2), vpage = page_of(i, g);
+        KTile<TYPE, HD> kt;
+        VTile<TYPE, HD> vt;
+        bool ok = vpage >= 0;  // the lane group's positions are in a page (not a hole)
+        kt.load(c, h, ch.at(i), kpage, g, m);
+        vt.load(c, h, ch.at(i), vpage, g, m);
+        kpage = page_of(i + kWaves, m >> 2);
+        vpage = page_of(i + kWaves, g);
+
+        // the rows
+        int pos[RT];
+        float qscale[RT];
+        U128 qf[RT][KS][NP];
+    #pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            const int rr = r0 + rt * 16 + m;
+            const bool live = rr < nrows;
+            const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
+            pos[rt] = live ? len - n + j : -1;
+            const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
+            float f[KS][8];
             float big = 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-                if (!whole) {
-                    const bool any = kv.ok && key0 + e <= pmax && (a.window <= 0 || key0 + e > pmin - a.window || key0 + e < a.sinks);
-                    kv.vs[e] = any ? kv.vs[e] : 0.f;
+    #pragma unroll
+            for (int t = 0; t < KS; t++) {
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
+                const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+                const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    #pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    f[t][e] = live ? w[e] : 0.f;
+                    big = fmaxf(big, fabsf(f[t][e]));
                 }
-                big = fmaxf(big, fabsf(kv.vs[e]));
             }
-            if (__any(big * vmul > 1.f && big < __builtin_inff())) {
-                for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
-                int ex = __builtin_amdgcn_frexp_expf(big);
-                ex = ex > 120 ? 120 : ex;
-                const float nm = ldexpf(1.f, -ex);
-                const float r = nm / vmul;
-                vmul = nm;
-#pragma unroll
-                for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                    for (int t = 0; t < DT; t++) o[rt][t] *= r;
-            }
-        } else if (!whole) {
-            // V of positions no row sees: zero, whatever the page holds there
-#pragma unroll
-            for (int w = 0; w < 4; w++) {
-                uint32_t keep = 0;
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int key = key0 + 2 * w + e;
-                    if (kv.ok && key <= pmax && (a.window <= 0 || key > pmin - a.window || key < a.sinks)) keep |= 0xFFFFu << (16 * e);
+            // f16 pieces: scale the row by a power of two so that its largest
+            // value is in [2^14, 2^15)
+            int sh = 0;
+            if constexpr (TYPE != kKvBF16) {
+                big = fmaxf(big, __shfl_xor(big, 16));
+                big = fmaxf(big, __shfl_xor(big, 32));
+                if (big > 0.f && big < __builtin_inff()) {
+                    sh = 15 - __builtin_amdgcn_frexp_expf(big);
+                    sh = sh > 100 ? 100 : sh;
                 }
-#pragma unroll
-                for (int t = 0; t < DT; t++) kv.v[4 * t + w] &= keep;
+            }
+            qscale[rt] = ldexpf(a.scale_log2, -sh);
+    #pragma unroll
+            for (int t = 0; t < KS; t++) {
+    #pragma unroll
+                for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
+                split8<Op>(f[t], qf[rt][t]);
             }
         }
-#pragma unroll
-        for (int u = 0; u < SUB; u++) {
-            f32x4 sacc[RT][2];
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++) sacc[rt][0] = sacc[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+
+        for (;;) {
+            const bool more = i + kWaves < end;
+            const int kpage2 = page_of(i + 2 * kWaves, m >> 2), vpage2 = page_of(i + 2 * kWaves, g);
+            f32x4 sacc[RT][2 * SUB];
+    #pragma unroll
+            for (int rt = 0; rt < RT; rt++)
+    #pragma unroll
+                for (int ub = 0; ub < 2 * SUB; ub++) sacc[rt][ub] = f32x4{0.f, 0.f, 0.f, 0.f};
+    #pragma unroll
             for (int t = 0; t < KS; t++) {
-#pragma unroll
-                for (int b = 0; b < 2; b++) {
-                    const Vec kx = kv.template kop<Vec>(u, b, t);
-#pragma unroll
+    #pragma unroll
+                for (int ub = 0; ub < 2 * SUB; ub++) {
+                    const Vec kx = kt.template op<Vec>(ub >> 1, ub & 1, t);
+    #pragma unroll
                     for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                        for (int p = 0; p < NP; p++) sacc[rt][b] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][b]);
+    #pragma unroll
+                        for (int p = 0; p < NP; p++) sacc[rt][ub] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][ub]);
                 }
             }
-            U128 pf[RT][NP];
-#pragma unroll
+            // the K registers are free: the next chunk's K flies during the
+            // softmax and the second product, its V during the next first one
+            if (more) kt.load(c, h, ch.at(i + kWaves), kpage, g, m);
+
+            const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
+            // a chunk that every row sees whole needs no masks
+            const int c0 = ch.at(i) * CK, c1 = c0 + CK - 1;
+            const bool whole = c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks) && __all(ok);
+            if constexpr (TYPE == kKvI8) {
+                float big = 0.f;
+    #pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    if (!whole) {
+                        const bool any = ok && key0 + e <= pmax && (a.window <= 0 || key0 + e > pmin - a.window || key0 + e < a.sinks);
+                        vt.vs[e] = any ? vt.vs[e] : 0.f;
+                    }
+                    big = fmaxf(big, fabsf(vt.vs[e]));
+                }
+                if (__any(big * vmul > 1.f && big < __builtin_inff())) {
+                    for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
+                    int ex = __builtin_amdgcn_frexp_expf(big);
+                    ex = ex > 120 ? 120 : ex;
+                    const float nm = ldexpf(1.f, -ex);
+                    const float r = nm / vmul;
+                    vmul = nm;
+    #pragma unroll
+                    for (int rt = 0; rt < RT; rt++)
+    #pragma unroll
+                        for (int t = 0; t < DT; t++) o[rt][t] *= r;
+                }
+            } else if (!whole) {
+                // V of positions no row sees: zero, whatever the page holds there
+    #pragma unroll
+                for (int w = 0; w < 4; w++) {
+                    uint32_t keep = 0;
+    #pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int key = key0 + 2 * w + e;
+                        if (ok && key <= pmax && (a.window <= 0 || key > pmin - a.window || key < a.sinks)) keep |= 0xFFFFu << (16 * e);
+                    }
+    #pragma unroll
+                    for (int t = 0; t < DT; t++) vt.v[t][w] &= keep;
+                }
+            }
+            U128 pf[RT][SUB][NP];
+    #pragma unroll
             for (int rt = 0; rt < RT; rt++) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
+                float x[PER];
+    #pragma unroll
+                for (int e = 0; e < PER; e++) {
                     x[e] = sacc[rt][e >> 2][e & 3] * qscale[rt];
-                    if constexpr (TYPE == kKvI8) x[e] *= kv.ks[8 * u + e];
-                    if (!whole) x[e] = kv.ok && sees(pos[rt], key0 + 8 * u + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                    if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
+                    if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
                 }
                 if constexpr (ACC) {
                     const int rr = r0 + rt * 16 + m;
                     if (rr < nrows) {
-                        float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0 + 8 * u;
-                        *reinterpret_cast<float4 *>(lp) = make_float4(x[0], x[1], x[2], x[3]);
-                        *reinterpret_cast<float4 *>(lp + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                        float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0;
+    #pragma unroll
+                        for (int e = 0; e < PER; e += 4)
+                            *reinterpret_cast<float4 *>(lp + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
                     }
                 }
-                float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                float mx = x[0];
+    #pragma unroll
+                for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
                 if (__any(mx > mrun[rt] + kSlack)) {
                     mx = fmaxf(mx, __shfl_xor(mx, 16));
                     mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -281,28 +306,38 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                     const float r = exp2_fast(mrun[rt] - mnew);
                     mrun[rt] = mnew;
                     lrun[rt] *= r;
-#pragma unroll
+    #pragma unroll
                     for (int t = 0; t < DT; t++) o[rt][t] *= r;
                 }
                 const float off = kBias - mrun[rt];
                 float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
+    #pragma unroll
+                for (int e = 0; e < PER; e++) {
                     x[e] = exp2_fast(x[e] + off);
                     sum += x[e];
-                    if constexpr (TYPE == kKvI8) x[e] *= kv.vs[8 * u + e] * vmul;
+                    if constexpr (TYPE == kKvI8) x[e] *= vt.vs[e] * vmul;
                 }
                 lrun[rt] += sum;
-                split8<Op>(x, pf[rt]);
+    #pragma unroll
+                for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
             }
-#pragma unroll
-            for (int t = 0; t < DT; t++) {
-                const Vec vx = kv.template vop<Vec>(u, t);
-#pragma unroll
-                for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                    for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][p]), o[rt][t]);
+    #pragma unroll
+            for (int u = 0; u < SUB; u++) {
+    #pragma unroll
+                for (int t = 0; t < DT; t++) {
+                    const Vec vx = vt.template op<Vec>(u, t);
+    #pragma unroll
+                    for (int rt = 0; rt < RT; rt++)
+    #pragma unroll
+                        for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
+                }
             }
+            if (more) vt.load(c, h, ch.at(i + kWaves), vpage, g, m);
+            if (!more) break;
+            i += kWaves;
+            ok = vpage >= 0;
+            kpage = kpage2;
+            vpage = vpage2;
         }
     }
 

@@ -41,7 +41,7 @@ struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
     static constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
     static constexpr int PIECES = HD * SZ;  // 16-byte pieces of 16 K rows, and of a V block
     static constexpr int N = (PIECES + 63) / 64;
-    uint4 k[N], v[N];
+    u32x4 k[N], v[N];
     float sc;
     bool ok;
 
@@ -54,8 +54,8 @@ struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
 #pragma unroll
         for (int i = 0; i < N; i++) {
             if (PIECES % 64 == 0 || lane + 64 * i < PIECES) {
-                k[i] = *reinterpret_cast<const uint4 *>(kp + (lane + 64 * i) * 16);
-                v[i] = *reinterpret_cast<const uint4 *>(vp + (lane + 64 * i) * 16);
+                k[i] = *reinterpret_cast<const u32x4 *>(kp + (lane + 64 * i) * 16);
+                v[i] = *reinterpret_cast<const u32x4 *>(vp + (lane + 64 * i) * 16);
             }
         }
         if constexpr (TYPE == kKvI8) {
@@ -66,32 +66,32 @@ struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
     // live: positions of the 16 that some row may see; V of the others is zero
     __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live) const {
         if (!ok) live = 0;
+        // dword j of a V piece: positions 2 j, 2 j + 1 of its 8 (an odd piece has the later 8)
+        uint32_t mask[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int e0 = live - 8 * (lane & 1) - 2 * j;
+            mask[j] = e0 >= 2 ? ~0u : e0 == 1 ? 0xFFFFu : 0u;
+        }
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int p = lane + 64 * i;
-            if (PIECES % 64 != 0 && p >= PIECES) break;
+            if (PIECES % 64 != 0 && p >= PIECES) continue;
             const int row = (p * 16) / (HD * SZ), at = (p * 16) % (HD * SZ);  // K: position, byte
             const int j = 16 * w + row;
             uint8_t *kd = buf + ((j & 32) + krow(j & 31)) * Lds<HD>::kRow;
             if constexpr (TYPE == kKvI8) {
                 const uint2 a = codes_to_f16(k[i].x), b = codes_to_f16(k[i].y), c2 = codes_to_f16(k[i].z), d = codes_to_f16(k[i].w);
-                *reinterpret_cast<uint4 *>(kd + at * 2) = make_uint4(a.x, a.y, b.x, b.y);
-                *reinterpret_cast<uint4 *>(kd + at * 2 + 16) = make_uint4(c2.x, c2.y, d.x, d.y);
+                *reinterpret_cast<u32x4 *>(kd + at * 2) = u32x4{a.x, a.y, b.x, b.y};
+                *reinterpret_cast<u32x4 *>(kd + at * 2 + 16) = u32x4{c2.x, c2.y, d.x, d.y};
                 const uint2 e = codes_to_f16(v[i].x), f = codes_to_f16(v[i].y), g = codes_to_f16(v[i].z), o = codes_to_f16(v[i].w);
                 uint8_t *vd = buf + Lds<HD>::kV + (w * HD + p) * 32;  // a piece is one column
-                *reinterpret_cast<uint4 *>(vd) = make_uint4(e.x, e.y, f.x, f.y);
-                *reinterpret_cast<uint4 *>(vd + 16) = make_uint4(g.x, g.y, o.x, o.y);
+                *reinterpret_cast<u32x4 *>(vd) = u32x4{e.x, e.y, f.x, f.y};
+                *reinterpret_cast<u32x4 *>(vd + 16) = u32x4{g.x, g.y, o.x, o.y};
             } else {
-                *reinterpret_cast<uint4 *>(kd + at) = k[i];
-                uint4 x = v[i];
-                if (live < 16) {
-                    const int e0 = live - 8 * (p & 1);  // positions of this piece that count
-                    x.x &= e0 >= 2 ? ~0u : e0 == 1 ? 0xFFFFu : 0u;
-                    x.y &= e0 >= 4 ? ~0u : e0 == 3 ? 0xFFFFu : 0u;
-                    x.z &= e0 >= 6 ? ~0u : e0 == 5 ? 0xFFFFu : 0u;
-                    x.w &= e0 >= 8 ? ~0u : e0 == 7 ? 0xFFFFu : 0u;
-                }
-                *reinterpret_cast<uint4 *>(buf + Lds<HD>::kV + w * HD * 32 + p * 16) = x;
+                *reinterpret_cast<u32x4 *>(kd + at) = k[i];
+                const u32x4 x = {v[i].x & mask[0], v[i].y & mask[1], v[i].z & mask[2], v[i].w & mask[3]};
+                *reinterpret_cast<u32x4 *>(buf + Lds<HD>::kV + w * HD * 32 + p * 16) = x;
             }
         }
         if constexpr (TYPE == kKvI8) {
@@ -103,7 +103,7 @@ struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
 };
 
 template <int TYPE, int HD>
-__global__ __launch_bounds__(256) void attn_prefill(AttnArgs a) {
+__global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
     constexpr int KS = HD / 16, DT = HD / 32, NP = Op::kPieces;
@@ -358,37 +358,56 @@ __global__ __launch_bounds__(256) void attn_prefill(AttnArgs a) {
 }
 
 // Joins the pieces of a row: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-// One workgroup a row; its four waves take every fourth piece.
+// One workgroup a row.  The pieces' factors go to LDS first; then HD / 4 lanes
+// read a piece (16 bytes each), 256 / (HD / 4) pieces at a time and four such
+// rounds in flight.  Bound by latency: with 64 pieces of 128 columns a thread
+// has eight loads.
+constexpr int kMaxPieces = 128;
+
 template <int HD>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
-    constexpr int PER = (HD + 63) / 64;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    constexpr int L = HD / 4, G = 256 / L;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t prow = blockIdx.x;
     if (a.start) {  // rows of no sequence stay as they were
         const int64_t row = prow / a.n_heads;
         if (row < a.start[0] || row >= a.start[a.c.n_seq]) return;
     }
+    __shared__ float s_r[kMaxPieces];
+    __shared__ f32x4 s_o[G][L];
+    // every wave finds the maximum and the sum for itself
+    float2 ml[kMaxPieces / 64];
     float mm = kNoMax;
-    for (int i = lane; i < a.splits; i += 64) mm = fmaxf(mm, a.part_ml[i * a.part_rows + prow].x);
-    for (int off = 32; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
-    float l = 0.f, o[PER];
-    for (int e = 0; e < PER; e++) o[e] = 0.f;
-    for (int i = wave; i < a.splits; i += 4) {
-        const int64_t at = i * a.part_rows + prow;
-        const float2 ml = a.part_ml[at];
-        const float r = exp2_fast(ml.x - mm);
-        l += r * ml.y;
-        for (int e = 0; e < PER; e++)
-            if (HD % 64 == 0 || lane + 64 * e < HD) o[e] += r * a.part_o[at * HD + lane + 64 * e];
+#pragma unroll
+    for (int k = 0; k < kMaxPieces / 64; k++) {
+        ml[k] = make_float2(kNoMax, 0.f);
+        if (lane + 64 * k < a.splits) ml[k] = a.part_ml[(lane + 64 * k) * a.part_rows + prow];
+        mm = fmaxf(mm, ml[k].x);
     }
-    __shared__ float s_l[4], s_o[4][PER * 64];
-    if (lane == 0) s_l[wave] = l;
-    for (int e = 0; e < PER; e++) s_o[wave][lane + 64 * e] = o[e];
+    for (int off = 32; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxPieces / 64; k++) {
+        const float r = exp2_fast(ml[k].x - mm);
+        l += r * ml[k].y;
+        if (tid < 64 && lane + 64 * k < a.splits) s_r[lane + 64 * k] = r;
+    }
+    for (int off = 32; off; off >>= 1) l += __shfl_xor(l, off);
     __syncthreads();
-    if (tid >= HD) return;
-    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-    const float v = (s_o[0][tid] + s_o[1][tid]) + (s_o[2][tid] + s_o[3][tid]);
-    a.out[prow * HD + tid] = l == 0.f ? 0.f : v / l;
+    const int g = tid / L, d = tid % L;
+    if (g < G) {
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o) + prow * L + d;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = g; i < a.splits; i += G) o += src[i * a.part_rows * L] * s_r[i];
+        s_o[g][d] = o;
+    }
+    __syncthreads();
+    if (tid >= L) return;
+    f32x4 o = s_o[0][tid];
+    for (int k = 1; k < G; k++) o += s_o[k][tid];
+    const f32x4 v = o * (l == 0.f ? 0.f : 1.f / l);
+    __builtin_memcpy(a.out + prow * HD + 4 * tid, &v, 16);
 }
 
 template <int TYPE, int HD>

@@ -192,11 +192,23 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
                 if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
             }
             __syncthreads();
-            if (tid == 0) {
-                int rest = left, b = 255;
-                while (b > 0 && hist[b] < rest) rest -= hist[b--];
-                s_prefix = prefix | ((uint32_t)b << shift);
-                s_left = rest;
+            if (wave == 0) {
+                // lane l has the four bins 255 - 4 l downwards; the one in
+                // which the count from the top reaches `left` says the digit
+                int cnt[4], all = 0;
+                for (int j = 0; j < 4; j++) all += cnt[j] = hist[255 - 4 * lane - j];
+                int upto = all;
+                for (int off = 1; off < 64; off <<= 1) {
+                    const int x = __shfl_up(upto, off);
+                    if (lane >= off) upto += x;
+                }
+                int above = upto - all;
+                if (above < left && left <= upto) {
+                    int j = 0;
+                    while (j < 3 && above + cnt[j] < left) above += cnt[j++];
+                    s_prefix = prefix | ((uint32_t)(255 - 4 * lane - j) << shift);
+                    s_left = left - above;
+                }
             }
             __syncthreads();
             prefix = s_prefix;

@@ -171,7 +171,7 @@ def test_append_even_rows(t):
 
 @pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
 @pytest.mark.parametrize("hd,heads,kv,page", [(64, 9, 3, 16), (96, 4, 2, 32), (128, 8, 2, 64), (256, 5, 1, 16),
-                                              (64, 17, 1, 128), (128, 2, 2, 16)])
+                                              (64, 17, 1, 128), (128, 2, 2, 16), (96, 20, 1, 64), (128, 18, 1, 32)])
 def test_decode_lengths(t, hd, heads, kv, page):
     """From an empty sequence to several chunks, ends inside pages and chunks."""
     lens = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 130, 257]
@@ -181,7 +181,7 @@ def test_decode_lengths(t, hd, heads, kv, page):
 
 @pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
 @pytest.mark.parametrize("n,heads,kv,hd", [(2, 4, 2, 64), (5, 6, 2, 128), (8, 8, 2, 64), (16, 3, 1, 96), (16, 8, 1, 256),
-                                           (3, 32, 1, 64)])
+                                           (3, 32, 1, 64), (8, 8, 1, 128), (1, 4, 1, 128), (1, 2, 1, 256), (2, 3, 1, 96)])
 def test_decode_several_tokens(t, n, heads, kv, hd):
     """n > 1, some sequences shorter than n: tokens without a position give zeros."""
     c, _ = make_cache(t, kv, hd, 32, [0, 1, n - 1, n, 40, 129, 300], 22)
