@@ -70,6 +70,14 @@ struct KvOp { typedef OpF16 Op; };
 template <>
 struct KvOp<kKvBF16> { typedef OpBF16 Op; };
 
+// A 16-byte load; NT for data that one workgroup reads once.
+template <bool NT>
+__device__ __forceinline__ u32x4 load_stream(const uint8_t *p) {
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+    if constexpr (NT) return __builtin_nontemporal_load(q);
+    return *q;
+}
+
 struct U128 { uint32_t w[4]; };
 template <class V>
 __device__ __forceinline__ V as_vec(U128 u) { return __builtin_bit_cast(V, u); }
@@ -129,5 +137,53 @@ __device__ __forceinline__ bool sees(int p, int key, int window, int sinks) {
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Joins the pieces of output row prow: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// One workgroup of 256 threads a row.  The pieces' factors go to LDS first; then HD / 4 lanes
+// read a piece (16 bytes each), 256 / (HD / 4) pieces at a time and four such
+// rounds in flight.  Bound by latency: with 64 pieces of 128 columns a thread
+// has eight loads.
+constexpr int kMaxPieces = 128;
+
+template <int HD>
+__device__ __forceinline__ void join_row(const AttnArgs &a, int64_t prow) {
+    constexpr int L = HD / 4, G = 256 / L;
+    const int tid = threadIdx.x, lane = tid & 63;
+    __shared__ float s_r[kMaxPieces];
+    __shared__ f32x4 s_o[G][L];
+    // every wave finds the maximum and the sum for itself
+    float2 ml[kMaxPieces / 64];
+    float mm = kNoMax;
+#pragma unroll
+    for (int k = 0; k < kMaxPieces / 64; k++) {
+        ml[k] = make_float2(kNoMax, 0.f);
+        if (lane + 64 * k < a.splits) ml[k] = a.part_ml[(lane + 64 * k) * a.part_rows + prow];
+        mm = fmaxf(mm, ml[k].x);
+    }
+    for (int off = 32; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
+    float l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxPieces / 64; k++) {
+        const float r = exp2_fast(ml[k].x - mm);
+        l += r * ml[k].y;
+        if (tid < 64 && lane + 64 * k < a.splits) s_r[lane + 64 * k] = r;
+    }
+    for (int off = 32; off; off >>= 1) l += __shfl_xor(l, off);
+    __syncthreads();
+    const int g = tid / L, d = tid % L;
+    if (g < G) {
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o) + prow * L + d;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = g; i < a.splits; i += G) o += src[i * a.part_rows * L] * s_r[i];
+        s_o[g][d] = o;
+    }
+    __syncthreads();
+    if (tid >= L) return;
+    f32x4 o = s_o[0][tid];
+    for (int k = 1; k < G; k++) o += s_o[k][tid];
+    const f32x4 v = o * (l == 0.f ? 0.f : 1.f / l);
+    __builtin_memcpy(a.out + prow * HD + 4 * tid, &v, 16);
+}
 
 }  // namespace qmv

@@ -118,8 +118,11 @@ static qmv_status decode_plan(const qmv_kv_cache *c, int32_t n, int32_t n_heads,
     p = attn_decode_plan(c->type, c->head_dim, c->n_seq, c->n_kv_heads, n_heads / c->n_kv_heads, n,
                          max_len, window, sinks, with_acc);
     if ((int64_t)p.tiles * c->n_kv_heads > 65535) return QMV_ESHAPE;
-    // the joining launch takes a workgroup of 256 threads a row
-    if ((p.splits > 1 || with_acc) && p.part_rows >= (1ll << 24)) return QMV_ESHAPE;
+    // the joining launch takes a workgroup of 256 threads a row, and for the
+    // weights one for every 256 positions of a key-value head
+    int64_t blocks = p.splits > 1 || with_acc ? p.part_rows : 0;
+    if (with_acc) blocks += c->n_seq * c->n_kv_heads * ((max_len + 255) / 256);
+    if (blocks >= (1ll << 24)) return QMV_ESHAPE;
     return QMV_OK;
 }
 

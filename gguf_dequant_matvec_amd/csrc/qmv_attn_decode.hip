@@ -46,6 +46,7 @@ struct KTile {
     static constexpr int W = HD * SZ / 16;  // dwords of a lane's quarter row
     uint32_t k[R][W];
 
+    template <bool NT>
     __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
         const int pos = chunk * kChunk<TYPE> + kChunk<TYPE> / 4 * (m >> 2);
         const int slot = (pos & ((1 << c.page_shift) - 1)) + (m & 3);
@@ -62,7 +63,7 @@ struct KTile {
             } else {
 #pragma unroll
                 for (int t = 0; t < HD * SZ / 64; t++) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(row + 64 * t + 16 * g);
+                    const u32x4 w = load_stream<NT>(row + 64 * t + 16 * g);
                     k[r][4 * t] = w.x, k[r][4 * t + 1] = w.y, k[r][4 * t + 2] = w.z, k[r][4 * t + 3] = w.w;
                 }
             }
@@ -89,6 +90,7 @@ struct VTile {
     uint32_t v[DT][4];
     float ks[TYPE == kKvI8 ? 16 : 1], vs[TYPE == kKvI8 ? 16 : 1];
 
+    template <bool NT>
     __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
         const int pmask = (1 << c.page_shift) - 1;
         const int slot = (chunk * kChunk<TYPE> + kChunk<TYPE> / 4 * g) & pmask;
@@ -96,7 +98,7 @@ struct VTile {
         const uint8_t *vp = head + (int64_t)(slot / kVBlock) * (HD * kVBlock * SZ) + (m * kVBlock + slot % kVBlock) * SZ;
 #pragma unroll
         for (int t = 0; t < DT; t++) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(vp + t * 16 * kVBlock * SZ);
+            const u32x4 w = load_stream<NT>(vp + t * 16 * kVBlock * SZ);
             v[t][0] = w.x, v[t][1] = w.y, v[t][2] = w.z, v[t][3] = w.w;
         }
         if constexpr (TYPE == kKvI8) {
@@ -125,6 +127,11 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
     typedef typename Op::Vec Vec;
     constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
     constexpr int KS = HD / 32, DT = HD / 16;
+    // With at most 16 rows a head's cache is read by one workgroup, once:
+    // nontemporal loads (32 sequences up to 8150 positions of 128 columns: 148
+    // -> 136 us).  More rows come with drafted tokens, whose tiles may read
+    // the same chunks: ordinary loads (8 x 8 tokens, window 4096: 34 against 37 us).
+    constexpr bool NT = RT == 1;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, g = lane >> 4;
     const int split = blockIdx.x, s = blockIdx.z;
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
@@ -165,8 +172,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
         KTile<TYPE, HD> kt;
         VTile<TYPE, HD> vt;
         bool ok = vpage >= 0;  // the lane group's positions are in a page (not a hole)
-        kt.load(c, h, ch.at(i), kpage, g, m);
-        vt.load(c, h, ch.at(i), vpage, g, m);
+        kt.template load<NT>(c, h, ch.at(i), kpage, g, m);
+        vt.template load<NT>(c, h, ch.at(i), vpage, g, m);
         kpage = page_of(i + kWaves, m >> 2);
         vpage = page_of(i + kWaves, g);
 
@@ -235,7 +242,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
             }
             // the K registers are free: the next chunk's K flies during the
             // softmax and the second product, its V during the next first one
-            if (more) kt.load(c, h, ch.at(i + kWaves), kpage, g, m);
+            if (more) kt.template load<NT>(c, h, ch.at(i + kWaves), kpage, g, m);
 
             const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
             // a chunk that every row sees whole needs no masks
@@ -332,7 +339,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                         for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
                 }
             }
-            if (more) vt.load(c, h, ch.at(i + kWaves), vpage, g, m);
+            if (more) vt.template load<NT>(c, h, ch.at(i + kWaves), vpage, g, m);
             if (!more) break;
             i += kWaves;
             ok = vpage >= 0;
@@ -409,14 +416,22 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
 }
 
 // acc[s][h][key] += sum over the rows of 2^(x - m) / l, rows in order.
-template <int TYPE>
-__global__ __launch_bounds__(256) void attn_weights(AttnArgs a, int rt16) {
+// The first part_rows workgroups join the pieces of a row each, the others take
+// 256 positions of a key-value head each: one launch for both.
+template <int TYPE, int HD>
+__global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     constexpr int CK = kChunk<TYPE>;
-    const int s = blockIdx.z, h = blockIdx.y;
+    if (blockIdx.x < a.part_rows) {
+        join_row<HD>(a, blockIdx.x);
+        return;
+    }
+    const int per = (a.limit + 255) / 256;  // workgroups a head
+    const int64_t unit = (int64_t)blockIdx.x - a.part_rows;
+    const int block = (int)(unit % per), h = (int)(unit / per % a.c.n_kv), s = (int)(unit / per / a.c.n_kv);
     const int len = kv_len(a.c, s, a.limit);
     const int n = (int)a.n, nrows = n * a.group;
-    if ((int64_t)blockIdx.x * 256 >= len) return;
-    const int key = blockIdx.x * 256 + threadIdx.x;
+    if ((int64_t)block * 256 >= len) return;
+    const int key = block * 256 + threadIdx.x;
     const int64_t head = (int64_t)s * a.c.n_kv + h;
     __shared__ float s_m[16], s_r[16];
     float sum = 0.f;
@@ -467,10 +482,12 @@ hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
         e = launch_main(attn_decode<TYPE, HD, RT, true>, grid, dim3(kWaves * 64), 0, s, a);
     else
         e = launch_main(attn_decode<TYPE, HD, RT, false>, grid, dim3(kWaves * 64), 0, s, a);
-    if (e != hipSuccess || (p.splits == 1 && !a.acc)) return e;
-    e = launch_attn_join(a, s);
-    if (e != hipSuccess || !a.acc) return e;
-    return launch_aux(attn_weights<TYPE>, dim3((a.limit + 255) / 256, a.c.n_kv, a.c.n_seq), dim3(256), 0, s, a, 16 * RT);
+    if (e != hipSuccess) return e;
+    if (a.acc) {
+        const int64_t blocks = p.part_rows + (int64_t)a.c.n_seq * a.c.n_kv * ((a.limit + 255) / 256);
+        return launch_aux(attn_join_weights<TYPE, HD>, dim3((uint32_t)blocks), dim3(256), 0, s, a, 16 * RT);
+    }
+    return p.splits > 1 ? launch_attn_join(a, s) : hipSuccess;
 }
 
 template <int TYPE, int HD>
@@ -509,7 +526,13 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
     }
     const int64_t chunks = (most + ck - 1) / ck;
     const int64_t base = n_seq * n_kv * p.tiles;
-    int64_t splits = (1024 + base - 1) / base;       // two to four workgroups per compute unit
+    // Two workgroups fit a compute unit of 256.  Sequences that may differ in
+    // length get twice that, for balance (the ragged batch above: 134 us with
+    // 512, 131 with 1024); one sequence, a window or a 32-row tile does not
+    // (131071 8-bit positions: 60 against 64 us; the drafted tokens: 26
+    // against 34 us).
+    const int64_t want = n_seq == 1 || window > 0 || p.rt == 2 ? 512 : 1024;
+    int64_t splits = (want + base - 1) / base;
     if (splits > chunks / 8) splits = chunks / 8;    // at least two chunks per wave
     if (splits > 128) splits = 128;
     p.splits = splits < 1 ? 1 : (int)splits;

@@ -155,6 +155,34 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
     const int64_t nrows = n * a.group;
     const int64_t r0 = (int64_t)tile * kBM;
 
+    // what the tile's and this wave's rows see
+    auto pos_of = [&](int64_t r) {
+        const int64_t p = (int64_t)len - n + (r < nrows ? r : nrows - 1) / a.group;
+        return p < -1 ? -1 : (int)p;
+    };
+    const int pmin = pos_of(r0), pmax = pos_of(r0 + kBM - 1);
+    const bool wave_live = r0 + 32 * wave < nrows;
+    const int wmin = pos_of(r0 + 32 * wave), wmax = wave_live ? pos_of(r0 + 32 * wave + 31) : -1;
+    const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, kBK);
+    const int begin = (int)((int64_t)ch.n * split / a.splits), end = (int)((int64_t)ch.n * (split + 1) / a.splits);
+
+    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
+    auto page_of = [&](int i) {  // page of this wave's 16 positions of chunk number i
+        if (i >= end) return -1;
+        const int pi = (ch.at(i) * kBK + 16 * wave) >> c.page_shift;
+        if (pi > last_page) return -1;
+        const int pg = c.table[(int64_t)s * c.table_ld + pi];
+        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
+    };
+    auto live_of = [&](int i) {  // how many of its 16 positions some row of the tile sees
+        const int left = pmax + 1 - (ch.at(i) * kBK + 16 * wave);
+        return left > 16 ? 16 : left < 0 ? 0 : left;
+    };
+    // the first chunk is on its way while the queries are split
+    Stage<TYPE, HD> st;
+    int page = __builtin_amdgcn_readfirstlane(page_of(begin));
+    st.load(c, h, page, begin < end ? ch.at(begin) * kBK + 16 * wave : 0, lane);
+
     // this wave's rows
     const int64_t rr = r0 + 32 * wave + col;
     const int64_t tok = rr / a.group;
@@ -194,17 +222,6 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
             split8<Op>(f, qf[t]);
         }
     }
-    // what the tile's and this wave's rows see
-    auto pos_of = [&](int64_t r) {
-        const int64_t p = (int64_t)len - n + (r < nrows ? r : nrows - 1) / a.group;
-        return p < -1 ? -1 : (int)p;
-    };
-    const int pmin = pos_of(r0), pmax = pos_of(r0 + kBM - 1);
-    const bool wave_live = r0 + 32 * wave < nrows;
-    const int wmin = pos_of(r0 + 32 * wave), wmax = wave_live ? pos_of(r0 + 32 * wave + 31) : -1;
-    const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, kBK);
-    const int begin = (int)((int64_t)ch.n * split / a.splits), end = (int)((int64_t)ch.n * (split + 1) / a.splits);
-
     float mrun = kNoMax, lrun = 0.f, vmul = kVmulNone;
     f32x16 o[DT];
 #pragma unroll
@@ -212,24 +229,8 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
 #pragma unroll
         for (int e = 0; e < 16; e++) o[t][e] = 0.f;
 
-    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
-    auto page_of = [&](int i) {  // page of this wave's 16 positions of chunk number i
-        if (i >= end) return -1;
-        const int pi = (ch.at(i) * kBK + 16 * wave) >> c.page_shift;
-        if (pi > last_page) return -1;
-        const int pg = c.table[(int64_t)s * c.table_ld + pi];
-        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
-    };
-    auto live_of = [&](int i) {  // how many of its 16 positions some row of the tile sees
-        const int left = pmax + 1 - (ch.at(i) * kBK + 16 * wave);
-        return left > 16 ? 16 : left < 0 ? 0 : left;
-    };
-    Stage<TYPE, HD> st;
-    int page = __builtin_amdgcn_readfirstlane(page_of(begin));
-    if (begin < end) {
-        st.load(c, h, page, ch.at(begin) * kBK + 16 * wave, lane);
+    if (begin < end)
         st.store(lds + (begin & 1) * Lds<HD>::kBytes, lds + Lds<HD>::kOk + (begin & 1) * 4, wave, lane, live_of(begin));
-    }
     page = __builtin_amdgcn_readfirstlane(page_of(begin + 1));
     for (int i = begin; i < end; i++) {
         uint8_t *buf = lds + (i & 1) * Lds<HD>::kBytes;
@@ -357,57 +358,14 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
     }
 }
 
-// Joins the pieces of a row: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-// One workgroup a row.  The pieces' factors go to LDS first; then HD / 4 lanes
-// read a piece (16 bytes each), 256 / (HD / 4) pieces at a time and four such
-// rounds in flight.  Bound by latency: with 64 pieces of 128 columns a thread
-// has eight loads.
-constexpr int kMaxPieces = 128;
-
 template <int HD>
 __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
-    constexpr int L = HD / 4, G = 256 / L;
-    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t prow = blockIdx.x;
     if (a.start) {  // rows of no sequence stay as they were
         const int64_t row = prow / a.n_heads;
         if (row < a.start[0] || row >= a.start[a.c.n_seq]) return;
     }
-    __shared__ float s_r[kMaxPieces];
-    __shared__ f32x4 s_o[G][L];
-    // every wave finds the maximum and the sum for itself
-    float2 ml[kMaxPieces / 64];
-    float mm = kNoMax;
-#pragma unroll
-    for (int k = 0; k < kMaxPieces / 64; k++) {
-        ml[k] = make_float2(kNoMax, 0.f);
-        if (lane + 64 * k < a.splits) ml[k] = a.part_ml[(lane + 64 * k) * a.part_rows + prow];
-        mm = fmaxf(mm, ml[k].x);
-    }
-    for (int off = 32; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
-    float l = 0.f;
-#pragma unroll
-    for (int k = 0; k < kMaxPieces / 64; k++) {
-        const float r = exp2_fast(ml[k].x - mm);
-        l += r * ml[k].y;
-        if (tid < 64 && lane + 64 * k < a.splits) s_r[lane + 64 * k] = r;
-    }
-    for (int off = 32; off; off >>= 1) l += __shfl_xor(l, off);
-    __syncthreads();
-    const int g = tid / L, d = tid % L;
-    if (g < G) {
-        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o) + prow * L + d;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = g; i < a.splits; i += G) o += src[i * a.part_rows * L] * s_r[i];
-        s_o[g][d] = o;
-    }
-    __syncthreads();
-    if (tid >= L) return;
-    f32x4 o = s_o[0][tid];
-    for (int k = 1; k < G; k++) o += s_o[k][tid];
-    const f32x4 v = o * (l == 0.f ? 0.f : 1.f / l);
-    __builtin_memcpy(a.out + prow * HD + 4 * tid, &v, 16);
+    join_row<HD>(a, prow);
 }
 
 template <int TYPE, int HD>

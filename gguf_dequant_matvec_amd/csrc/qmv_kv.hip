@@ -4,18 +4,21 @@
 #include "qmv_internal.h"
 #include "qmv_kv.h"
 
+#include <type_traits>
+
 namespace qmv {
 
 namespace {
 
 // ---- append -----------------------------------------------------------------
-// A workgroup takes 16 consecutive rows of one key-value head.  K rows are
-// rounded and stored as they come (16 bytes a thread); V goes through LDS,
-// because a V block keeps the 16 positions of one column next to each other:
-// lanes run over the rows first, so the 16 two-byte stores of a column land in
-// one 32-byte run.  Bound by the f32 reads.
-constexpr int kAppendRows = 16;
-
+// A workgroup takes ROWS consecutive rows of one key-value head.  All f32
+// values are on their way before the positions are looked up (two dependent
+// loads).  K rows are rounded and stored as they come, 16 bytes a thread.  V
+// goes through LDS, already rounded, because a V block keeps the 16 positions
+// of one column next to each other: a thread gathers 8 positions of a column
+// and stores them at once where the workgroup's rows cover all 8, else one by
+// one.  Bound by the f32 reads, or for few rows by latency: 16 rows keep more
+// workgroups in flight, 64 leave fewer partly covered runs.
 template <int TYPE>
 __device__ __forceinline__ uint32_t kv_round(float x) {
     if constexpr (TYPE == kKvF16) {
@@ -31,19 +34,43 @@ __device__ __forceinline__ int kv_code(float x, float d) {
     return (int)fminf(fmaxf(r, -127.f), 127.f);
 }
 
-template <int TYPE, int HD>
+template <int TYPE, int HD, int ROWS>
 __global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int32_t *start,
                                                  const float *__restrict__ k, int64_t ldk,
                                                  const float *__restrict__ v, int64_t ldv) {
     constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
-    constexpr int PIECES = HD / 8;  // 8 columns a thread
-    __shared__ int s_page[kAppendRows], s_slot[kAppendRows];
-    __shared__ float s_v[kAppendRows][HD + 1];
-    __shared__ float s_d[2][kAppendRows];
+    constexpr int PIECES = HD / 8;                         // 8 columns a thread
+    constexpr int N = (ROWS * PIECES + 255) / 256;         // pieces a thread
+    constexpr int VROW = HD + (TYPE == kKvI8 ? 4 : 2);     // padded row in LDS, values
+    typedef typename std::conditional<TYPE == kKvI8, int8_t, uint16_t>::type Val;
+    __shared__ int s_page[ROWS], s_slot[ROWS];
+    __shared__ bool s_run[ROWS];  // the row's aligned group of 8 positions is here, row by row
+    __shared__ __align__(16) Val s_v[ROWS * VROW];
+    __shared__ float s_d[2][ROWS];
+    __shared__ float s_part[TYPE == kKvI8 ? 2 : 1][TYPE == kKvI8 ? ROWS * PIECES : 1];
     const int tid = threadIdx.x, h = blockIdx.y;
-    const int64_t row0 = (int64_t)blockIdx.x * kAppendRows;
+    const int64_t row0 = (int64_t)blockIdx.x * ROWS;
+    const int rows = n - row0 < ROWS ? (int)(n - row0) : ROWS;
 
-    if (tid < kAppendRows) {
+    float kf[N][8], vf[N][8];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int e = tid + 256 * i, r = e / PIECES, p = e % PIECES;
+        if (r < rows) {
+            const uint8_t *ks = reinterpret_cast<const uint8_t *>(k + (row0 + r) * ldk + (int64_t)h * HD + p * 8);
+            const uint8_t *vs = reinterpret_cast<const uint8_t *>(v + (row0 + r) * ldv + (int64_t)h * HD + p * 8);
+            const float4 a = __builtin_bit_cast(float4, load16(ks)), b = __builtin_bit_cast(float4, load16(ks + 16));
+            const float4 x = __builtin_bit_cast(float4, load16(vs)), y = __builtin_bit_cast(float4, load16(vs + 16));
+            kf[i][0] = a.x, kf[i][1] = a.y, kf[i][2] = a.z, kf[i][3] = a.w;
+            kf[i][4] = b.x, kf[i][5] = b.y, kf[i][6] = b.z, kf[i][7] = b.w;
+            vf[i][0] = x.x, vf[i][1] = x.y, vf[i][2] = x.z, vf[i][3] = x.w;
+            vf[i][4] = y.x, vf[i][5] = y.y, vf[i][6] = y.z, vf[i][7] = y.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) kf[i][j] = vf[i][j] = 0.f;
+        }
+    }
+    if (tid < ROWS) {
         const int64_t r = row0 + tid;
         int page = -1, slot = 0;
         if (r < n) {
@@ -73,81 +100,120 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int3
         s_page[tid] = page;
         s_slot[tid] = slot;
     }
-    if (TYPE == kKvI8) {
-        // row maxima: 16 lanes a row
-        const int i = tid >> 4, l = tid & 15;
-        float mk = 0.f, mv = 0.f;
-        if (row0 + i < n) {
-            const float *kr = k + (row0 + i) * ldk + (int64_t)h * HD;
-            const float *vr = v + (row0 + i) * ldv + (int64_t)h * HD;
-            for (int d = l; d < HD; d += 16) {
-                // (x > m keeps m for a NaN: the sum of the row's NaN with 0 * x stays NaN below)
-                mk = fabsf(kr[d]) > mk || kr[d] != kr[d] ? fabsf(kr[d]) : mk;
-                mv = fabsf(vr[d]) > mv || vr[d] != vr[d] ? fabsf(vr[d]) : mv;
+    if constexpr (TYPE == kKvI8) {
+        // row maxima; a NaN anywhere makes the maximum NaN
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int e = tid + 256 * i;
+            float mk = 0.f, mv = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                mk = fmaxf(mk, fabsf(kf[i][j]));
+                mv = fmaxf(mv, fabsf(vf[i][j]));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j++) {  // (fmaxf drops a NaN)
+                mk = kf[i][j] != kf[i][j] ? kf[i][j] : mk;
+                mv = vf[i][j] != vf[i][j] ? vf[i][j] : mv;
+            }
+            if (e < ROWS * PIECES) {
+                s_part[0][e] = mk;
+                s_part[1][e] = mv;
             }
         }
-        for (int o = 8; o; o >>= 1) {
-            const float a = __shfl_xor(mk, o, 16), b = __shfl_xor(mv, o, 16);
-            mk = a > mk || a != a ? a : mk;
-            mv = b > mv || b != b ? b : mv;
+        __syncthreads();
+        for (int e = tid; e < 2 * ROWS; e += 256) {
+            const int which = e / ROWS, r = e % ROWS;
+            float m = 0.f;
+            bool nan = false;
+            for (int p = 0; p < PIECES; p++) {
+                const float x = s_part[which][r * PIECES + p];
+                nan = nan || x != x;
+                m = fmaxf(m, x);
+            }
+            s_d[which][r] = nan ? __builtin_nanf("") : m / 127.f;
         }
-        if (l == 0) {
-            s_d[0][i] = mk / 127.f;
-            s_d[1][i] = mv / 127.f;
-        }
-    }
-    for (int e = tid; e < kAppendRows * HD; e += 256) {
-        const int i = e / HD, d = e % HD;
-        if (row0 + i < n) s_v[i][d] = v[(row0 + i) * ldv + (int64_t)h * HD + d];
     }
     __syncthreads();
 
     const int64_t page_size = 1ll << c.page_shift;
-    for (int e = tid; e < kAppendRows * PIECES; e += 256) {
-        const int i = e / PIECES, p = e % PIECES;
-        if (s_page[i] < 0) continue;
-        const uint8_t *src = reinterpret_cast<const uint8_t *>(k + (row0 + i) * ldk + (int64_t)h * HD + p * 8);
-        const float4 x = __builtin_bit_cast(float4, load16(src));
-        const float4 y = __builtin_bit_cast(float4, load16(src + 16));
-        const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        uint8_t *dst = kv_head(c, s_page[i], h) + ((int64_t)s_slot[i] * HD + p * 8) * SZ;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if constexpr (TYPE == kKvI8) {
-            for (int j = 0; j < 8; j++) w[j >> 2] |= (uint32_t)(kv_code(f[j], s_d[0][i]) & 0xFF) << (8 * (j & 3));
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int e = tid + 256 * i, r = e / PIECES, p = e % PIECES;
+        if (r >= ROWS) continue;
+        const int page = s_page[r];
+        uint32_t w[4] = {0, 0, 0, 0}, x[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if constexpr (TYPE == kKvI8) {
+                w[j >> 2] |= (uint32_t)(kv_code(kf[i][j], s_d[0][r]) & 0xFF) << (8 * (j & 3));
+                x[j >> 2] |= (uint32_t)(kv_code(vf[i][j], s_d[1][r]) & 0xFF) << (8 * (j & 3));
+            } else {
+                w[j >> 1] |= kv_round<TYPE>(kf[i][j]) << (16 * (j & 1));
+                x[j >> 1] |= kv_round<TYPE>(vf[i][j]) << (16 * (j & 1));
+            }
+        }
+        uint32_t *sv = reinterpret_cast<uint32_t *>(s_v + r * VROW + p * 8);
+#pragma unroll
+        for (int j = 0; j < 2 * SZ; j++) sv[j] = x[j];
+        if (page < 0) continue;
+        uint8_t *dst = kv_head(c, page, h) + ((int64_t)s_slot[r] * HD + p * 8) * SZ;
+        if constexpr (TYPE == kKvI8)
             *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        } else {
-            for (int j = 0; j < 8; j++) w[j >> 1] |= kv_round<TYPE>(f[j]) << (16 * (j & 1));
+        else
             *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (tid < ROWS) {
+        const int r8 = tid - (s_slot[tid] & 7);
+        bool run = r8 >= 0 && r8 + 8 <= ROWS;
+        for (int j = 0; run && j < 8; j++)
+            run = s_page[r8 + j] == s_page[tid] && s_slot[r8 + j] == (s_slot[tid] & ~7) + j;
+        s_run[tid] = run;
+    }
+    if (TYPE == kKvI8 && tid < 2 * ROWS) {
+        const int r = tid % ROWS, which = tid / ROWS;
+        if (s_page[r] >= 0) {
+            float *sc = reinterpret_cast<float *>(kv_head(c, s_page[r], h) + 2 * page_size * HD);
+            sc[which * page_size + s_slot[r]] = s_d[which][r];
         }
     }
-    for (int e = tid; e < kAppendRows * HD; e += 256) {
-        const int i = e % kAppendRows, d = e / kAppendRows;
-        if (s_page[i] < 0) continue;
-        const int slot = s_slot[i];
-        uint8_t *dst = kv_head(c, s_page[i], h) + page_size * HD * SZ +
+    __syncthreads();
+    // V: lanes run over columns; a whole group leaves with its first row
+    for (int e = tid; e < ROWS * HD; e += 256) {
+        const int r = e / HD, d = e % HD;
+        const int page = s_page[r], slot = s_slot[r];
+        if (page < 0) continue;
+        uint8_t *dst = kv_head(c, page, h) + page_size * HD * SZ +
                        ((int64_t)(slot / kVBlock) * (HD * kVBlock) + d * kVBlock + slot % kVBlock) * SZ;
-        if constexpr (TYPE == kKvI8)
-            *reinterpret_cast<int8_t *>(dst) = (int8_t)kv_code(s_v[i][d], s_d[1][i]);
-        else
-            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)kv_round<TYPE>(s_v[i][d]);
-    }
-    if (TYPE == kKvI8 && tid < 2 * kAppendRows) {
-        const int i = tid & 15, which = tid >> 4;
-        if (s_page[i] >= 0) {
-            float *sc = reinterpret_cast<float *>(kv_head(c, s_page[i], h) + 2 * page_size * HD);
-            sc[which * page_size + s_slot[i]] = s_d[which][i];
+        if (!s_run[r]) {
+            *reinterpret_cast<Val *>(dst) = s_v[r * VROW + d];
+        } else if ((slot & 7) == 0) {
+            uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t b = TYPE == kKvI8 ? (uint8_t)s_v[(r + j) * VROW + d] : (uint16_t)s_v[(r + j) * VROW + d];
+                w[j / (4 / SZ)] |= b << (8 * SZ * (j % (4 / SZ)));
+            }
+            if constexpr (TYPE == kKvI8)
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
 
 // ---- eviction: choosing -------------------------------------------------------
-// One workgroup per sequence and key-value head.  The m-th largest score of
-// the middle positions is found by four 8-bit radix passes over an
-// order-preserving integer key (counts in LDS), then one ordered pass writes
-// the kept positions by prefix sums; among equal scores at the border the
-// lowest positions are kept.
+// One workgroup per sequence and key-value head.  A thread has 8 consecutive
+// positions (up to 8192 a workgroup at a time; with no more the keys stay in
+// registers).  The m-th largest score of the middle positions is found by four
+// 8-bit radix passes over an order-preserving integer key (counts in LDS),
+// then prefix sums over the threads place the kept positions in order; among
+// equal scores at the border the lowest positions are kept.  Bound by latency:
+// three barriers a pass.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
+constexpr int kSelPer = 8;                            // positions a thread
+constexpr int kSelStep = kSelThreads * kSelPer;
 
 __device__ __forceinline__ uint32_t score_key(float v) {
     if (v != v) return 0xFFFFFFFFu;   // NaN ranks above everything
@@ -178,6 +244,23 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
     const int lo = e.first, hi = len - e.recent;   // candidates: lo <= position < hi
     const int m = e.keep - e.first - e.recent;     // of which m stay, 0 <= m < hi - lo
 
+    uint32_t key[kSelPer];
+    auto load_keys = [&](int base) {
+        const int p0 = base + tid * kSelPer;
+        float f[kSelPer];
+        if (p0 + kSelPer <= len) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(acc + p0);
+            const float4 a = __builtin_bit_cast(float4, load16(src)), b = __builtin_bit_cast(float4, load16(src + 16));
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSelPer; j++) f[j] = p0 + j < len ? acc[p0 + j] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kSelPer; j++) key[j] = score_key(f[j]);
+    };
+    load_keys(0);
+
     __shared__ int hist[256];
     __shared__ uint32_t s_prefix;
     __shared__ int s_left;
@@ -185,11 +268,14 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
     int left = m;  // rank still to go inside the current prefix
     if (m > 0) {
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+            if (tid < 256) hist[tid] = 0;
             __syncthreads();
-            for (int i = lo + tid; i < hi; i += kSelThreads) {
-                const uint32_t key = score_key(acc[i]);
-                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+            for (int base = 0; base < len; base += kSelStep) {
+                if (len > kSelStep) load_keys(base);
+                const int p0 = base + tid * kSelPer;
+#pragma unroll
+                for (int j = 0; j < kSelPer; j++)
+                    if (p0 + j >= lo && p0 + j < hi && (key[j] & mask) == prefix) atomicAdd(&hist[(key[j] >> shift) & 255], 1);
             }
             __syncthreads();
             if (wave == 0) {
@@ -219,43 +305,52 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
     // kept: everything protected, every key above `prefix`, and the first
     // `left` candidates equal to it
     __shared__ int w_ties[kSelWaves], w_kept[kSelWaves];
+    auto before = [&](int own, int *w_sum, int *all) {  // sum of the earlier threads' counts
+        int upto = own;
+        for (int off = 1; off < 64; off <<= 1) {
+            const int x = __shfl_up(upto, off);
+            if (lane >= off) upto += x;
+        }
+        if (lane == 63) w_sum[wave] = upto;
+        __syncthreads();
+        int r = upto - own, sum = 0;
+        for (int w = 0; w < kSelWaves; w++) {
+            if (w < wave) r += w_sum[w];
+            sum += w_sum[w];
+        }
+        *all = sum;
+        return r;
+    };
     int ties_before = 0, kept_before = 0;
-    for (int base = 0; base < len; base += kSelThreads) {
-        const int i = base + tid;
-        bool sure = false, tie = false;
-        float v = 0.f;
-        if (i < len) {
-            v = acc[i];
-            if (i < lo || i >= hi) {
-                sure = true;
-            } else if (m > 0) {
-                const uint32_t key = score_key(v);
-                sure = key > prefix;
-                tie = key == prefix;
+    for (int base = 0; base < len; base += kSelStep) {
+        if (len > kSelStep) load_keys(base);
+        const int p0 = base + tid * kSelPer;
+        uint32_t sure = 0, tie = 0;
+#pragma unroll
+        for (int j = 0; j < kSelPer; j++) {
+            const int i = p0 + j;
+            if (i >= len) continue;
+            if (i < lo || i >= hi || (m > 0 && key[j] > prefix)) sure |= 1u << j;
+            else if (m > 0 && key[j] == prefix) tie |= 1u << j;
+        }
+        int all_ties, all_kept;
+        int rank = ties_before + before(__popc(tie), w_ties, &all_ties);
+#pragma unroll
+        for (int j = 0; j < kSelPer; j++)
+            if ((tie >> j) & 1) {
+                if (rank < left) sure |= 1u << j;
+                rank++;
             }
-        }
-        const uint64_t below = (1ull << lane) - 1;
-        const uint64_t tb = __ballot(tie);
-        if (lane == 0) w_ties[wave] = __popcll(tb);
-        __syncthreads();
-        int rank = ties_before + __popcll(tb & below), all_ties = 0;
-        for (int w = 0; w < kSelWaves; w++) {
-            if (w < wave) rank += w_ties[w];
-            all_ties += w_ties[w];
-        }
-        const bool keep = sure || (tie && rank < left);
-        const uint64_t kb = __ballot(keep);
-        if (lane == 0) w_kept[wave] = __popcll(kb);
-        __syncthreads();
-        int at = kept_before + __popcll(kb & below), all_kept = 0;
-        for (int w = 0; w < kSelWaves; w++) {
-            if (w < wave) at += w_kept[w];
-            all_kept += w_kept[w];
-        }
-        if (keep && at < e.keep) {
-            kept[at] = i;
-            acc_out[at] = v;
-        }
+        int at = kept_before + before(__popc(sure), w_kept, &all_kept);
+#pragma unroll
+        for (int j = 0; j < kSelPer; j++)
+            if ((sure >> j) & 1) {
+                if (at < e.keep) {
+                    kept[at] = p0 + j;
+                    acc_out[at] = acc[p0 + j];
+                }
+                at++;
+            }
         ties_before += all_ties;
         kept_before += all_kept;
         __syncthreads();
@@ -263,27 +358,44 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
 }
 
 // ---- eviction: moving -----------------------------------------------------------
-// A workgroup fills one V block (16 positions) of the destination.  K rows are
-// copied as they are; for V it reads each source block once (kept positions
-// are in order, so the 16 sources lie in few blocks) and picks the kept
-// columns into LDS, from where the new block leaves in one run.
+// A workgroup fills 64 positions (four V blocks) of the destination.  K rows
+// are copied as they are.  The sources are in order, so they lie in few
+// source V blocks (five where one position in sixteen is dropped): those are
+// read whole, up to GROUP at a time, into LDS rows padded so that columns
+// fall into different banks, and each thread picks the kept positions of its
+// columns, 16 bytes of the new block at a time.  Bound by memory: both caches
+// once.
+constexpr int kMove = 64;
+
 template <int SZ, int HD>
 __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
+    constexpr int ROW = HD * SZ;                         // bytes of a K row
+    constexpr int KP = kMove * ROW / 16;                 // 16-byte pieces of the K rows
+    constexpr int KN = (KP + 255) / 256;
+    constexpr int VB = HD * kVBlock * SZ;                // bytes of a V block
+    constexpr int VP = VB / 16, VN = (VP + 255) / 256;   // its pieces
+    constexpr int PAD = SZ == 2 ? 40 : 20;               // LDS bytes of a column of a block
+    constexpr int GROUP = HD == 256 ? 4 : 6;             // source blocks in LDS
+    constexpr int PER = 16 / SZ;                         // positions in a piece
+    constexpr int OUT = kMove / PER * HD;                // pieces of the new blocks
+    constexpr int ON = (OUT + 255) / 256;
+    typedef typename std::conditional<SZ == 2, uint16_t, uint8_t>::type Val;
+
     const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
     const int len = kv_len(c, s, e.limit);
     const int out_len = len < e.keep ? len : e.keep;
-    const int i0 = blockIdx.x * kVBlock;
+    const int i0 = blockIdx.x * kMove;
     if (i0 >= out_len) return;
-    const int cnt = out_len - i0 < kVBlock ? out_len - i0 : kVBlock;
+    const int cnt = out_len - i0 < kMove ? out_len - i0 : kMove;
     const int64_t page_size = 1ll << c.page_shift;
-    const int dpg = e.dst[(int64_t)s * e.dst_ld + (i0 >> c.page_shift)];
-    if ((uint32_t)dpg >= (uint32_t)c.n_pages) return;
-    uint8_t *dst = kv_head(c, dpg, h);
-    const int slot0 = i0 & (int)(page_size - 1);
+    const int pmask = (int)page_size - 1;
 
-    __shared__ int s_src[kVBlock], s_page[kVBlock];
-    __shared__ __align__(16) uint8_t s_v[HD * kVBlock * SZ];
-    if (tid < kVBlock) {
+    __shared__ int s_src[kMove], s_page[kMove], s_ord[kMove];
+    __shared__ int s_first[kMove + 1];   // first source of each source block
+    __shared__ int s_dst[kMove / kVBlock];
+    __shared__ int s_blocks;
+    __shared__ __align__(16) uint8_t s_v[GROUP * HD * PAD];
+    if (tid < kMove) {
         int src = -1, page = -1;
         if (tid < cnt) {
             src = e.kept[((int64_t)s * c.n_kv + h) * e.keep + i0 + tid];
@@ -291,75 +403,144 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
         }
         s_src[tid] = src;
         s_page[tid] = page;
+        const int prev = __shfl_up(src, 1);
+        const bool first = tid < cnt && (tid == 0 || src / kVBlock != prev / kVBlock);
+        const uint64_t all = __ballot(first);
+        const int ord = __popcll(all & ((2ull << tid) - 1)) - 1;
+        s_ord[tid] = ord;
+        if (first) s_first[ord] = tid;
+        if (tid == 0) s_blocks = __popcll(all);
+    } else if (tid < kMove + kMove / kVBlock) {
+        const int at = i0 + (tid - kMove) * kVBlock;
+        int pg = -1;
+        if (at < out_len) {
+            pg = e.dst[(int64_t)s * e.dst_ld + (at >> c.page_shift)];
+            if ((uint32_t)pg >= (uint32_t)c.n_pages) pg = -1;
+        }
+        s_dst[tid - kMove] = pg;
     }
-    // a block that is not filled keeps its other positions
-    constexpr int VB = HD * kVBlock * SZ;  // bytes of a V block
-    uint8_t *vdst = dst + page_size * HD * SZ + (int64_t)(slot0 / kVBlock) * VB;
-    if (cnt < kVBlock)
-        for (int o = tid * 16; o < VB; o += 256 * 16) *reinterpret_cast<uint4 *>(s_v + o) = *reinterpret_cast<const uint4 *>(vdst + o);
     __syncthreads();
 
-    constexpr int ROW = HD * SZ;
-    for (int o = tid * 16; o < cnt * ROW; o += 256 * 16) {
-        const int i = o / ROW, b = o % ROW;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (s_page[i] >= 0)
-            w = *reinterpret_cast<const uint4 *>(kv_head(c, s_page[i], h) + (s_src[i] & (page_size - 1)) * ROW + b);
-        *reinterpret_cast<uint4 *>(dst + (int64_t)(slot0 + i) * ROW + b) = w;
+    // K: all loads, then all stores
+    uint4 kw[KN];
+#pragma unroll
+    for (int j = 0; j < KN; j++) {
+        const int o = (tid + 256 * j) * 16, i = o / ROW, b = o % ROW;
+        kw[j] = make_uint4(0, 0, 0, 0);
+        if (i < cnt && s_page[i] >= 0)
+            kw[j] = *reinterpret_cast<const uint4 *>(kv_head(c, s_page[i], h) + (int64_t)(s_src[i] & pmask) * ROW + b);
     }
-    for (int a = 0; a < cnt;) {
-        // sources a .. z-1 share one source block
-        int z = a + 1;
-        while (z < cnt && s_src[z] / kVBlock == s_src[a] / kVBlock) z++;
-        const uint8_t *vsrc = nullptr;
-        if (s_page[a] >= 0)
-            vsrc = kv_head(c, s_page[a], h) + page_size * HD * SZ +
-                   (int64_t)((s_src[a] & (int)(page_size - 1)) / kVBlock) * VB;
-        for (int o = tid * 16; o < VB; o += 256 * 16) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (vsrc) w = *reinterpret_cast<const uint4 *>(vsrc + o);
-            constexpr int PER = 16 / SZ;  // positions in 16 bytes
-            const int d = o / (kVBlock * SZ), p0 = (o / SZ) % kVBlock;
-            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
-            for (int i = a; i < z; i++) {
-                const int p = s_src[i] % kVBlock - p0;
-                if (p < 0 || p >= PER) continue;
+    const int blocks = s_blocks;
+    uint4 vw[GROUP][VN];
+    auto load_group = [&](int g0) {
+#pragma unroll
+        for (int k = 0; k < GROUP; k++) {
+            const int b = g0 + k;
+            const int a = b < blocks ? s_first[b] : 0;
+            const int page = b < blocks ? s_page[a] : -1;
+            const uint8_t *src = kv_head(c, page < 0 ? 0 : page, h) + page_size * ROW + (int64_t)((s_src[a] & pmask) / kVBlock) * VB;
+#pragma unroll
+            for (int j = 0; j < VN; j++) {
+                const int p = tid + 256 * j;
+                vw[k][j] = make_uint4(0, 0, 0, 0);
+                if (page >= 0 && p < VP) vw[k][j] = *reinterpret_cast<const uint4 *>(src + p * 16);
+            }
+        }
+    };
+    load_group(0);
+#pragma unroll
+    for (int j = 0; j < KN; j++) {
+        const int o = (tid + 256 * j) * 16, i = o / ROW, b = o % ROW;
+        if (i >= cnt || s_dst[i / kVBlock] < 0) continue;
+        *reinterpret_cast<uint4 *>(kv_head(c, s_dst[i / kVBlock], h) + (int64_t)((i0 + i) & pmask) * ROW + b) = kw[j];
+    }
+    uint32_t out[ON][4];
+#pragma unroll
+    for (int j = 0; j < ON; j++) out[j][0] = out[j][1] = out[j][2] = out[j][3] = 0;
+    for (int g0 = 0; g0 < blocks; g0 += GROUP) {
+        if (g0 > 0) load_group(g0);
+#pragma unroll
+        for (int k = 0; k < GROUP; k++) {
+#pragma unroll
+            for (int j = 0; j < VN; j++) {
+                const int p = tid + 256 * j;  // SZ 2: half of a column; SZ 1: a column
+                if (p >= VP) continue;
+                const uint4 w = vw[k][j];
                 if constexpr (SZ == 2) {
-                    const uint32_t x = p < 4 ? (p < 2 ? wd[0] : wd[1]) : (p < 6 ? wd[2] : wd[3]);
-                    reinterpret_cast<uint16_t *>(s_v)[d * kVBlock + i] = (uint16_t)(x >> (16 * (p & 1)));
+                    uint2 *at = reinterpret_cast<uint2 *>(s_v + (k * HD + p / 2) * PAD + 16 * (p % 2));
+                    at[0] = make_uint2(w.x, w.y);
+                    at[1] = make_uint2(w.z, w.w);
                 } else {
-                    const uint32_t x = p < 8 ? (p < 4 ? wd[0] : wd[1]) : (p < 12 ? wd[2] : wd[3]);
-                    s_v[d * kVBlock + i] = (uint8_t)(x >> (8 * (p & 3)));
+                    uint32_t *at = reinterpret_cast<uint32_t *>(s_v + (k * HD + p) * PAD);
+                    at[0] = w.x, at[1] = w.y, at[2] = w.z, at[3] = w.w;
                 }
             }
         }
-        a = z;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < ON; j++) {
+            const int u = tid + 256 * j, d = u % HD, i = u / HD * PER;  // column, first position
+            if (u >= OUT) continue;
+#pragma unroll
+            for (int x = 0; x < PER; x++) {
+                const int k = s_ord[i + x] - g0;
+                if (i + x < cnt && k >= 0 && k < GROUP) {
+                    const Val *col = reinterpret_cast<const Val *>(s_v + (k * HD + d) * PAD);
+                    out[j][x * SZ / 4] |= (uint32_t)col[s_src[i + x] % kVBlock] << (8 * SZ * (x % (4 / SZ)));
+                }
+            }
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int o = tid * 16; o < VB; o += 256 * 16) *reinterpret_cast<uint4 *>(vdst + o) = *reinterpret_cast<const uint4 *>(s_v + o);
-    if (SZ == 1 && tid < 2 * cnt) {
-        const int i = tid % cnt, which = tid / cnt;
-        float f = 0.f;
-        if (s_page[i] >= 0)
-            f = reinterpret_cast<const float *>(kv_head(c, s_page[i], h) + 2 * page_size * HD)[which * page_size + (s_src[i] & (page_size - 1))];
-        reinterpret_cast<float *>(dst + 2 * page_size * HD)[which * page_size + slot0 + i] = f;
+#pragma unroll
+    for (int j = 0; j < ON; j++) {
+        const int u = tid + 256 * j, d = u % HD, i = u / HD * PER;
+        if (u >= OUT || i >= cnt || s_dst[i / kVBlock] < 0) continue;
+        const int slot = (i0 + i) & pmask;
+        uint8_t *dst = kv_head(c, s_dst[i / kVBlock], h) + page_size * ROW + (int64_t)(slot / kVBlock) * VB + (d * kVBlock + slot % kVBlock) * SZ;
+        if (i + PER <= cnt) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
+        } else {  // positions past the new length stay as they were
+#pragma unroll
+            for (int x = 0; x < PER; x++)
+                if (i + x < cnt) reinterpret_cast<Val *>(dst)[x] = (Val)(out[j][x * SZ / 4] >> (8 * SZ * (x % (4 / SZ))));
+        }
     }
+    if (SZ == 1 && tid < 2 * kMove) {
+        const int i = tid % kMove, which = tid / kMove;
+        if (i < cnt && s_dst[i / kVBlock] >= 0) {
+            float f = 0.f;
+            if (s_page[i] >= 0)
+                f = reinterpret_cast<const float *>(kv_head(c, s_page[i], h) + 2 * page_size * HD)[which * page_size + (s_src[i] & pmask)];
+            reinterpret_cast<float *>(kv_head(c, s_dst[i / kVBlock], h) + 2 * page_size * HD)[which * page_size + ((i0 + i) & pmask)] = f;
+        }
+    }
+}
+
+template <int HD, int ROWS>
+hipError_t append_rows(int type, const KvArgs &c, int64_t n, const int32_t *start, const float *k,
+                       int64_t ldk, const float *v, int64_t ldv, hipStream_t s) {
+    const dim3 grid((uint32_t)((n + ROWS - 1) / ROWS), c.n_kv);
+    if (type == kKvF16)
+        return launch_main(kv_append<kKvF16, HD, ROWS>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
+    if (type == kKvBF16)
+        return launch_main(kv_append<kKvBF16, HD, ROWS>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
+    return launch_main(kv_append<kKvI8, HD, ROWS>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
 }
 
 template <int HD>
 hipError_t append_hd(int type, const KvArgs &c, int64_t n, const int32_t *start, const float *k,
                      int64_t ldk, const float *v, int64_t ldv, hipStream_t s) {
-    const dim3 grid((uint32_t)((n + kAppendRows - 1) / kAppendRows), c.n_kv);
-    if (type == kKvF16)
-        return launch_main(kv_append<kKvF16, HD>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
-    if (type == kKvBF16)
-        return launch_main(kv_append<kKvBF16, HD>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
-    return launch_main(kv_append<kKvI8, HD>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
+    if constexpr (HD <= 128) {
+        // 64 rows a workgroup once that still gives two per compute unit
+        if (n * c.n_kv >= 64 * 512) return append_rows<HD, 64>(type, c, n, start, k, ldk, v, ldv, s);
+    }
+    return append_rows<HD, 16>(type, c, n, start, k, ldk, v, ldv, s);
 }
 
 template <int HD>
 hipError_t move_hd(int type, const KvArgs &c, const EvictArgs &e, hipStream_t s) {
-    const dim3 grid((e.keep + kVBlock - 1) / kVBlock, c.n_kv, c.n_seq);
+    const dim3 grid((e.keep + kMove - 1) / kMove, c.n_kv, c.n_seq);
     if (type == kKvI8) return launch_main(kv_evict_move<1, HD>, grid, dim3(256), 0, s, c, e);
     return launch_main(kv_evict_move<2, HD>, grid, dim3(256), 0, s, c, e);
 }

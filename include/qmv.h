@@ -432,7 +432,8 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * [n_seq * n][n_heads * head_dim].  n_heads a multiple of n_kv_heads.
  * max_len: the longest seq_len of the call (longer ones are taken as max_len,
  * or as what a table row addresses); it sizes the workspace and decides into
- * how many pieces the length is split.  With acc, n_seq * n * n_heads < 2^24.
+ * how many pieces the length is split.  With acc, n_seq * n * n_heads +
+ * n_seq * n_kv_heads * ceil(max_len / 256) < 2^24.
  * acc: NULL, or f32 [n_seq][n_kv_heads][ld_acc], ld_acc >= max_len: position
  * t of key-value head h gets, added, the weights w_t of the n tokens and of the
  * query heads that share h (what qmv_kv_evict ranks by).
@@ -441,7 +442,7 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * f32.  Results do not depend on anything but the arguments.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is
  * 0), 16-byte aligned, no initial contents needed.  One launch, a second one
- * to join the pieces when the length is split, a third for acc. */
+ * to join the pieces when the length is split or acc is given. */
 qmv_status qmv_attn_decode(const qmv_kv_cache *cache, int32_t n, int32_t n_heads, const float *q,
                            int64_t ldq, float scale, int32_t window, int32_t sinks, float *out,
                            int64_t max_len, float *acc, int64_t ld_acc, void *workspace,

@@ -167,6 +167,23 @@ def test_append_even_rows(t):
     assert np.array_equal(d.pool(), c.pool)
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,kv,page", [(64, 8, 64), (96, 9, 16), (128, 8, 32)])
+def test_append_many_rows(t, hd, kv, page):
+    """Long prompts: runs of 8 positions, cut by the sequences' and the workgroups' borders."""
+    lens = [2000, 5, 1203, 64, 1000]
+    news = [1997, 1, 1203, 0, 997]
+    c, rng = make_cache(t, kv, hd, page, lens, 13)
+    c.table[2, 300 // page] = -1
+    d = Dev(c)
+    start = (1 + np.concatenate([[0], np.cumsum(news)])).astype(np.int32)
+    n = int(start[-1]) + 2
+    k, v = (rng.standard_normal((n, kv, hd), dtype=np.float32) for _ in range(2))
+    q.qmv_kv_append(d.h, n, dev(k), dev(v), start=dev(start))
+    c.append(start, k, v)
+    assert np.array_equal(d.pool(), c.pool)
+
+
 # ---- decode -----------------------------------------------------------------
 
 @pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
@@ -375,6 +392,14 @@ def test_evict_scores(case):
          "special": rng.choice([np.inf, -np.inf, np.nan, 0.5, 1e-40], (1, kv, n)),
          "tiny": np.float32(1) + rng.integers(0, 40, (1, kv, n)).astype(np.float32) * np.float32(2.0 ** -23)}[case]
     run_evict(c, 1203, 4, 100, x.astype(np.float32))
+
+
+@pytest.mark.parametrize("n,keep", [(8192, 8000), (8193, 300), (20011, 15000)])
+def test_evict_long(n, keep):
+    """More positions than a workgroup ranks at a time."""
+    c, rng = make_cache("bf16", 1, 64, 64, [n, 100], 44, spare=2 * -(-keep // 64))
+    x = np.round(rng.random((2, 1, n + 3), dtype=np.float32) * 500)      # many equal scores
+    run_evict(c, keep, 4, 128, x)
 
 
 def test_evict_holes():
