@@ -18,7 +18,7 @@ namespace {
 // of one column next to each other: a thread gathers 8 positions of a column
 // and stores them at once where the workgroup's rows cover all 8, else one by
 // one.  Bound by the f32 reads, or for few rows by latency: 16 rows keep more
-// workgroups in flight, 64 leave fewer partly covered runs.
+// workgroups in flight, 32 leave fewer partly covered runs.
 template <int TYPE>
 __device__ __forceinline__ uint32_t kv_round(float x) {
     if constexpr (TYPE == kKvF16) {
@@ -203,24 +203,33 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int3
 }
 
 // ---- eviction: choosing -------------------------------------------------------
-// One workgroup per sequence and key-value head.  A thread has 8 consecutive
-// positions (up to 8192 a workgroup at a time; with no more the keys stay in
-// registers).  The m-th largest score of the middle positions is found by four
-// 8-bit radix passes over an order-preserving integer key (counts in LDS),
-// then prefix sums over the threads place the kept positions in order; among
-// equal scores at the border the lowest positions are kept.  Bound by latency:
-// three barriers a pass.
+// One workgroup per sequence and key-value head, 1024 PER positions at a time,
+// PER a thread (thread t has t, t + 1024, ...: neighbouring lanes read
+// neighbouring scores; with no more positions than that they stay in registers).  The
+// m-th largest score of the middle positions is found by four 8-bit radix
+// passes over an order-preserving integer key (counts in LDS), then counts per
+// wave and step, one prefix sum over them and the lanes' ballots place the
+// kept positions in order; among equal scores at the border the lowest
+// positions are kept.  Bound by latency: three barriers a pass.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
-constexpr int kSelPer = 8;                            // positions a thread
-constexpr int kSelStep = kSelThreads * kSelPer;
+
+// 16 bytes that are read once and not again (the old pages are given back).
+__device__ __forceinline__ uint4 load_once(const uint8_t *p) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
 
 __device__ __forceinline__ uint32_t score_key(float v) {
     if (v != v) return 0xFFFFFFFFu;   // NaN ranks above everything
     return float_key(v + 0.f);        // -0 counts as +0
 }
 
+template <int PER>
 __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictArgs e) {
+    constexpr int STEP = kSelThreads * PER;
+    constexpr int COUNTS = PER * kSelWaves, EACH = (COUNTS + 63) / 64;  // counts, and a lane's share
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
     const int len = kv_len(c, s, e.limit);
@@ -244,20 +253,16 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
     const int lo = e.first, hi = len - e.recent;   // candidates: lo <= position < hi
     const int m = e.keep - e.first - e.recent;     // of which m stay, 0 <= m < hi - lo
 
-    uint32_t key[kSelPer];
+    float f[PER];  // the thread's scores, and their keys
+    uint32_t key[PER];
     auto load_keys = [&](int base) {
-        const int p0 = base + tid * kSelPer;
-        float f[kSelPer];
-        if (p0 + kSelPer <= len) {
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(acc + p0);
-            const float4 a = __builtin_bit_cast(float4, load16(src)), b = __builtin_bit_cast(float4, load16(src + 16));
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
 #pragma unroll
-            for (int j = 0; j < kSelPer; j++) f[j] = p0 + j < len ? acc[p0 + j] : 0.f;
+        for (int j = 0; j < PER; j++) {
+            const int i = base + j * kSelThreads + tid;
+            f[j] = i < len ? acc[i] : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kSelPer; j++) key[j] = score_key(f[j]);
+        for (int j = 0; j < PER; j++) key[j] = score_key(f[j]);
     };
     load_keys(0);
 
@@ -270,12 +275,13 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
         for (int shift = 24; shift >= 0; shift -= 8) {
             if (tid < 256) hist[tid] = 0;
             __syncthreads();
-            for (int base = 0; base < len; base += kSelStep) {
-                if (len > kSelStep) load_keys(base);
-                const int p0 = base + tid * kSelPer;
+            for (int base = 0; base < len; base += STEP) {
+                if (len > STEP) load_keys(base);
 #pragma unroll
-                for (int j = 0; j < kSelPer; j++)
-                    if (p0 + j >= lo && p0 + j < hi && (key[j] & mask) == prefix) atomicAdd(&hist[(key[j] >> shift) & 255], 1);
+                for (int j = 0; j < PER; j++) {
+                    const int i = base + j * kSelThreads + tid;
+                    if (i >= lo && i < hi && (key[j] & mask) == prefix) atomicAdd(&hist[(key[j] >> shift) & 255], 1);
+                }
             }
             __syncthreads();
             if (wave == 0) {
@@ -304,55 +310,66 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
     }
     // kept: everything protected, every key above `prefix`, and the first
     // `left` candidates equal to it
-    __shared__ int w_ties[kSelWaves], w_kept[kSelWaves];
-    auto before = [&](int own, int *w_sum, int *all) {  // sum of the earlier threads' counts
-        int upto = own;
-        for (int off = 1; off < 64; off <<= 1) {
-            const int x = __shfl_up(upto, off);
-            if (lane >= off) upto += x;
+    __shared__ int s_cnt[2][EACH * 64], s_all[2];
+    // exclusive prefix sum of the counts, by wave 0
+    auto scan = [&](int which) {
+        if (wave == 0) {
+            int own[EACH], all = 0;
+#pragma unroll
+            for (int j = 0; j < EACH; j++) all += own[j] = lane * EACH + j < COUNTS ? s_cnt[which][lane * EACH + j] : 0;
+            int upto = all;
+            for (int off = 1; off < 64; off <<= 1) {
+                const int x = __shfl_up(upto, off);
+                if (lane >= off) upto += x;
+            }
+            int at = upto - all;
+#pragma unroll
+            for (int j = 0; j < EACH; j++) {
+                s_cnt[which][lane * EACH + j] = at;
+                at += own[j];
+            }
+            if (lane == 63) s_all[which] = upto;
         }
-        if (lane == 63) w_sum[wave] = upto;
-        __syncthreads();
-        int r = upto - own, sum = 0;
-        for (int w = 0; w < kSelWaves; w++) {
-            if (w < wave) r += w_sum[w];
-            sum += w_sum[w];
-        }
-        *all = sum;
-        return r;
     };
+    const uint64_t below = (1ull << lane) - 1;
     int ties_before = 0, kept_before = 0;
-    for (int base = 0; base < len; base += kSelStep) {
-        if (len > kSelStep) load_keys(base);
-        const int p0 = base + tid * kSelPer;
+    for (int base = 0; base < len; base += STEP) {
+        if (len > STEP) load_keys(base);
         uint32_t sure = 0, tie = 0;
 #pragma unroll
-        for (int j = 0; j < kSelPer; j++) {
-            const int i = p0 + j;
-            if (i >= len) continue;
-            if (i < lo || i >= hi || (m > 0 && key[j] > prefix)) sure |= 1u << j;
-            else if (m > 0 && key[j] == prefix) tie |= 1u << j;
+        for (int j = 0; j < PER; j++) {
+            const int i = base + j * kSelThreads + tid;
+            const bool mid = i >= lo && i < hi;
+            if (i < len && (!mid || (m > 0 && key[j] > prefix))) sure |= 1u << j;
+            if (mid && m > 0 && key[j] == prefix) tie |= 1u << j;
+            const uint64_t b = __ballot((tie >> j) & 1);
+            if (lane == 0) s_cnt[0][j * kSelWaves + wave] = (int)__popcll(b);
         }
-        int all_ties, all_kept;
-        int rank = ties_before + before(__popc(tie), w_ties, &all_ties);
+        __syncthreads();
+        scan(0);
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kSelPer; j++)
-            if ((tie >> j) & 1) {
-                if (rank < left) sure |= 1u << j;
-                rank++;
-            }
-        int at = kept_before + before(__popc(sure), w_kept, &all_kept);
+        for (int j = 0; j < PER; j++) {
+            const uint64_t b = __ballot((tie >> j) & 1);
+            const int rank = ties_before + s_cnt[0][j * kSelWaves + wave] + (int)__popcll(b & below);
+            if (((tie >> j) & 1) && rank < left) sure |= 1u << j;
+            const uint64_t k = __ballot((sure >> j) & 1);
+            if (lane == 0) s_cnt[1][j * kSelWaves + wave] = (int)__popcll(k);
+        }
+        __syncthreads();
+        scan(1);
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kSelPer; j++)
-            if ((sure >> j) & 1) {
-                if (at < e.keep) {
-                    kept[at] = p0 + j;
-                    acc_out[at] = acc[p0 + j];
-                }
-                at++;
+        for (int j = 0; j < PER; j++) {
+            const uint64_t k = __ballot((sure >> j) & 1);
+            const int at = kept_before + s_cnt[1][j * kSelWaves + wave] + (int)__popcll(k & below);
+            if (((sure >> j) & 1) && at < e.keep) {
+                kept[at] = base + j * kSelThreads + tid;
+                acc_out[at] = f[j];
             }
-        ties_before += all_ties;
-        kept_before += all_kept;
+        }
+        ties_before += s_all[0];
+        kept_before += s_all[1];
         __syncthreads();
     }
 }
@@ -428,7 +445,7 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
         const int o = (tid + 256 * j) * 16, i = o / ROW, b = o % ROW;
         kw[j] = make_uint4(0, 0, 0, 0);
         if (i < cnt && s_page[i] >= 0)
-            kw[j] = *reinterpret_cast<const uint4 *>(kv_head(c, s_page[i], h) + (int64_t)(s_src[i] & pmask) * ROW + b);
+            kw[j] = load_once(kv_head(c, s_page[i], h) + (int64_t)(s_src[i] & pmask) * ROW + b);
     }
     const int blocks = s_blocks;
     uint4 vw[GROUP][VN];
@@ -443,7 +460,7 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
             for (int j = 0; j < VN; j++) {
                 const int p = tid + 256 * j;
                 vw[k][j] = make_uint4(0, 0, 0, 0);
-                if (page >= 0 && p < VP) vw[k][j] = *reinterpret_cast<const uint4 *>(src + p * 16);
+                if (page >= 0 && p < VP) vw[k][j] = load_once(src + p * 16);
             }
         }
     };
@@ -531,10 +548,9 @@ hipError_t append_rows(int type, const KvArgs &c, int64_t n, const int32_t *star
 template <int HD>
 hipError_t append_hd(int type, const KvArgs &c, int64_t n, const int32_t *start, const float *k,
                      int64_t ldk, const float *v, int64_t ldv, hipStream_t s) {
-    if constexpr (HD <= 128) {
-        // 64 rows a workgroup once that still gives two per compute unit
-        if (n * c.n_kv >= 64 * 512) return append_rows<HD, 64>(type, c, n, start, k, ldk, v, ldv, s);
-    }
+    // 32 rows once that still gives two workgroups per compute unit (6808 rows
+    // of 8 heads of 128: 20.8 us, with 16 rows 23.5, with 64 rows 23.6)
+    if (n * c.n_kv >= 32 * 512) return append_rows<HD, 32>(type, c, n, start, k, ldk, v, ldv, s);
     return append_rows<HD, 16>(type, c, n, start, k, ldk, v, ldv, s);
 }
 
@@ -560,7 +576,11 @@ hipError_t launch_kv_append(int type, const KvArgs &c, int64_t n, const int32_t 
 }
 
 hipError_t launch_kv_evict(int type, const KvArgs &c, const EvictArgs &e, hipStream_t s) {
-    hipError_t r = launch_aux(kv_evict_select, dim3(c.n_kv, c.n_seq), dim3(kSelThreads), 0, s, c, e);
+    const dim3 grid(c.n_kv, c.n_seq);
+    // short sequences take the short code (1001 positions: 8.9 -> 6.3 us)
+    hipError_t r = e.limit <= kSelThreads
+                       ? launch_aux(kv_evict_select<1>, grid, dim3(kSelThreads), 0, s, c, e)
+                       : launch_aux(kv_evict_select<8>, grid, dim3(kSelThreads), 0, s, c, e);
     if (r != hipSuccess) return r;
     switch (c.hd) {
     case 64: return move_hd<64>(type, c, e, s);
