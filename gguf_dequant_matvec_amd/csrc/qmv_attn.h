@@ -24,7 +24,7 @@ constexpr float kNoMax = -1e30f;  // running maximum before any visible position
 
 // 8-bit V rows carry their scale into the probabilities; `vmul`, a power of
 // two, keeps the largest scale so far at most 1.  Before the first row:
-constexpr float kVmulNone = 0x1p100f;
+constexpr float kVmulNone = 0x1p100f, kVlogNone = 100.f;
 
 // Matrix-core operands of a cache type.  f32 queries and probabilities are
 // split into 16-bit pieces whose sum is the f32 value to 2^-22 or better (two
@@ -69,6 +69,14 @@ template <int TYPE>
 struct KvOp { typedef OpF16 Op; };
 template <>
 struct KvOp<kKvBF16> { typedef OpBF16 Op; };
+
+// The factor of a row's logits, given the power of two its query was scaled
+// by: positive, so that the maximum can be taken before it (and never 0, as a
+// masked -inf has to stay one).
+__device__ __forceinline__ float logit_factor(float scale_log2, int sh) {
+    const float f = ldexpf(scale_log2, -sh);
+    return f == 0.f ? 1.17549435e-38f : f;
+}
 
 // A 16-byte load; NT for data that one workgroup reads once.
 template <bool NT>

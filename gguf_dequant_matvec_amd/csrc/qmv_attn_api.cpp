@@ -99,7 +99,11 @@ static qmv_status check_attn(const qmv_kv_cache *c, int32_t n_heads, int64_t max
     return QMV_OK;
 }
 
-static void fill_attn(AttnArgs &a, const AttnPlan &p, void *ws) {
+static void fill_attn(AttnArgs &a, const AttnPlan &p, float scale, void *ws) {
+    // the kernels want a positive factor; the sign goes to the queries
+    const float f = (scale < 0.f ? -scale : scale) * 1.4426950408889634f;
+    a.scale_log2 = scale == 0.f ? 1.f : f;
+    a.q_sign = scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f;
     a.group = a.n_heads / a.c.n_kv;
     a.tiles = p.tiles;
     a.splits = p.splits;
@@ -159,8 +163,7 @@ qmv_status qmv_attn_decode(const qmv_kv_cache *cache, int32_t n, int32_t n_heads
     a.n_heads = n_heads;
     a.window = window;
     a.sinks = sinks;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    fill_attn(a, p, workspace);
+    fill_attn(a, p, scale, workspace);
     a.logits = (float *)((uint8_t *)workspace + p.logits_off);
     a.ld_logits = p.ld_logits;
     a.acc = acc;
@@ -214,8 +217,7 @@ qmv_status qmv_attn_prefill(const qmv_kv_cache *cache, int64_t n, const int32_t 
     a.n_heads = n_heads;
     a.window = window;
     a.sinks = sinks;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    fill_attn(a, p, workspace);
+    fill_attn(a, p, scale, workspace);
     return from_hip(launch_attn_prefill(cache->type, a, p, stream));
 }
 

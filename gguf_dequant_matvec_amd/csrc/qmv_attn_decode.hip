@@ -157,7 +157,9 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
     };
     float mrun[RT], lrun[RT];
     f32x4 o[RT][DT];
-    float vmul = kVmulNone;  // 8-bit: power of two that brings the row scales of V to at most 1
+    // 8-bit: power of two that brings the row scales of V to at most 1, its
+    // logarithm (it enters with the exponent) and its inverse
+    float vmul = kVmulNone, vlog = TYPE == kKvI8 ? kVlogNone : 0.f, vback = 1.f / kVmulNone;
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         mrun[rt] = kNoMax;
@@ -197,7 +199,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                 const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    f[t][e] = live ? w[e] : 0.f;
+                    f[t][e] = live ? w[e] * a.q_sign : 0.f;
                     big = fmaxf(big, fabsf(f[t][e]));
                 }
             }
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                     sh = sh > 100 ? 100 : sh;
                 }
             }
-            qscale[rt] = ldexpf(a.scale_log2, -sh);
+            qscale[rt] = logit_factor(a.scale_log2, sh);
     #pragma unroll
             for (int t = 0; t < KS; t++) {
     #pragma unroll
@@ -265,6 +267,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                     const float nm = ldexpf(1.f, -ex);
                     const float r = nm / vmul;
                     vmul = nm;
+                    vlog = (float)-ex;
+                    vback = ldexpf(1.f, ex);
     #pragma unroll
                     for (int rt = 0; rt < RT; rt++)
     #pragma unroll
@@ -290,7 +294,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                 float x[PER];
     #pragma unroll
                 for (int e = 0; e < PER; e++) {
-                    x[e] = sacc[rt][e >> 2][e & 3] * qscale[rt];
+                    x[e] = sacc[rt][e >> 2][e & 3];
                     if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
                     if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
                 }
@@ -300,12 +304,13 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                         float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0;
     #pragma unroll
                         for (int e = 0; e < PER; e += 4)
-                            *reinterpret_cast<float4 *>(lp + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                            *reinterpret_cast<float4 *>(lp + e) = make_float4(x[e] * qscale[rt], x[e + 1] * qscale[rt], x[e + 2] * qscale[rt], x[e + 3] * qscale[rt]);
                     }
                 }
                 float mx = x[0];
     #pragma unroll
                 for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
+                mx *= qscale[rt];
                 if (__any(mx > mrun[rt] + kSlack)) {
                     mx = fmaxf(mx, __shfl_xor(mx, 16));
                     mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -316,15 +321,15 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
     #pragma unroll
                     for (int t = 0; t < DT; t++) o[rt][t] *= r;
                 }
-                const float off = kBias - mrun[rt];
+                const float off = kBias - mrun[rt] + vlog;
                 float sum = 0.f;
     #pragma unroll
                 for (int e = 0; e < PER; e++) {
-                    x[e] = exp2_fast(x[e] + off);
+                    x[e] = exp2_fast(fmaf(x[e], qscale[rt], off));
                     sum += x[e];
-                    if constexpr (TYPE == kKvI8) x[e] *= vt.vs[e] * vmul;
+                    if constexpr (TYPE == kKvI8) x[e] *= vt.vs[e];
                 }
-                lrun[rt] += sum;
+                lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
     #pragma unroll
                 for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
             }
@@ -358,7 +363,6 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
         if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
     }
     __syncthreads();
-    const float back = 1.f / vmul;
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         float mm = kNoMax;
@@ -368,7 +372,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
         mrun[rt] = mm;
         lrun[rt] *= r;
         if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
-        const float ro = TYPE == kKvI8 ? r * back : r;
+        const float ro = TYPE == kKvI8 ? r * vback : r;
 #pragma unroll
         for (int t = 0; t < DT; t++) o[rt][t] *= ro;
     }

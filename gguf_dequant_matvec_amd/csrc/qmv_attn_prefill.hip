@@ -27,7 +27,8 @@ struct Lds {  // one buffer, bytes
     static constexpr int kRow = HD * 2 + 16;            // K row
     static constexpr int kV = kBK * kRow;               // V blocks
     static constexpr int kScale = kV + kBK * HD * 2;    // row scales of K, then of V
-    static constexpr int kBytes = kScale + 2 * kBK * 4;
+    static constexpr int kVmax = kScale + 2 * kBK * 4;  // largest row scale of V, one a block
+    static constexpr int kBytes = kVmax + 16;
     static constexpr int kOk = 2 * kBytes;              // per buffer: 4 flags, one a block
     static constexpr int kTotal = kOk + 32;
 };
@@ -95,8 +96,11 @@ struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
             }
         }
         if constexpr (TYPE == kKvI8) {
-            if (lane < 32)
-                reinterpret_cast<float *>(buf + Lds<HD>::kScale)[(lane >> 4) * kBK + 16 * w + (lane & 15)] = (lane & 15) < live ? sc : 0.f;
+            const float mine = (lane & 15) < live ? sc : 0.f;
+            if (lane < 32) reinterpret_cast<float *>(buf + Lds<HD>::kScale)[(lane >> 4) * kBK + 16 * w + (lane & 15)] = mine;
+            float big = mine < __builtin_inff() ? mine : 0.f;
+            for (int off = 8; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
+            if (lane == 16) reinterpret_cast<float *>(buf + Lds<HD>::kVmax)[w] = big;
         }
         if (lane == 0) flag[w] = ok;
     }
@@ -211,18 +215,19 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
                 sh = sh > 100 ? 100 : sh;
             }
         }
-        qscale = ldexpf(a.scale_log2, -sh);
+        qscale = logit_factor(a.scale_log2, sh);
 #pragma unroll
         for (int t = 0; t < KS; t++) {
             const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
             const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
             float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 8; e++) f[e] = live ? ldexpf(f[e], sh) : 0.f;
+            for (int e = 0; e < 8; e++) f[e] = live ? ldexpf(f[e] * a.q_sign, sh) : 0.f;
             split8<Op>(f, qf[t]);
         }
     }
-    float mrun = kNoMax, lrun = 0.f, vmul = kVmulNone;
+    float mrun = kNoMax, lrun = 0.f;
+    float vmul = kVmulNone, vlog = TYPE == kKvI8 ? kVlogNone : 0.f, vback = 1.f / kVmulNone;  // as in the decode kernel
     f32x16 o[DT];
 #pragma unroll
     for (int t = 0; t < DT; t++)
@@ -259,10 +264,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
                 for (int p = 0; p < NP; p++) sa = Op::mfma32(kx, as_vec<Vec>(qf[t][p]), sa);
             }
             float x[16];
-            float mx = -__builtin_inff(), vbig = 0.f;
+            float mx = -__builtin_inff();
             f32x4 vs[4];
 #pragma unroll
-            for (int e = 0; e < 16; e++) x[e] = sa[e] * qscale;
+            for (int e = 0; e < 16; e++) x[e] = sa[e];
             if constexpr (TYPE == kKvI8) {
 #pragma unroll
                 for (int u = 0; u < 4; u++) {
@@ -272,7 +277,6 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         x[4 * u + e] *= ks[e];
-                        vbig = fmaxf(vbig, fabsf(vs[u][e]));
                     }
                 }
             }
@@ -286,6 +290,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
             }
 #pragma unroll
             for (int e = 0; e < 16; e++) mx = fmaxf(mx, x[e]);
+            mx *= qscale;
             if (__any(mx > mrun + kSlack)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
                 const float mnew = fmaxf(mrun, mx);
@@ -296,26 +301,29 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
                 for (int t = 0; t < DT; t++) o[t] *= r;
             }
             if constexpr (TYPE == kKvI8) {
-                if (__any(vbig * vmul > 1.f && vbig < __builtin_inff())) {
-                    for (int off = 32; off; off >>= 1) vbig = fmaxf(vbig, __shfl_xor(vbig, off));
+                const f32x4 vm = *reinterpret_cast<const f32x4 *>(buf + Lds<HD>::kVmax);
+                const float vbig = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));  // the chunk's
+                if (vbig * vmul > 1.f) {
                     int ex = __builtin_amdgcn_frexp_expf(vbig);
                     ex = ex > 120 ? 120 : ex;
                     const float nm = ldexpf(1.f, -ex);
                     const float r = nm / vmul;
                     vmul = nm;
+                    vlog = (float)-ex;
+                    vback = ldexpf(1.f, ex);
 #pragma unroll
                     for (int t = 0; t < DT; t++) o[t] *= r;
                 }
             }
-            const float off = kBias - mrun;
+            const float off = kBias - mrun + vlog;
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e++) {
-                x[e] = exp2_fast(x[e] + off);
+                x[e] = exp2_fast(fmaf(x[e], qscale, off));
                 sum += x[e];
-                if constexpr (TYPE == kKvI8) x[e] *= vs[e >> 2][e & 3] * vmul;
+                if constexpr (TYPE == kKvI8) x[e] *= vs[e >> 2][e & 3];
             }
-            lrun += sum;
+            lrun += TYPE == kKvI8 ? sum * vback : sum;
             U128 pf[2][NP];
             split8<Op>(x, pf[0]);
             split8<Op>(x + 8, pf[1]);
@@ -338,7 +346,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
     lrun += __shfl_xor(lrun, 32);
     if (!live) return;
     const int64_t orow = row * a.n_heads + h * a.group + hg;
-    float mul = TYPE == kKvI8 ? 1.f / vmul : 1.f;
+    float mul = TYPE == kKvI8 ? vback : 1.f;
     float *dst;
     if (a.splits == 1) {
         mul = lrun == 0.f ? 0.f : mul / lrun;  // a row that sees nothing: zeros

@@ -83,7 +83,8 @@ struct AttnArgs {
     int32_t window, sinks;   // window 0: none
     int32_t limit;           // longest sequence (max_len, and what the table addresses)
     int32_t tiles, splits;
-    float scale_log2;        // scale * log2(e)
+    float scale_log2;        // |scale| * log2(e), not zero
+    float q_sign;            // what queries are multiplied by: the scale's sign (0 for scale 0)
     float2 *part_ml;         // [splits][part_rows] running maximum and sum
     float *part_o;           // [splits][part_rows][hd]
     int64_t part_rows;       // rows * n_heads; piece i of output row r is at i * part_rows + r

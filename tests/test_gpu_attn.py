@@ -258,6 +258,22 @@ def test_decode_query_range(t, size):
     close(host(out).reshape(want.shape), want, tol, f"query size {size}")
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-38])
+def test_scale_sign(t, scale):
+    """Any scale: negative, none, vanishing; in both calls."""
+    c, _ = make_cache(t, 1, 64, 16, [70], 30)
+    d = Dev(c)
+    qh = synth.normal(3, synth.T_X, (20, 2, 64), 1.0)
+    want, tol, _, _ = ref.attention(c, [0, 20], qh, float(np.float32(scale)), 80)
+    out = torch.empty(20, 128, device="cuda")
+    q.qmv_attn_prefill(d.h, 20, 2, dev(qh.reshape(20, -1)), scale, out, 80)
+    close(host(out).reshape(want.shape), want, tol, f"prefill scale {scale}")
+    out = torch.empty(16, 128, device="cuda")
+    q.qmv_attn_decode(d.h, 16, 2, dev(qh[4:].reshape(16, -1)), scale, out, 80)
+    close(host(out).reshape(16, 2, 64), want[4:], tol[4:], f"decode scale {scale}")
+
+
 @pytest.mark.parametrize("size", [1e-20, 1e-7, 3e4, 1e20])
 def test_decode_i8_value_range(size):
     """8-bit V rows of any scale, and of very different scales in one sequence."""
