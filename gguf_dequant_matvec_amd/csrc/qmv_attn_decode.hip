@@ -16,8 +16,8 @@
 //  - The softmax maximum is lazy: O and the sum are rescaled only when some
 //    logit exceeds the running maximum by 2^kSlack; the probabilities then
 //    are at most 2^(kBias + kSlack), which f16 pieces hold.
-// A wave takes every fourth chunk of its workgroup's piece of the length, the
-// four waves are joined through LDS, and the pieces by a second launch.
+// A wave takes every NW-th chunk of its workgroup's piece of the length, the NW
+// waves are joined through LDS, and the pieces by a second launch.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
 
@@ -25,7 +25,6 @@ namespace qmv {
 
 namespace {
 
-constexpr int kWaves = 4;
 
 template <int TYPE>
 constexpr int kChunk = TYPE == kKvI8 ? 64 : 32;  // positions a wave takes at a time (16 KB at 128 columns)
@@ -121,8 +120,8 @@ struct VTile {
     }
 };
 
-template <int TYPE, int HD, int RT, bool ACC>
-__global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
+template <int TYPE, int HD, int RT, int NW, bool ACC>
+__global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
     constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
@@ -176,8 +175,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
         bool ok = vpage >= 0;  // the lane group's positions are in a page (not a hole)
         kt.template load<NT>(c, h, ch.at(i), kpage, g, m);
         vt.template load<NT>(c, h, ch.at(i), vpage, g, m);
-        kpage = page_of(i + kWaves, m >> 2);
-        vpage = page_of(i + kWaves, g);
+        kpage = page_of(i + NW, m >> 2);
+        vpage = page_of(i + NW, g);
 
         // the rows
         int pos[RT];
@@ -224,8 +223,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
         }
 
         for (;;) {
-            const bool more = i + kWaves < end;
-            const int kpage2 = page_of(i + 2 * kWaves, m >> 2), vpage2 = page_of(i + 2 * kWaves, g);
+            const bool more = i + NW < end;
+            const int kpage2 = page_of(i + 2 * NW, m >> 2), vpage2 = page_of(i + 2 * NW, g);
             f32x4 sacc[RT][2 * SUB];
     #pragma unroll
             for (int rt = 0; rt < RT; rt++)
@@ -244,7 +243,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
             }
             // the K registers are free: the next chunk's K flies during the
             // softmax and the second product, its V during the next first one
-            if (more) kt.template load<NT>(c, h, ch.at(i + kWaves), kpage, g, m);
+            if (more) kt.template load<NT>(c, h, ch.at(i + NW), kpage, g, m);
 
             const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
             // a chunk that every row sees whole needs no masks
@@ -344,17 +343,17 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
                         for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
                 }
             }
-            if (more) vt.template load<NT>(c, h, ch.at(i + kWaves), vpage, g, m);
+            if (more) vt.template load<NT>(c, h, ch.at(i + NW), vpage, g, m);
             if (!more) break;
-            i += kWaves;
+            i += NW;
             ok = vpage >= 0;
             kpage = kpage2;
             vpage = vpage2;
         }
     }
 
-    // join the four waves: a common maximum, then the partial sums pairwise
-    __shared__ float s_m[kWaves][RT * 16], s_l[kWaves][RT * 16];
+    // join the waves: a common maximum, then the partial sums two by two
+    __shared__ float s_m[NW][RT * 16], s_l[NW][RT * 16];
     __shared__ f32x4 s_o[2][RT * DT * 64];
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
@@ -366,7 +365,7 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
 #pragma unroll
     for (int rt = 0; rt < RT; rt++) {
         float mm = kNoMax;
-        for (int w = 0; w < kWaves; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
+        for (int w = 0; w < NW; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
         // (a NaN maximum cannot be: fmaxf drops NaN; a NaN sum stays)
         const float r = exp2_fast(mrun[rt] - mm);
         mrun[rt] = mm;
@@ -376,19 +375,21 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
 #pragma unroll
         for (int t = 0; t < DT; t++) o[rt][t] *= ro;
     }
-    for (int half = 2; half; half >>= 1) {
-        if (wave >= half && wave < 2 * half) {
+    for (int from = NW - 2; from >= 0; from -= 2) {
+        // waves from, from + 1 add to the two before them; last 1 to 0
+        const int w0 = from > 0 ? from : 1, n_from = from > 0 ? 2 : 1, to = from > 0 ? from - 2 : 0;
+        if (wave >= w0 && wave < w0 + n_from) {
 #pragma unroll
             for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-                for (int t = 0; t < DT; t++) s_o[wave - half][(rt * DT + t) * 64 + lane] = o[rt][t];
+                for (int t = 0; t < DT; t++) s_o[wave - w0][(rt * DT + t) * 64 + lane] = o[rt][t];
         }
         __syncthreads();
-        if (wave < half) {
+        if (wave >= to && wave < to + n_from) {
 #pragma unroll
             for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-                for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave][(rt * DT + t) * 64 + lane];
+                for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave - to][(rt * DT + t) * 64 + lane];
         }
         __syncthreads();
     }
@@ -398,7 +399,8 @@ __global__ __launch_bounds__(kWaves * 64) void attn_decode(AttnArgs a) {
     for (int rt = 0; rt < RT; rt++) {
         const int rr = r0 + rt * 16 + m;
         if (rr >= nrows) continue;
-        const float l = (s_l[0][rt * 16 + m] + s_l[1][rt * 16 + m]) + (s_l[2][rt * 16 + m] + s_l[3][rt * 16 + m]);
+        float l = 0.f;
+        for (int w = 0; w < NW; w++) l += s_l[w][rt * 16 + m];
         float *dst;
         float mul = 1.f;
         if (direct) {
@@ -478,14 +480,14 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     if (key < len) a.acc[head * a.ld_acc + key] += sum;
 }
 
-template <int TYPE, int HD, int RT>
+template <int TYPE, int HD, int RT, int NW>
 hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     const dim3 grid(p.splits, a.c.n_kv * p.tiles, a.c.n_seq);
     hipError_t e;
     if (a.acc)
-        e = launch_main(attn_decode<TYPE, HD, RT, true>, grid, dim3(kWaves * 64), 0, s, a);
+        e = launch_main(attn_decode<TYPE, HD, RT, NW, true>, grid, dim3(NW * 64), 0, s, a);
     else
-        e = launch_main(attn_decode<TYPE, HD, RT, false>, grid, dim3(kWaves * 64), 0, s, a);
+        e = launch_main(attn_decode<TYPE, HD, RT, NW, false>, grid, dim3(NW * 64), 0, s, a);
     if (e != hipSuccess) return e;
     if (a.acc) {
         const int64_t blocks = p.part_rows + (int64_t)a.c.n_seq * a.c.n_kv * ((a.limit + 255) / 256);
@@ -494,9 +496,28 @@ hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     return p.splits > 1 ? launch_attn_join(a, s) : hipSuccess;
 }
 
+// Whether the 256 registers that eight waves leave each lane hold the kernel's
+// operands; four waves have 512.
+constexpr bool eight_fit(int type, int hd, int rt) {
+    return rt == 1 ? hd <= 128 : hd == 64 || (hd == 96 && type != kKvI8);
+}
+
+template <int TYPE, int HD, int RT>
+hipError_t launch_rt(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    // 32-row tiles take eight waves wherever they fit, 16-row tiles either
+    if constexpr (eight_fit(TYPE, HD, RT)) {
+        if (RT == 2 || p.waves == 8) return launch_typed<TYPE, HD, RT, 8>(a, p, s);
+    }
+    if constexpr (RT == 1 || !eight_fit(TYPE, HD, RT)) return launch_typed<TYPE, HD, RT, 4>(a, p, s);
+    return hipErrorInvalidValue;
+}
+
 template <int TYPE, int HD>
 hipError_t launch_hd(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
-    return p.rt == 2 ? launch_typed<TYPE, HD, 2>(a, p, s) : launch_typed<TYPE, HD, 1>(a, p, s);
+    if constexpr (HD <= 128) {
+        if (p.rt == 2) return launch_rt<TYPE, HD, 2>(a, p, s);
+    }
+    return launch_rt<TYPE, HD, 1>(a, p, s);
 }
 
 template <int TYPE>
@@ -505,7 +526,7 @@ hipError_t launch_type(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     case 64: return launch_hd<TYPE, 64>(a, p, s);
     case 96: return launch_hd<TYPE, 96>(a, p, s);
     case 128: return launch_hd<TYPE, 128>(a, p, s);
-    case 256: return launch_typed<TYPE, 256, 1>(a, p, s);
+    case 256: return launch_hd<TYPE, 256>(a, p, s);
     default: return hipErrorInvalidValue;
     }
 }
@@ -530,16 +551,20 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
     }
     const int64_t chunks = (most + ck - 1) / ck;
     const int64_t base = n_seq * n_kv * p.tiles;
-    // Two workgroups fit a compute unit of 256.  Sequences that may differ in
-    // length get twice that, for balance (the ragged batch above: 134 us with
-    // 512, 131 with 1024); one sequence, a window or a 32-row tile does not
-    // (131071 8-bit positions: 60 against 64 us; the drafted tokens: 26
-    // against 34 us).
-    const int64_t want = n_seq == 1 || window > 0 || p.rt == 2 ? 512 : 1024;
+    // Eight waves fit a compute unit of 256: two workgroups of four.  Sequences
+    // that may differ in length get twice that, for balance (the ragged batch
+    // above: 134 us with 512, 131 with 1024); one sequence or a window does
+    // not (131071 8-bit positions: 60 against 64 us), and tiles of 32 rows
+    // take one workgroup, of eight waves (the drafted tokens: 24 us against 26
+    // with 512 of four and 34 with 1024) or, where registers say so, of four.
+    const int64_t want = p.rt == 2 ? 256 : n_seq == 1 || window > 0 ? 512 : 1024;
     int64_t splits = (want + base - 1) / base;
-    if (splits > chunks / 8) splits = chunks / 8;    // at least two chunks per wave
+    if (splits > chunks / 8) splits = chunks / 8;    // at least a chunk, with four waves two, per wave
     if (splits > 128) splits = 128;
     p.splits = splits < 1 ? 1 : (int)splits;
+    // a launch of few, unsplit workgroups is a chain of latencies: eight waves
+    // halve the chunks in it (301 positions, 3 heads: 7.3 -> 6.6 us)
+    p.waves = eight_fit(type, hd, p.rt) && (p.rt == 2 || (p.splits == 1 && base <= 256)) ? 8 : 4;
     size_t at = 0;
     if (p.splits > 1 || with_acc) {
         p.ml_off = at;

@@ -11,8 +11,9 @@
 // The products are S^T = K Q^T and O^T = V^T P^T: K rows lie in LDS in the
 // order in which the 32x32 operand takes them so that each lane's
 // accumulators are 8 consecutive positions of its query, the operand layout
-// of P, and no value moves between lanes.  K rows are padded by 16 bytes and V
-// keeps the cache's block layout; both are read without bank conflicts.
+// of P, and no value moves between lanes.  K rows are swizzled by 16-byte
+// pieces and V keeps the cache's block layout; both are read without bank
+// conflicts.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
 
@@ -24,90 +25,120 @@ constexpr int kBM = 128, kBK = 64;
 
 template <int HD>
 struct Lds {  // one buffer, bytes
-    static constexpr int kRow = HD * 2 + 16;            // K row
+    static constexpr int kRow = HD * 2;                 // K row
     static constexpr int kV = kBK * kRow;               // V blocks
-    static constexpr int kScale = kV + kBK * HD * 2;    // row scales of K, then of V
+    static constexpr int kScale = kV + kBK * HD * 2;    // 8-bit: row scales of K, then of V
     static constexpr int kVmax = kScale + 2 * kBK * 4;  // largest row scale of V, one a block
-    static constexpr int kBytes = kVmax + 16;
-    static constexpr int kOk = 2 * kBytes;              // per buffer: 4 flags, one a block
-    static constexpr int kTotal = kOk + 32;
+    static constexpr int kBytes(int type) { return type == kKvI8 ? kVmax + 16 : kScale; }
+    static constexpr int kOk(int type) { return 2 * kBytes(type); }  // per buffer: 4 flags, one a block
+    static constexpr int kTotal(int type) { return kOk(type) + 32; }
 };
 
-// LDS row of position j (0..31) of a half chunk: operand row 8 b + 4 h + i
-// holds position 16 (b / 2) + 8 h + 4 (b % 2) + i.
-__device__ __forceinline__ int krow(int j) { return (j & 16) | ((j & 4) << 1) | ((j & 8) >> 1) | (j & 3); }
+// K rows lie in LDS in the order of the 32x32 operand, row 8 b + 4 h + i of a
+// half chunk being position 16 (b / 2) + 8 h + 4 (b % 2) + i: bits 2 and 3
+// change places, both ways.
+__device__ __forceinline__ int krow(int j) { return (j & ~12) | ((j & 4) << 1) | ((j & 8) >> 1); }
+// LDS delivers 256 bytes a cycle, 16 bytes to each of 16 lanes, so the lanes
+// of 16 neighbouring rows (columns of V) that read the same piece must find it
+// in 16 different places modulo 256 bytes.  Place of piece p in K row r:
+template <int HD>
+__device__ __forceinline__ int kslot(int r, int p) {
+    return HD == 64 ? p ^ ((r >> 1) & 7) : HD == 96 ? p ^ ((r >> 2) & 3) : p ^ (r & 15);
+}
+// ... and of half p of column d of a V block:
+__device__ __forceinline__ int vslot(int d, int p) { return 2 * d + (p ^ ((d >> 3) & 1)); }
 
+// A wave's 16 positions of a chunk on their way to LDS.  f16 and bf16 values
+// go straight from memory to LDS (each lane names the piece whose place its
+// slot of the wave's run of 1 KB is), 8-bit codes are widened on the way.
 template <int TYPE, int HD>
-struct Stage {  // a wave's 16 positions of a chunk on their way to LDS
+struct Stage {
     static constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
     static constexpr int PIECES = HD * SZ;  // 16-byte pieces of 16 K rows, and of a V block
     static constexpr int N = (PIECES + 63) / 64;
-    u32x4 k[N], v[N];
+    u32x4 k[TYPE == kKvI8 ? N : 1], v[TYPE == kKvI8 ? N : 1];
     float sc;
     bool ok;
 
-    __device__ __forceinline__ void load(const KvArgs &c, int h, int page, int pos, int lane) {
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int page, int pos, uint8_t *buf, int w, int lane) {
         ok = page >= 0;
         const uint8_t *base = kv_head(c, page < 0 ? 0 : page, h);
         const int slot = pos & ((1 << c.page_shift) - 1);
         const uint8_t *kp = base + (int64_t)slot * (HD * SZ);
         const uint8_t *vp = base + ((int64_t)(HD * SZ) << c.page_shift) + (int64_t)slot * (HD * SZ);
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            if (PIECES % 64 == 0 || lane + 64 * i < PIECES) {
-                k[i] = *reinterpret_cast<const u32x4 *>(kp + (lane + 64 * i) * 16);
-                v[i] = *reinterpret_cast<const u32x4 *>(vp + (lane + 64 * i) * 16);
-            }
-        }
         if constexpr (TYPE == kKvI8) {
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                if (PIECES % 64 == 0 || lane + 64 * i < PIECES) {
+                    k[i] = *reinterpret_cast<const u32x4 *>(kp + (lane + 64 * i) * 16);
+                    v[i] = *reinterpret_cast<const u32x4 *>(vp + (lane + 64 * i) * 16);
+                }
+            }
             const float *s = reinterpret_cast<const float *>(base + ((int64_t)(2 * HD) << c.page_shift));
             sc = lane < 32 ? s[((lane >> 4) << c.page_shift) + slot + (lane & 15)] : 0.f;
+        } else {
+            constexpr int PPR = HD / 8;  // pieces of a row
+            uint8_t *kd = buf + 16 * w * Lds<HD>::kRow, *vd = buf + Lds<HD>::kV + w * HD * 32;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int q = lane + 64 * i, row = q / PPR;
+                const int from = krow(row) * (HD * 2) + kslot<HD>(row, q % PPR) * 16;
+                to_lds(kp + from, kd + i * 1024);
+                to_lds(vp + vslot(q / 2, q % 2) * 16, vd + i * 1024);
+            }
         }
     }
     // live: positions of the 16 that some row may see; V of the others is zero
     __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live) const {
         if (!ok) live = 0;
-        // dword j of a V piece: positions 2 j, 2 j + 1 of its 8 (an odd piece has the later 8)
-        uint32_t mask[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int e0 = live - 8 * (lane & 1) - 2 * j;
-            mask[j] = e0 >= 2 ? ~0u : e0 == 1 ? 0xFFFFu : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int p = lane + 64 * i;
-            if (PIECES % 64 != 0 && p >= PIECES) continue;
-            const int row = (p * 16) / (HD * SZ), at = (p * 16) % (HD * SZ);  // K: position, byte
-            const int j = 16 * w + row;
-            uint8_t *kd = buf + ((j & 32) + krow(j & 31)) * Lds<HD>::kRow;
-            if constexpr (TYPE == kKvI8) {
-                const uint2 a = codes_to_f16(k[i].x), b = codes_to_f16(k[i].y), c2 = codes_to_f16(k[i].z), d = codes_to_f16(k[i].w);
-                *reinterpret_cast<u32x4 *>(kd + at * 2) = u32x4{a.x, a.y, b.x, b.y};
-                *reinterpret_cast<u32x4 *>(kd + at * 2 + 16) = u32x4{c2.x, c2.y, d.x, d.y};
-                const uint2 e = codes_to_f16(v[i].x), f = codes_to_f16(v[i].y), g = codes_to_f16(v[i].z), o = codes_to_f16(v[i].w);
-                uint8_t *vd = buf + Lds<HD>::kV + (w * HD + p) * 32;  // a piece is one column
-                *reinterpret_cast<u32x4 *>(vd) = u32x4{e.x, e.y, f.x, f.y};
-                *reinterpret_cast<u32x4 *>(vd + 16) = u32x4{g.x, g.y, o.x, o.y};
-            } else {
-                *reinterpret_cast<u32x4 *>(kd + at) = k[i];
-                const u32x4 x = {v[i].x & mask[0], v[i].y & mask[1], v[i].z & mask[2], v[i].w & mask[3]};
-                *reinterpret_cast<u32x4 *>(buf + Lds<HD>::kV + w * HD * 32 + p * 16) = x;
-            }
-        }
         if constexpr (TYPE == kKvI8) {
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int p = lane + 64 * i;
+                if (PIECES % 64 != 0 && p >= PIECES) continue;
+                const int pos = (p * 16) / HD, at = (p * 16) % HD / 8;  // K: position, piece in LDS
+                const int row = 16 * w + krow(pos);
+                uint8_t *kd = buf + row * Lds<HD>::kRow;
+                const uint2 a = codes_to_f16(k[i].x), b = codes_to_f16(k[i].y), c2 = codes_to_f16(k[i].z), d = codes_to_f16(k[i].w);
+                *reinterpret_cast<u32x4 *>(kd + kslot<HD>(row, at) * 16) = u32x4{a.x, a.y, b.x, b.y};
+                *reinterpret_cast<u32x4 *>(kd + kslot<HD>(row, at + 1) * 16) = u32x4{c2.x, c2.y, d.x, d.y};
+                const uint2 e = codes_to_f16(v[i].x), f = codes_to_f16(v[i].y), g = codes_to_f16(v[i].z), o = codes_to_f16(v[i].w);
+                uint8_t *vd = buf + Lds<HD>::kV + w * HD * 32;  // a piece is one column
+                *reinterpret_cast<u32x4 *>(vd + vslot(p, 0) * 16) = u32x4{e.x, e.y, f.x, f.y};
+                *reinterpret_cast<u32x4 *>(vd + vslot(p, 1) * 16) = u32x4{g.x, g.y, o.x, o.y};
+            }
             const float mine = (lane & 15) < live ? sc : 0.f;
             if (lane < 32) reinterpret_cast<float *>(buf + Lds<HD>::kScale)[(lane >> 4) * kBK + 16 * w + (lane & 15)] = mine;
             float big = mine < __builtin_inff() ? mine : 0.f;
             for (int off = 8; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
             if (lane == 16) reinterpret_cast<float *>(buf + Lds<HD>::kVmax)[w] = big;
+        } else {
+            __builtin_amdgcn_s_waitcnt(kWaitVm0);  // the wave's own pieces are in LDS
+            if (live < 16) {
+                uint8_t *vd = buf + Lds<HD>::kV + w * HD * 32;
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    uint32_t *p = reinterpret_cast<uint32_t *>(vd + (lane + 64 * i) * 16);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {  // dword j: positions 2 j, 2 j + 1 (the second half has the later 8)
+                        const int e0 = live - 8 * (vslot((lane + 64 * i) / 2, lane & 1) & 1) - 2 * j;
+                        if (e0 < 2) p[j] = e0 == 1 ? p[j] & 0xFFFFu : 0u;
+                    }
+                }
+            }
         }
         if (lane == 0) flag[w] = ok;
+    }
+    // s_waitcnt vmcnt(0), the other counters at their largest
+    static constexpr int kWaitVm0 = 0x0F70;
+    static __device__ __forceinline__ void to_lds(const uint8_t *from, uint8_t *to) {
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                         (__attribute__((address_space(3))) void *)to, 16, 0, 0);
     }
 };
 
 template <int TYPE, int HD>
-__global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs a) {
+__global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_prefill(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
     constexpr int KS = HD / 16, DT = HD / 32, NP = Op::kPieces;
@@ -185,7 +216,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
     // the first chunk is on its way while the queries are split
     Stage<TYPE, HD> st;
     int page = __builtin_amdgcn_readfirstlane(page_of(begin));
-    st.load(c, h, page, begin < end ? ch.at(begin) * kBK + 16 * wave : 0, lane);
+    auto buf_of = [&](int i) { return lds + (i & 1) * Lds<HD>::kBytes(TYPE); };
+    auto ok_of = [&](int i) { return lds + Lds<HD>::kOk(TYPE) + (i & 1) * 4; };
+    st.load(c, h, page, begin < end ? ch.at(begin) * kBK + 16 * wave : 0, buf_of(begin), wave, lane);
 
     // this wave's rows
     const int64_t rr = r0 + 32 * wave + col;
@@ -195,6 +228,8 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
     const bool live = rr < nrows && row >= 0 && row < a.rows;
     const int64_t pos64 = (int64_t)len - n + tok;
     const int pos = live && pos64 >= 0 ? (int)pos64 : -1;
+    // first position in the row's window; the sinks before it stay visible
+    const int wlo = a.window > 0 ? pos - a.window + 1 : -1;
     U128 qf[KS][NP];
     float qscale;
     {
@@ -234,16 +269,15 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
 #pragma unroll
         for (int e = 0; e < 16; e++) o[t][e] = 0.f;
 
-    if (begin < end)
-        st.store(lds + (begin & 1) * Lds<HD>::kBytes, lds + Lds<HD>::kOk + (begin & 1) * 4, wave, lane, live_of(begin));
     page = __builtin_amdgcn_readfirstlane(page_of(begin + 1));
+    if (begin < end) st.store(buf_of(begin), ok_of(begin), wave, lane, live_of(begin));
     for (int i = begin; i < end; i++) {
-        uint8_t *buf = lds + (i & 1) * Lds<HD>::kBytes;
+        const uint8_t *buf = buf_of(i);
         const bool more = i + 1 < end;
-        if (more) st.load(c, h, page, ch.at(i + 1) * kBK + 16 * wave, lane);
-        const int next_page = page_of(i + 2);
         __syncthreads();  // buffer i is written; everyone is done with buffer i - 1
-        const uint32_t okf = *reinterpret_cast<const uint32_t *>(lds + Lds<HD>::kOk + (i & 1) * 4);
+        if (more) st.load(c, h, page, ch.at(i + 1) * kBK + 16 * wave, buf_of(i + 1), wave, lane);
+        const int next_page = page_of(i + 2);
+        const uint32_t okf = *reinterpret_cast<const uint32_t *>(ok_of(i));
         const float *ksc = reinterpret_cast<const float *>(buf + Lds<HD>::kScale);
         const float *vsc = ksc + kBK;
 #pragma unroll
@@ -256,13 +290,37 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
             f32x16 sa;
 #pragma unroll
             for (int e = 0; e < 16; e++) sa[e] = 0.f;
-            const uint8_t *kp = buf + (32 * half + col) * Lds<HD>::kRow + 16 * hh;
+            const uint8_t *kp = buf + (32 * half + col) * Lds<HD>::kRow;
+            Vec kx[KS];
 #pragma unroll
-            for (int t = 0; t < KS; t++) {
-                const Vec kx = *reinterpret_cast<const Vec *>(kp + 32 * t);
+            for (int t = 0; t < KS; t++) kx[t] = *reinterpret_cast<const Vec *>(kp + kslot<HD>(col, 2 * t + hh) * 16);
 #pragma unroll
-                for (int p = 0; p < NP; p++) sa = Op::mfma32(kx, as_vec<Vec>(qf[t][p]), sa);
+            for (int t = 0; t < KS; t++)
+#pragma unroll
+                for (int p = 0; p < NP; p++) sa = Op::mfma32(kx[t], as_vec<Vec>(qf[t][p]), sa);
+            // four K reads ahead of the products
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+            for (int t = 0; t < KS - 4; t++) {
+                __builtin_amdgcn_sched_group_barrier(0x8, NP, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
+            __builtin_amdgcn_sched_group_barrier(0x8, 4 * NP, 0);
+            // With two waves a SIMD and long products, the wave past its first
+            // product goes first, so that the two fall out of step and one's
+            // softmax runs beside the other's products (128 columns: 295 -> 282
+            // us for 4096 tokens; 64 columns lose 1%).
+            if constexpr (HD >= 128) __builtin_amdgcn_s_setprio(1);
+            // V's operands fly during the softmax where there are registers for them
+            constexpr int EARLY = HD == 256 ? 0 : TYPE == kKvF16 ? 2 : HD == 64 && TYPE == kKvBF16 ? 1 : 0;
+            Vec vx[2][DT];
+            const uint8_t *vp = buf + Lds<HD>::kV + 2 * half * HD * 32 + vslot(col, hh) * 16;
+            auto read_v = [&](int u) {
+#pragma unroll
+                for (int t = 0; t < DT; t++) vx[u][t] = *reinterpret_cast<const Vec *>(vp + u * HD * 32 + t * 32 * 32);
+            };
+            if constexpr (EARLY > 0) read_v(0);
+            if constexpr (EARLY > 1) read_v(1);
             float x[16];
             float mx = -__builtin_inff();
             f32x4 vs[4];
@@ -284,8 +342,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
 #pragma unroll
                 for (int e = 0; e < 16; e++) {
                     const int key = c0 + 16 * (e >> 3) + 8 * hh + (e & 7);
-                    const bool in = (ok2 >> (8 * (e >> 3))) & 1;
-                    x[e] = in && sees(pos, key, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                    const int top = (ok2 >> (8 * (e >> 3))) & 1 ? pos : -1;  // a hole: nothing
+                    const bool in = (key <= top) & ((key >= wlo) | (key < a.sinks));
+                    x[e] = in ? x[e] : -__builtin_inff();
                 }
             }
 #pragma unroll
@@ -327,20 +386,18 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : 2) void attn_prefill(AttnArgs 
             U128 pf[2][NP];
             split8<Op>(x, pf[0]);
             split8<Op>(x + 8, pf[1]);
-            const uint8_t *vp = buf + Lds<HD>::kV + (2 * half * HD + col) * 32 + 16 * hh;
+            if constexpr (EARLY < 1) read_v(0);
+            if constexpr (EARLY < 2) read_v(1);
 #pragma unroll
-            for (int u = 0; u < 2; u++) {
+            for (int u = 0; u < 2; u++)
 #pragma unroll
-                for (int t = 0; t < DT; t++) {
-                    const Vec vx = *reinterpret_cast<const Vec *>(vp + u * HD * 32 + t * 32 * 32);
+                for (int t = 0; t < DT; t++)
 #pragma unroll
-                    for (int p = 0; p < NP; p++) o[t] = Op::mfma32(vx, as_vec<Vec>(pf[u][p]), o[t]);
-                }
-            }
+                    for (int p = 0; p < NP; p++) o[t] = Op::mfma32(vx[u][t], as_vec<Vec>(pf[u][p]), o[t]);
+            if constexpr (HD >= 128) __builtin_amdgcn_s_setprio(0);
         }
-        if (more)
-            st.store(lds + ((i + 1) & 1) * Lds<HD>::kBytes, lds + Lds<HD>::kOk + ((i + 1) & 1) * 4, wave, lane, live_of(i + 1));
         page = __builtin_amdgcn_readfirstlane(next_page);
+        if (more) st.store(buf_of(i + 1), ok_of(i + 1), wave, lane, live_of(i + 1));
     }
 
     lrun += __shfl_xor(lrun, 32);
@@ -379,10 +436,10 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
 template <int TYPE, int HD>
 hipError_t launch_typed(const AttnArgs &a, int64_t slots, hipStream_t s) {
     const void *fn = (const void *)attn_prefill<TYPE, HD>;
-    hipError_t e = ensure_lds(fn, Lds<HD>::kTotal);
+    hipError_t e = ensure_lds(fn, Lds<HD>::kTotal(TYPE));
     if (e != hipSuccess) return e;
     const dim3 grid(a.c.n_kv, (uint32_t)slots, a.splits);
-    e = launch_main(attn_prefill<TYPE, HD>, grid, dim3(256), Lds<HD>::kTotal, s, a);
+    e = launch_main(attn_prefill<TYPE, HD>, grid, dim3(256), Lds<HD>::kTotal(TYPE), s, a);
     if (e != hipSuccess || a.splits == 1) return e;
     return launch_attn_join(a, s);
 }

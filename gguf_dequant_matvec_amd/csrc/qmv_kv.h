@@ -94,10 +94,10 @@ struct AttnArgs {
     int64_t ld_acc;
 };
 
-// How a decode call is cut: 16-row operand tiles per wave, row tiles per
-// key-value head, pieces of the cache's length; workspace offsets in bytes.
+// How a call is cut: 16-row operand tiles per wave, row tiles per key-value
+// head, pieces of the cache's length, waves per workgroup; workspace offsets in bytes.
 struct AttnPlan {
-    int rt, tiles, splits;
+    int rt, tiles, splits, waves;
     int64_t part_rows;
     int64_t ld_logits;
     size_t ml_off, o_off, logits_off, bytes;
