@@ -408,8 +408,9 @@ size_t qmv_kv_page_bytes(int32_t type, int32_t n_kv_heads, int32_t head_dim, int
  * k, v: f32, row r at k + r * ldk (v + r * ldv), n_kv_heads * head_dim values
  * (ldk, ldv >= that: K and V may be column ranges of a stacked QKV product).
  * n rows in all, n <= QMV_MAX_KV_ROWS.  start: device int32[n_seq + 1], not
- * decreasing: rows start[s] .. start[s + 1] - 1 are sequence s's new tokens
- * (rows outside start[0] .. start[n_seq] - 1 are left out); NULL: n / n_seq
+ * decreasing, from at least 0 to at most n: rows start[s] .. start[s + 1] - 1
+ * are sequence s's new tokens (rows outside start[0] .. start[n_seq] - 1 are
+ * left out); NULL: n / n_seq
  * rows each (n a multiple of n_seq).  The j-th of a sequence's m new rows
  * goes to position seq_len[s] - m + j.  One launch. */
 qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *start,

@@ -554,6 +554,136 @@ def test_graph_replay_follows_lengths(window):
         assert np.isfinite(got).all()
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+def test_lengths_out_of_range(t):
+    """Lengths below 0, past max_len and past what a table row addresses are cut to the range."""
+    # (304: all that a table row addresses holds finite values)
+    c, rng = make_cache(t, 2, 64, 16, [304, 304, 304, 304, 40], 64)
+    c.seq_len = np.array([300, -3, 10 ** 9, 2 ** 31 - 1, -2 ** 31], np.int32)
+    run_decode(c, 2, 4, with_acc=True)
+    run_decode(c, 2, 4, max_len=200, window=64, sinks=2)
+    run_prefill(c, [20, 3, 200, 0, 5], 4)
+    run_prefill(c, [20, 3, 200, 0, 5], 4, max_len=100)
+    k, v = (rng.standard_normal((10, 2, 64), dtype=np.float32) for _ in range(2))
+    d = Dev(c)
+    q.qmv_kv_append(d.h, 10, dev(k), dev(v))
+    c.append(np.arange(6) * 2, k, v)
+    assert np.array_equal(d.pool(), c.pool)
+    c2, rng = make_cache(t, 2, 64, 16, [300, 300, 300], 65, spare=30)
+    c2.seq_len = np.array([10 ** 9, -1, 299], np.int32)
+    run_evict(c2, 150, 3, 10, rng.random((3, 2, 280), dtype=np.float32))      # scores for 280 positions only
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("page", [256, 4096])
+def test_large_pages(t, page):
+    lens = [700, 5, 256]
+    c, rng = make_cache(t, 2, 64, page, lens, 66, spare=12)
+    run_decode(c, 1, 4, with_acc=True)
+    run_prefill(c, [100, 5, 256], 4, window=70, sinks=3)
+    k, v = (rng.standard_normal((9, 2, 64), dtype=np.float32) for _ in range(2))
+    d = Dev(c)
+    q.qmv_kv_append(d.h, 9, dev(k), dev(v))
+    c.append(np.arange(4) * 3, k, v)
+    assert np.array_equal(d.pool(), c.pool)
+    run_evict(c, 300, 4, 60, rng.random((3, 2, 700), dtype=np.float32))
+
+
+@pytest.mark.parametrize("t", ["f16", "i8"])
+def test_many_sequences(t):
+    """More sequences than a wave has lanes, many of them without new rows."""
+    n = 300
+    lens = [(7 * i) % 41 for i in range(n)]
+    news = [0 if i % 3 else min(lens[i], (5 * i) % 23) for i in range(n)]
+    c, _ = make_cache(t, 1, 64, 16, lens, 67)
+    run_prefill(c, news, 2, before=2, after=1)
+    run_decode(c, 1, 2)
+
+
+def test_outputs_at_any_float():
+    """q, out and acc may start at any float of a tensor."""
+    c, _ = make_cache("f16", 1, 64, 16, [90, 41], 68)
+    d = Dev(c)
+    qh = synth.normal(2, synth.T_X, (2, 3 * 64 + 1), 1.0)
+    qd = dev(qh)[:, 1:]
+    for off in (1, 3):
+        buf = torch.full((2 * 3 * 64 + 8,), -5.0, device="cuda")
+        out = buf[off:off + 2 * 3 * 64]
+        q.qmv_attn_decode(d.h, 1, 3, qd, 0.125, out, 96)
+        want, tol, _, _ = ref.attention(c, [0, 1, 2], np.ascontiguousarray(qh[:, 1:]).reshape(2, 3, 64), 0.125, 96)
+        close(host(out).reshape(want.shape), want, tol, f"decode, out + {off}")
+        out.fill_(-5.0)
+        q.qmv_attn_prefill(d.h, 2, 3, qd, 0.125, out, 96)
+        close(host(out).reshape(want.shape), want, tol, f"prefill, out + {off}")
+        assert torch.all(buf[:off] == -5.0) and torch.all(buf[off + 2 * 3 * 64:] == -5.0)
+
+
+@pytest.mark.parametrize("exp", [-20, -22, 3])
+def test_f16_values_near_the_ends(exp):
+    """Cached f16 values among the subnormals keep their relative precision."""
+    c, _ = make_cache("f16", 1, 64, 16, [150], 69)
+    for p in range(c.n_pages):
+        k, v, _ = c.parts(p, 0)
+        with np.errstate(all="ignore"):
+            k[:] = (k.astype(np.float32) * np.float32(2.0 ** exp)).astype(np.float16)
+            v[:] = (v.astype(np.float32) * np.float32(2.0 ** exp)).astype(np.float16)
+    d = Dev(c)
+    qh = synth.normal(2, synth.T_X, (1, 2, 64), 1.0)
+    scale = float(np.float32(0.2 * 2.0 ** -exp))
+    want, tol, _, _ = ref.attention(c, [0, 1], qh, scale, 150)
+    out = torch.empty(128, device="cuda")
+    q.qmv_attn_decode(d.h, 1, 2, dev(qh.reshape(1, -1)), scale, out, 150)
+    close(host(out).reshape(want.shape), want, tol, f"decode 2^{exp}")
+    q.qmv_attn_prefill(d.h, 1, 2, dev(qh.reshape(1, -1)), scale, out, 150)
+    close(host(out).reshape(want.shape), want, tol, f"prefill 2^{exp}")
+
+
+def test_graph_replay_prefill_and_evict():
+    """A split prompt call and an eviction captured once; each replay, with new
+    inputs in place and eager work between, equals the eager calls bit for bit."""
+    kv, heads, hd, page, keep = 1, 4, 128, 64, 700
+    c, rng = make_cache("bf16", kv, hd, page, [3000, 900], 70, spare=2 * -(-keep // 64))
+    d = Dev(c)
+    start = dev(np.array([0, 30, 41], np.int32))
+    qd, out = torch.zeros(41, heads * hd, device="cuda"), torch.zeros(41, heads * hd, device="cuda")
+    ws = workspace(q.qmv_attn_prefill_workspace(d.h, 41, heads, c.cap))
+    assert ws is not None
+    per = -(-keep // page)
+    dst = dev(np.arange(c.n_pages - 2 * per, c.n_pages, dtype=np.int32).reshape(2, per))
+    acc = torch.zeros(2, kv, 3000, device="cuda")
+    kept = torch.zeros(2, kv, keep, dtype=torch.int32, device="cuda")
+    acc_out, len_out = torch.zeros(2, kv, keep, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+
+    def fn():
+        q.qmv_attn_prefill(d.h, 41, heads, qd, hd ** -0.5, out, c.cap, start=start, workspace=ws)
+        q.qmv_kv_evict(d.h, dst, keep, 4, 64, acc, kept, acc_out, len_out)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fn()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fn()
+    outs = (out, kept, acc_out, len_out, d.pages)
+    for rep in range(4):
+        qd.copy_(dev(rng.standard_normal(qd.shape, dtype=np.float32)))
+        acc.copy_(dev(rng.random(acc.shape, dtype=np.float32)))
+        for x in outs[:4]:
+            x.fill_(-3)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [host(x).copy() for x in outs]
+        for x in outs[:4]:
+            x.fill_(-3)
+        fn()
+        torch.cuda.synchronize()
+        for a, b in zip(got, outs):
+            assert np.array_equal(a, host(b)), rep
+
+
 def test_other_stream():
     """On a stream of its own, ordered by the caller; two streams at once with a
     workspace each."""
