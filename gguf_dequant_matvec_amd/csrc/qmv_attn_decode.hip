@@ -129,8 +129,11 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
     // With at most 16 rows a head's cache is read by one workgroup, once:
     // nontemporal loads (32 sequences up to 8150 positions of 128 columns: 148
     // -> 136 us).  More rows come with drafted tokens, whose tiles may read
-    // the same chunks: ordinary loads (8 x 8 tokens, window 4096: 34 against 37 us).
-    constexpr bool NT = RT == 1;
+    // the same chunks: ordinary loads (8 x 8 tokens, window 4096: 34 against 37
+    // us).  256 columns always take 16-row tiles, one or several of them:
+    // ordinary (16 x 8192 positions, 4 tiles: 259 against 334 us, one tile: 116
+    // against 113).
+    constexpr bool NT = RT == 1 && HD <= 128;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, g = lane >> 4;
     const int split = blockIdx.x, s = blockIdx.z;
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
