@@ -18,13 +18,16 @@
 //    are at most 2^(kBias + kSlack), which f16 pieces hold.
 // A wave takes every NW-th chunk of its workgroup's piece of the length, the NW
 // waves are joined through LDS, and the pieces by a second launch.
+// Measured: 32 sequences up to 8150 positions, 32 / 8 heads of 128, f16, 805 MB
+// of cache: 128 us (6.3 TB/s; a streaming read reaches 7.27) and 4.4 us for the
+// join; one sequence of 131071 int8 positions, 277 MB: 55 and 4.5 us; 301
+// positions, 9 / 3 heads of 64: 6.0 us, a chain of latencies.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
 
 namespace qmv {
 
 namespace {
-
 
 template <int TYPE>
 constexpr int kChunk = TYPE == kKvI8 ? 64 : 32;  // positions a wave takes at a time (16 KB at 128 columns)
@@ -185,7 +188,7 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
         int pos[RT];
         float qscale[RT];
         U128 qf[RT][KS][NP];
-    #pragma unroll
+#pragma unroll
         for (int rt = 0; rt < RT; rt++) {
             const int rr = r0 + rt * 16 + m;
             const bool live = rr < nrows;
@@ -194,12 +197,12 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
             const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
             float f[KS][8];
             float big = 0.f;
-    #pragma unroll
+#pragma unroll
             for (int t = 0; t < KS; t++) {
                 const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
                 const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
                 const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 8; e++) {
                     f[t][e] = live ? w[e] * a.q_sign : 0.f;
                     big = fmaxf(big, fabsf(f[t][e]));
@@ -217,9 +220,9 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
                 }
             }
             qscale[rt] = logit_factor(a.scale_log2, sh);
-    #pragma unroll
+#pragma unroll
             for (int t = 0; t < KS; t++) {
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
                 split8<Op>(f[t], qf[rt][t]);
             }
@@ -229,18 +232,18 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
             const bool more = i + NW < end;
             const int kpage2 = page_of(i + 2 * NW, m >> 2), vpage2 = page_of(i + 2 * NW, g);
             f32x4 sacc[RT][2 * SUB];
-    #pragma unroll
+#pragma unroll
             for (int rt = 0; rt < RT; rt++)
-    #pragma unroll
+#pragma unroll
                 for (int ub = 0; ub < 2 * SUB; ub++) sacc[rt][ub] = f32x4{0.f, 0.f, 0.f, 0.f};
-    #pragma unroll
+#pragma unroll
             for (int t = 0; t < KS; t++) {
-    #pragma unroll
+#pragma unroll
                 for (int ub = 0; ub < 2 * SUB; ub++) {
                     const Vec kx = kt.template op<Vec>(ub >> 1, ub & 1, t);
-    #pragma unroll
+#pragma unroll
                     for (int rt = 0; rt < RT; rt++)
-    #pragma unroll
+#pragma unroll
                         for (int p = 0; p < NP; p++) sacc[rt][ub] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][ub]);
                 }
             }
@@ -254,7 +257,7 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
             const bool whole = c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks) && __all(ok);
             if constexpr (TYPE == kKvI8) {
                 float big = 0.f;
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 16; e++) {
                     if (!whole) {
                         const bool any = ok && key0 + e <= pmax && (a.window <= 0 || key0 + e > pmin - a.window || key0 + e < a.sinks);
@@ -271,30 +274,30 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
                     vmul = nm;
                     vlog = (float)-ex;
                     vback = ldexpf(1.f, ex);
-    #pragma unroll
+#pragma unroll
                     for (int rt = 0; rt < RT; rt++)
-    #pragma unroll
+#pragma unroll
                         for (int t = 0; t < DT; t++) o[rt][t] *= r;
                 }
             } else if (!whole) {
                 // V of positions no row sees: zero, whatever the page holds there
-    #pragma unroll
+#pragma unroll
                 for (int w = 0; w < 4; w++) {
                     uint32_t keep = 0;
-    #pragma unroll
+#pragma unroll
                     for (int e = 0; e < 2; e++) {
                         const int key = key0 + 2 * w + e;
                         if (ok && key <= pmax && (a.window <= 0 || key > pmin - a.window || key < a.sinks)) keep |= 0xFFFFu << (16 * e);
                     }
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < DT; t++) vt.v[t][w] &= keep;
                 }
             }
             U128 pf[RT][SUB][NP];
-    #pragma unroll
+#pragma unroll
             for (int rt = 0; rt < RT; rt++) {
                 float x[PER];
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < PER; e++) {
                     x[e] = sacc[rt][e >> 2][e & 3];
                     if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
@@ -304,13 +307,13 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
                     const int rr = r0 + rt * 16 + m;
                     if (rr < nrows) {
                         float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0;
-    #pragma unroll
+#pragma unroll
                         for (int e = 0; e < PER; e += 4)
                             *reinterpret_cast<float4 *>(lp + e) = make_float4(x[e] * qscale[rt], x[e + 1] * qscale[rt], x[e + 2] * qscale[rt], x[e + 3] * qscale[rt]);
                     }
                 }
                 float mx = x[0];
-    #pragma unroll
+#pragma unroll
                 for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
                 mx *= qscale[rt];
                 if (__any(mx > mrun[rt] + kSlack)) {
@@ -320,29 +323,29 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
                     const float r = exp2_fast(mrun[rt] - mnew);
                     mrun[rt] = mnew;
                     lrun[rt] *= r;
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < DT; t++) o[rt][t] *= r;
                 }
                 const float off = kBias - mrun[rt] + vlog;
                 float sum = 0.f;
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < PER; e++) {
                     x[e] = exp2_fast(fmaf(x[e], qscale[rt], off));
                     sum += x[e];
                     if constexpr (TYPE == kKvI8) x[e] *= vt.vs[e];
                 }
                 lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
-    #pragma unroll
+#pragma unroll
                 for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
             }
-    #pragma unroll
+#pragma unroll
             for (int u = 0; u < SUB; u++) {
-    #pragma unroll
+#pragma unroll
                 for (int t = 0; t < DT; t++) {
                     const Vec vx = vt.template op<Vec>(u, t);
-    #pragma unroll
+#pragma unroll
                     for (int rt = 0; rt < RT; rt++)
-    #pragma unroll
+#pragma unroll
                         for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
                 }
             }
@@ -426,7 +429,8 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
 
 // acc[s][h][key] += sum over the rows of 2^(x - m) / l, rows in order.
 // The first part_rows workgroups join the pieces of a row each, the others take
-// 256 positions of a key-value head each: one launch for both.
+// 256 positions of a key-value head each: one launch for both (4 sequences of
+// 4352 positions: 4.8 us, latency; it reads the logits once).
 template <int TYPE, int HD>
 __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     constexpr int CK = kChunk<TYPE>;

@@ -17,8 +17,9 @@ namespace {
 // goes through LDS, already rounded, because a V block keeps the 16 positions
 // of one column next to each other: a thread gathers 8 positions of a column
 // and stores them at once where the workgroup's rows cover all 8, else one by
-// one.  Bound by the f32 reads, or for few rows by latency: 16 rows keep more
-// workgroups in flight, 32 leave fewer partly covered runs.
+// one.  Bound by memory, or for few rows by latency: 16 rows keep more
+// workgroups in flight, 32 leave fewer partly covered runs.  Measured: 6808
+// rows of 8 heads of 128, bf16, 83.7 MB: 20.2 us (4.1 TB/s); 16 rows: 4.3 us.
 template <int TYPE>
 __device__ __forceinline__ uint32_t kv_round(float x) {
     if constexpr (TYPE == kKvF16) {
@@ -210,7 +211,8 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int3
 // passes over an order-preserving integer key (counts in LDS), then counts per
 // wave and step, one prefix sum over them and the lanes' ballots place the
 // kept positions in order; among equal scores at the border the lowest
-// positions are kept.  Bound by latency: three barriers a pass.
+// positions are kept.  Bound by latency, three barriers a pass:
+// 64 heads of 4352 positions 11.1 us, 3 of 1001 5.6 us.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWaves = kSelThreads / 64;
 
@@ -380,8 +382,9 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
 // source V blocks (five where one position in sixteen is dropped): those are
 // read whole, up to GROUP at a time, into LDS rows padded so that columns
 // fall into different banks, and each thread picks the kept positions of its
-// columns, 16 bytes of the new block at a time.  Bound by memory: both caches
-// once.
+// columns, 16 bytes of the new block at a time.  Bound by memory, both caches
+// once: 64 heads of 4352 -> 4096 rows of 128 f16 columns, 269 MB, 63 us (4.3
+// TB/s; a plain copy runs at 4.98).
 constexpr int kMove = 64;
 
 template <int SZ, int HD>
