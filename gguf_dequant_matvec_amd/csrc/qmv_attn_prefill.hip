@@ -13,9 +13,9 @@
 // accumulators are 8 consecutive positions of its query, the operand layout
 // of P, and no value moves between lanes.  K rows are swizzled by 16-byte
 // pieces and V keeps the cache's block layout; both are read without bank
-// conflicts.  Measured: 4096 tokens, 32 / 8 heads of 128, f16: 256 - 280 us,
+// conflicts.  Measured: 4096 tokens, 32 / 8 heads of 128, f16: 254 - 275 us,
 // 1.0 PFLOP/s of operand work where library products reach 1.15; int8 prompts
-// in a window of 1024, heads of 64: 261 - 285 us, bound by the softmax's vector
+// in a window of 1024, heads of 64: 257 - 280 us, bound by the softmax's vector
 // instructions.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
@@ -189,9 +189,29 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         row0 = a.start[s];
         n = (int64_t)a.start[s + 1] - row0;
     }
-    const int len = kv_len(c, s, a.limit);
     const int64_t nrows = n * a.group;
     const int64_t r0 = (int64_t)tile * kBM;
+
+    // This wave's rows.  The queries do not wait for lengths and pages, and
+    // loads return in order: issued first, they are split while the first
+    // chunk is on its way (97 tokens 8.1 -> 7.3 us).
+    const int64_t rr = r0 + 32 * wave + col;
+    const int64_t tok = rr / a.group;
+    const int hg = (int)(rr % a.group);
+    const int64_t row = row0 + tok;
+    const bool live = rr < nrows && row >= 0 && row < a.rows;
+    float f[KS][8];
+    {
+        const float *qp = a.q + (live ? row : 0) * a.ldq + (int64_t)(h * a.group + (live ? hg : 0)) * HD + 8 * hh;
+#pragma unroll
+        for (int t = 0; t < KS; t++) {
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
+            const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+            f[t][0] = x.x, f[t][1] = x.y, f[t][2] = x.z, f[t][3] = x.w;
+            f[t][4] = y.x, f[t][5] = y.y, f[t][6] = y.z, f[t][7] = y.w;
+        }
+    }
+    const int len = kv_len(c, s, a.limit);
 
     // what the tile's and this wave's rows see
     auto pos_of = [&](int64_t r) {
@@ -223,12 +243,6 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
     auto ok_of = [&](int i) { return lds + Lds<HD>::kOk(TYPE) + (i & 1) * 4; };
     st.load(c, h, page, begin < end ? ch.at(begin) * kBK + 16 * wave : 0, buf_of(begin), wave, lane);
 
-    // this wave's rows
-    const int64_t rr = r0 + 32 * wave + col;
-    const int64_t tok = rr / a.group;
-    const int hg = (int)(rr % a.group);
-    const int64_t row = row0 + tok;
-    const bool live = rr < nrows && row >= 0 && row < a.rows;
     const int64_t pos64 = (int64_t)len - n + tok;
     const int pos = live && pos64 >= 0 ? (int)pos64 : -1;
     // first position in the row's window; the sinks before it stay visible
@@ -236,17 +250,13 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
     U128 qf[KS][NP];
     float qscale;
     {
-        const float *qp = a.q + (live ? row : 0) * a.ldq + (int64_t)(h * a.group + (live ? hg : 0)) * HD + 8 * hh;
         float big = 0.f;
         int sh = 0;
         if constexpr (TYPE != kKvBF16) {
 #pragma unroll
-            for (int t = 0; t < KS; t++) {
-                const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
-                const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
-                big = fmaxf(big, fmaxf(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))),
-                                       fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)))));
-            }
+            for (int t = 0; t < KS; t++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(f[t][e]));
             big = fmaxf(big, __shfl_xor(big, 32));
             if (big > 0.f && big < __builtin_inff()) {
                 sh = 15 - __builtin_amdgcn_frexp_expf(big);
@@ -256,12 +266,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         qscale = logit_factor(a.scale_log2, sh);
 #pragma unroll
         for (int t = 0; t < KS; t++) {
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
-            const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
-            float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 8; e++) f[e] = live ? ldexpf(f[e] * a.q_sign, sh) : 0.f;
-            split8<Op>(f, qf[t]);
+            for (int e = 0; e < 8; e++) f[t][e] = live ? ldexpf(f[t][e] * a.q_sign, sh) : 0.f;
+            split8<Op>(f[t], qf[t]);
         }
     }
     float mrun = kNoMax, lrun = 0.f;
