@@ -35,6 +35,7 @@ constexpr float kVmulNone = 0x1p100f, kVlogNone = 100.f;
 struct OpF16 {
     typedef f16x8 Vec;
     static constexpr int kPieces = 2;
+    static constexpr uint32_t kExp = 0x7C00, kExpStep = 0x0400;  // exponent bits, the lowest of them
     // to nearest even, one instruction for both: two pieces are off by at
     // most 2^-22 (truncation would leave 2^-20, all to one side)
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -53,6 +54,7 @@ struct OpF16 {
 struct OpBF16 {
     typedef bf16x8 Vec;
     static constexpr int kPieces = 3;
+    static constexpr uint32_t kExp = 0x7F80, kExpStep = 0x0080;
     static __device__ __forceinline__ uint32_t pack(float a, float b) {  // truncation
         return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
     }
@@ -107,6 +109,33 @@ __device__ __forceinline__ void split8(float *f, U128 *piece) {
     }
 }
 
+__device__ __forceinline__ bool sees(int p, int key, int window, int sinks) {
+    return key <= p && (window <= 0 || key > p - window || key < sinks);
+}
+
+// A masked weight is 0, but 0 times a NaN or an infinity is NaN: where rows of
+// a tile see different positions, V values that are not finite are taken out
+// before the product, and the rows that do see one get an infinity in its
+// column by a product of their own: kHuge, the largest bf16 value, in both
+// operands overflows f32, and 0 in the other operand gives 0.
+constexpr uint32_t kHuge = 0x7F7F;
+
+// Bits 0 and 16: which of a dword's two values are not finite (all exponent
+// bits set: adding the lowest of them carries into the sign bit).
+template <class Op>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+    return (((w & (Op::kExp * 0x10001u)) + Op::kExpStep * 0x10001u) & 0x80008000u) >> 15;
+}
+// The operand of "the row sees position key + e" for e = 0 .. 7.
+__device__ __forceinline__ U128 seen8(bool there, int pos, int key, int window, int sinks) {
+    U128 v;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        v.w[j] = (there && sees(pos, key + 2 * j, window, sinks) ? kHuge : 0u) |
+                 (there && sees(pos, key + 2 * j + 1, window, sinks) ? kHuge << 16 : 0u);
+    return v;
+}
+
 // Four int8 codes of a dword as two dwords of f16 pairs, exactly: 1024 + 128 +
 // code is the f16 whose low byte is the code with its sign bit flipped.
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t v) {
@@ -138,10 +167,6 @@ __device__ __forceinline__ Chunks visible_chunks(int pmin, int pmax, int window,
     }
     v.n = v.sink + (end > v.win0 ? end - v.win0 : 0);
     return v;
-}
-
-__device__ __forceinline__ bool sees(int p, int key, int window, int sinks) {
-    return key <= p && (window <= 0 || key > p - window || key < sinks);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -265,32 +265,24 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
                     }
                     big = fmaxf(big, fabsf(vt.vs[e]));
                 }
-                if (__any(big * vmul > 1.f && big < __builtin_inff())) {
+                if (__any(big * vmul > 1.f)) {
+                    big = 0.f;  // again, without infinities
+#pragma unroll
+                    for (int e = 0; e < 16; e++) big = fmaxf(big, fabsf(vt.vs[e]) < __builtin_inff() ? fabsf(vt.vs[e]) : 0.f);
                     for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
-                    int ex = __builtin_amdgcn_frexp_expf(big);
-                    ex = ex > 120 ? 120 : ex;
-                    const float nm = ldexpf(1.f, -ex);
-                    const float r = nm / vmul;
-                    vmul = nm;
-                    vlog = (float)-ex;
-                    vback = ldexpf(1.f, ex);
+                    if (big * vmul > 1.f) {
+                        int ex = __builtin_amdgcn_frexp_expf(big);
+                        ex = ex > 120 ? 120 : ex;
+                        const float nm = ldexpf(1.f, -ex);
+                        const float r = nm / vmul;
+                        vmul = nm;
+                        vlog = (float)-ex;
+                        vback = ldexpf(1.f, ex);
 #pragma unroll
-                    for (int rt = 0; rt < RT; rt++)
+                        for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-                        for (int t = 0; t < DT; t++) o[rt][t] *= r;
-                }
-            } else if (!whole) {
-                // V of positions no row sees: zero, whatever the page holds there
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t keep = 0;
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int key = key0 + 2 * w + e;
-                        if (ok && key <= pmax && (a.window <= 0 || key > pmin - a.window || key < a.sinks)) keep |= 0xFFFFu << (16 * e);
+                            for (int t = 0; t < DT; t++) o[rt][t] *= r;
                     }
-#pragma unroll
-                    for (int t = 0; t < DT; t++) vt.v[t][w] &= keep;
                 }
             }
             U128 pf[RT][SUB][NP];
@@ -332,11 +324,41 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
                 for (int e = 0; e < PER; e++) {
                     x[e] = exp2_fast(fmaf(x[e], qscale[rt], off));
                     sum += x[e];
-                    if constexpr (TYPE == kKvI8) x[e] *= vt.vs[e];
+                    if constexpr (TYPE == kKvI8) {
+                        const float w = x[e] * vt.vs[e];
+                        x[e] = whole || x[e] != 0.f ? w : 0.f;  // (a scale that the row does not see may be NaN)
+                    }
                 }
                 lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
 #pragma unroll
                 for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
+            }
+            if constexpr (TYPE != kKvI8) {
+                if (!whole) {
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int t = 0; t < DT; t++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) bad |= not_finite<Op>(vt.v[t][j]);
+                    if (__any(bad != 0)) {
+                        U128 seen[RT];
+#pragma unroll
+                        for (int rt = 0; rt < RT; rt++) seen[rt] = seen8(ok, pos[rt], key0, a.window, a.sinks);
+#pragma unroll
+                        for (int t = 0; t < DT; t++) {
+                            U128 marks;
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const uint32_t b = not_finite<Op>(vt.v[t][j]);
+                                vt.v[t][j] &= ~(b * 0xFFFFu);
+                                marks.w[j] = b * kHuge;
+                            }
+#pragma unroll
+                            for (int rt = 0; rt < RT; rt++)
+                                o[rt][t] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][t]);
+                        }
+                    }
+                }
             }
 #pragma unroll
             for (int u = 0; u < SUB; u++) {
@@ -479,7 +501,7 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
                 const bool read = k < ch.sink || (k >= ch.win0 && k < ch.win0 + (ch.n - ch.sink));
                 if (read && s_r[i] != 0.f) {
                     const float x = a.logits[(head * nrows + r0 + i) * a.ld_logits + key];
-                    sum += exp2_fast(x - s_m[i]) * s_r[i];
+                    if (x != -__builtin_inff()) sum += exp2_fast(x - s_m[i]) * s_r[i];  // (0 times a NaN row's factor)
                 }
             }
         }
@@ -506,7 +528,7 @@ hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
 // Whether the 256 registers that eight waves leave each lane hold the kernel's
 // operands; four waves have 512.
 constexpr bool eight_fit(int type, int hd, int rt) {
-    return rt == 1 ? hd <= 128 : hd == 64 || (hd == 96 && type != kKvI8);
+    return rt == 1 ? hd <= 128 : hd == 64 || (hd == 96 && type == kKvF16);
 }
 
 template <int TYPE, int HD, int RT>

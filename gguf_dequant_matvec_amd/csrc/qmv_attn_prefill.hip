@@ -32,8 +32,10 @@ struct Lds {  // one buffer, bytes
     static constexpr int kV = kBK * kRow;               // V blocks
     static constexpr int kScale = kV + kBK * HD * 2;    // 8-bit: row scales of K, then of V
     static constexpr int kVmax = kScale + 2 * kBK * 4;  // largest row scale of V, one a block
-    static constexpr int kBytes(int type) { return type == kKvI8 ? kVmax + 16 : kScale; }
-    static constexpr int kOk(int type) { return 2 * kBytes(type); }  // per buffer: 4 flags, one a block
+    static constexpr int kMarks = kScale;               // 16-bit: a bit for every value of V, [block][column][16]
+    static constexpr int kBytes(int type) { return type == kKvI8 ? kVmax + 16 : kMarks + 4 * HD * 2; }
+    static constexpr int kOk(int type) { return 2 * kBytes(type); }  // per buffer: 4 flags, one a block:
+                                                                     // 1: no hole, 2: marks set
     static constexpr int kTotal(int type) { return kOk(type) + 32; }
 };
 
@@ -91,9 +93,12 @@ struct Stage {
             }
         }
     }
-    // live: positions of the 16 that some row may see; V of the others is zero
-    __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live) const {
+    // live: positions of the 16 that some row may see; 8-bit: scales of the
+    // others, which may be anything, are left out.  whole: every row sees every
+    // position; where not, V values that are not finite leave marks and zeros.
+    __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live, bool whole) const {
         if (!ok) live = 0;
+        bool marked = false;
         if constexpr (TYPE == kKvI8) {
 #pragma unroll
             for (int i = 0; i < N; i++) {
@@ -117,20 +122,29 @@ struct Stage {
             if (lane == 16) reinterpret_cast<float *>(buf + Lds<HD>::kVmax)[w] = big;
         } else {
             __builtin_amdgcn_s_waitcnt(kWaitVm0);  // the wave's own pieces are in LDS
-            if (live < 16) {
+            if (!whole || !ok) {
+                typedef typename KvOp<TYPE>::Op Op;
                 uint8_t *vd = buf + Lds<HD>::kV + w * HD * 32;
+                uint32_t any = 0;
 #pragma unroll
                 for (int i = 0; i < N; i++) {
-                    uint32_t *p = reinterpret_cast<uint32_t *>(vd + (lane + 64 * i) * 16);
+                    const int q = lane + 64 * i, d = q / 2, half = vslot(d, q & 1) & 1;
+                    U128 v = *reinterpret_cast<const U128 *>(vd + q * 16);
+                    uint32_t bits = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {  // dword j: positions 2 j, 2 j + 1 (the second half has the later 8)
-                        const int e0 = live - 8 * (vslot((lane + 64 * i) / 2, lane & 1) & 1) - 2 * j;
-                        if (e0 < 2) p[j] = e0 == 1 ? p[j] & 0xFFFFu : 0u;
+                    for (int j = 0; j < 4; j++) {
+                        const uint32_t bad = not_finite<Op>(v.w[j]);
+                        v.w[j] &= ~(bad * 0xFFFFu);
+                        bits |= ((bad & 1) | (bad >> 15)) << (2 * j);
                     }
+                    buf[Lds<HD>::kMarks + (w * HD + d) * 2 + half] = (uint8_t)bits;
+                    if (bits) *reinterpret_cast<U128 *>(vd + q * 16) = v;
+                    any |= bits;
                 }
+                marked = __any(any != 0);
             }
         }
-        if (lane == 0) flag[w] = ok;
+        if (lane == 0) flag[w] = (ok ? 1 : 0) | (marked ? 2 : 0);
     }
     // s_waitcnt vmcnt(0), the other counters at their largest
     static constexpr int kWaitVm0 = 0x0F70;
@@ -236,6 +250,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         const int left = pmax + 1 - (ch.at(i) * kBK + 16 * wave);
         return left > 16 ? 16 : left < 0 ? 0 : left;
     };
+    auto whole_of = [&](int i) {  // whether every row of the tile sees all of it
+        const int c0 = ch.at(i) * kBK, c1 = c0 + kBK - 1;
+        return c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks);
+    };
     // the first chunk is on its way while the queries are split
     Stage<TYPE, HD> st;
     int page = __builtin_amdgcn_readfirstlane(page_of(begin));
@@ -280,7 +298,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         for (int e = 0; e < 16; e++) o[t][e] = 0.f;
 
     page = __builtin_amdgcn_readfirstlane(page_of(begin + 1));
-    if (begin < end) st.store(buf_of(begin), ok_of(begin), wave, lane, live_of(begin));
+    if (begin < end) st.store(buf_of(begin), ok_of(begin), wave, lane, live_of(begin), whole_of(begin));
     for (int i = begin; i < end; i++) {
         const uint8_t *buf = buf_of(i);
         const bool more = i + 1 < end;
@@ -297,6 +315,28 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
             if (c0 > wmax || (a.window > 0 && c1 <= wmin - a.window && c0 >= a.sinks)) continue;
             const uint32_t ok2 = __builtin_amdgcn_readfirstlane((okf >> (16 * half)) & 0x0101u);
             const bool whole = c1 <= wmin && (a.window <= 0 || c0 > wmax - a.window || c1 < a.sinks) && ok2 == 0x0101u;
+            if constexpr (TYPE != kKvI8) {
+                const uint32_t marked = __builtin_amdgcn_readfirstlane((okf >> (16 * half)) & 0x0202u);
+                if (marked) {
+                    U128 seen[2];
+#pragma unroll
+                    for (int u = 0; u < 2; u++)
+                        seen[u] = seen8((ok2 >> (8 * u)) & 1, pos, c0 + 16 * u + 8 * hh, a.window, a.sinks);
+#pragma unroll
+                    for (int t = 0; t < DT; t++) {
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            if (!((marked >> (8 * u)) & 2)) continue;
+                            const uint32_t bits = buf[Lds<HD>::kMarks + ((2 * half + u) * HD + 32 * t + col) * 2 + hh];
+                            U128 marks;
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                marks.w[j] = ((bits >> (2 * j)) & 1) * kHuge | ((bits >> (2 * j + 1)) & 1) * (kHuge << 16);
+                            o[t] = OpBF16::mfma32(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[u]), o[t]);
+                        }
+                    }
+                }
+            }
             f32x16 sa;
 #pragma unroll
             for (int e = 0; e < 16; e++) sa[e] = 0.f;
@@ -355,6 +395,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
                     const int top = (ok2 >> (8 * (e >> 3))) & 1 ? pos : -1;  // a hole: nothing
                     const bool in = (key <= top) & ((key >= wlo) | (key < a.sinks));
                     x[e] = in ? x[e] : -__builtin_inff();
+                    if constexpr (TYPE == kKvI8) vs[e >> 2][e & 3] = in ? vs[e >> 2][e & 3] : 0.f;  // it may be NaN
                 }
             }
 #pragma unroll
@@ -407,7 +448,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
             if constexpr (HD >= 128) __builtin_amdgcn_s_setprio(0);
         }
         page = __builtin_amdgcn_readfirstlane(next_page);
-        if (more) st.store(buf_of(i + 1), ok_of(i + 1), wave, lane, live_of(i + 1));
+        if (more) st.store(buf_of(i + 1), ok_of(i + 1), wave, lane, live_of(i + 1), whole_of(i + 1));
     }
 
     lrun += __shfl_xor(lrun, 32);

@@ -367,9 +367,12 @@ qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *
  * Positions 0 .. seq_len[s] - 1 of sequence s exist, the new tokens of the
  * call among them: the last n positions are its n new tokens, and a new token
  * at a negative position (seq_len[s] < n, as for padding sequences with
- * seq_len 0) has no place in the cache and sees nothing.  Values at
- * positions that exist must be finite; what slots behind the last position
- * hold does not matter.  Lengths and table are read on the device when the
+ * seq_len 0) has no place in the cache and sees nothing.  A row's result
+ * depends on the positions it sees alone: what slots behind the last position
+ * or hidden positions hold does not matter, NaN and infinities included (a
+ * value that is not finite in V makes its column NaN or infinite in the rows
+ * that see it; a hidden 8-bit V row of far larger scale may cost a row of the
+ * same call resolution, see qmv_attn_decode).  Lengths and table are read on the device when the
  * call runs, so a captured call follows them from replay to replay. */
 typedef enum {
     QMV_KV_F16 = 1,   /* the GGUF ids of F16, I8 and BF16 */
@@ -438,9 +441,10 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * acc: NULL, or f32 [n_seq][n_kv_heads][ld_acc], ld_acc >= max_len: position
  * t of key-value head h gets, added, the weights w_t of the n tokens and of the
  * query heads that share h (what qmv_kv_evict ranks by).
- * f32 throughout: queries and weights enter the matrix cores as exact sums of
- * 16-bit pieces (f16 hi + lo, bf16 in three), maximum, sum and output are
- * f32.  Results do not depend on anything but the arguments.
+ * f32 throughout: queries and weights enter the matrix cores as sums of 16-bit
+ * pieces (f16 hi + lo, bf16 in three), maximum, sum and output are f32.  f16
+ * and 8-bit caches resolve weights (8-bit: weight times V row scale) down to
+ * 2^-36 of the largest.  Results do not depend on anything but the arguments.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is
  * 0), 16-byte aligned, no initial contents needed.  One launch, a second one
  * to join the pieces when the length is split or acc is given. */

@@ -360,6 +360,64 @@ def test_prefill_holes_and_large_logits(t):
     run_prefill(c, [60, 40], 4, window=90, sinks=20, qstd=40.0)
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (37, 3)])
+def test_hidden_values_do_not_matter(t, hd, window, sinks):
+    """NaN and infinities in K or V of existing positions: rows that do not see
+    the position are as without them, rows that do are not finite (V: in that
+    column, or for the 8-bit scales in all)."""
+    n, length, heads, page = 16, 333, 4, 16
+    spots = [(332, "v", np.nan, 5), (330, "v", np.inf, 7), (325, "k", np.nan, 3), (299, "v", -np.inf, 0),
+             (290, "k", np.inf, 9), (1, "v", np.nan, 11), (length - 60, "v", np.nan, 2)]
+    base, _ = make_cache(t, 1, hd, page, [length], 37)
+    scale = hd ** -0.5
+    qh = synth.normal(8, synth.T_X, (n + 44, heads, hd), 1.0)
+    for what, m in (("decode", 1), ("decode", n), ("prefill", n + 44)):
+        q0 = qh[-m:]
+        clean, tol, _, _ = ref.attention(base, [0, m], q0, scale, base.cap, window, sinks)
+        for p, part, bad, col in spots:
+            c = ref.Cache(t, 1, hd, page, base.n_pages, base.table, base.seq_len)
+            c.pool = base.pool.copy()
+            pg, slot = c.where(0, p)
+            k, v, sc = c.parts(pg, 0)
+            if t == "i8":
+                sc[0 if part == "k" else 1, slot] = bad
+            else:
+                code = np.float16(bad) if t == "f16" else ref.round_bf16(np.float32(bad) if np.isinf(bad) else 0)
+                if t == "bf16" and np.isnan(bad):
+                    code = np.uint16(0x7FC0)
+                if part == "k":
+                    k[slot, col] = code
+                else:
+                    v[slot // 16, col, slot % 16] = code
+            d = Dev(c)
+            out = torch.empty(m * heads * hd, device="cuda")
+            if what == "decode":
+                ws = workspace(q.qmv_attn_decode_workspace(d.h, m, heads, c.cap, window, sinks))
+                q.qmv_attn_decode(d.h, m, heads, dev(q0.reshape(m, -1)), scale, out, c.cap, window=window, sinks=sinks,
+                                  workspace=ws)
+            else:
+                ws = workspace(q.qmv_attn_prefill_workspace(d.h, m, heads, c.cap, window, sinks))
+                q.qmv_attn_prefill(d.h, m, heads, dev(q0.reshape(m, -1)), scale, out, c.cap, window=window, sinks=sinks,
+                                   workspace=ws)
+            got = host(out).reshape(m, heads, hd)
+            pos = length - m + np.arange(m)
+            sees = p <= pos
+            if window:
+                sees &= (p > pos - window) | (p < sinks)
+            name = f"{what} {t} m{m} {part}[{p}]={bad}"
+            close(got[~sees], clean[~sees], tol[~sees], name)
+            if not sees.any():
+                continue
+            if part == "v" and t != "i8":
+                assert not np.isfinite(got[sees][:, :, col]).any(), name
+                other = np.arange(hd) != col
+                close(got[sees][:, :, other], clean[sees][:, :, other], tol[sees][:, :, other], name)
+            elif part == "v" or np.isnan(bad):
+                assert not np.isfinite(got[sees]).any(), name
+
+
 def test_prefill_matches_decode():
     """Both calls compute the same rows (n <= 16), each within its bound."""
     c, _ = make_cache("f16", 2, 128, 64, [700, 16, 31], 36)
