@@ -117,7 +117,7 @@ struct Stage {
             }
             const float mine = (lane & 15) < live ? sc : 0.f;
             if (lane < 32) reinterpret_cast<float *>(buf + Lds<HD>::kScale)[(lane >> 4) * kBK + 16 * w + (lane & 15)] = mine;
-            float big = mine < __builtin_inff() ? mine : 0.f;
+            float big = fabsf(mine) < __builtin_inff() ? fabsf(mine) : 0.f;
             for (int off = 8; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
             if (lane == 16) reinterpret_cast<float *>(buf + Lds<HD>::kVmax)[w] = big;
         } else {
