@@ -231,6 +231,7 @@ qmv_status qmv_kv_evict(const qmv_kv_cache *cache, const int32_t *dst_table, int
     if (!dst_table || !acc || !kept || !acc_out || !len_out) return QMV_EINVAL;
     if (dst_ld < 1 || dst_ld > (1ll << 30) / cache->page_size) return QMV_ESHAPE;
     if (keep < 1 || keep > dst_ld * cache->page_size) return QMV_ESHAPE;
+    if (keep > (1 << 30) - 64) return QMV_ESHAPE;  // 2^24 workgroups of 256 threads are one too many
     if (first < 0 || recent < 0 || (int64_t)first + recent > keep) return QMV_ESHAPE;
     if (ld_acc < 1 || ld_acc > (1ll << 40) || ld_out < keep || ld_out > (1ll << 40)) return QMV_ESHAPE;
     if (!aligned(dst_table, 4) || !aligned(acc, 4) || !aligned(kept, 4) || !aligned(acc_out, 4) || !aligned(len_out, 4))

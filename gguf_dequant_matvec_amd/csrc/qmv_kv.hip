@@ -240,7 +240,6 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
     float *acc_out = e.acc_out + head * e.ld_out;
     const float *acc = e.acc + head * e.ld_acc;
     const int out_len = len < e.keep ? len : e.keep;
-    if (h == 0 && tid == 0) e.len_out[s] = out_len;
     for (int i = out_len + tid; i < e.keep; i += kSelThreads) {
         kept[i] = -1;
         acc_out[i] = 0.f;
@@ -404,6 +403,8 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
     const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
     const int len = kv_len(c, s, e.limit);
     const int out_len = len < e.keep ? len : e.keep;
+    // (seq_len itself may be len_out: cutting a cut length changes nothing)
+    if (blockIdx.x == 0 && h == 0 && tid == 0) e.len_out[s] = out_len;
     const int i0 = blockIdx.x * kMove;
     if (i0 >= out_len) return;
     const int cnt = out_len - i0 < kMove ? out_len - i0 : kMove;

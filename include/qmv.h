@@ -484,8 +484,11 @@ size_t qmv_attn_prefill_workspace(const qmv_kv_cache *cache, int64_t n, int32_t 
  * acc: f32 [n_seq][n_kv_heads][ld_acc]; seq_len is taken as at most ld_acc.
  * Outputs: kept int32 [n_seq][n_kv_heads][keep], the old positions (-1 past
  * the new length); acc_out f32 [n_seq][n_kv_heads][ld_out], ld_out >= keep,
- * their acc (0 past the new length, up to keep); len_out int32[n_seq],
- * min(seq_len, keep).  Two launches, no workspace. */
+ * their acc (0 past the new length up to keep, behind that left as it was:
+ * clear it before decode steps add to it); len_out int32[n_seq],
+ * min(seq_len, keep).  len_out may be the cache's seq_len; other outputs must
+ * not overlap each other or the inputs.  keep <= 2^30 - 64.  Two launches, no
+ * workspace. */
 qmv_status qmv_kv_evict(const qmv_kv_cache *cache, const int32_t *dst_table, int64_t dst_ld,
                         int32_t keep, int32_t first, int32_t recent, const float *acc,
                         int64_t ld_acc, int32_t *kept, float *acc_out, int64_t ld_out,

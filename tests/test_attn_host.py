@@ -151,6 +151,12 @@ def test_evict_refusals():
         assert status_of(evict, c, **kw) == "QMV_EALIGN", kw
 
 
+def test_evict_largest_keep():
+    """The most positions whose workgroups one launch can have."""
+    c = cache(table_ld=1 << 26)
+    assert status_of(evict, c, keep=(1 << 30) - 63, dst_ld=1 << 26, ld_out=1 << 30) == "QMV_ESHAPE"
+
+
 def test_binding_refusals():
     """Tensors whose type, shape or strides the C call cannot see."""
     torch = pytest.importorskip("torch")

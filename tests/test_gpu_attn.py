@@ -488,6 +488,25 @@ def test_evict_holes():
     run_evict(c, 70, 4, 10, rng.random((2, 2, 200), dtype=np.float32), dst)
 
 
+@pytest.mark.parametrize("t", ["f16", "i8"])
+def test_evict_lengths_in_place(t):
+    """len_out may be the cache's own seq_len: every head still cuts from the old length."""
+    keep, lens = 100, [1500, 0, 99, 100, 101, 1030]
+    c, rng = make_cache(t, 16, 64, 16, lens, 45, spare=len(lens) * -(-keep // 16))
+    per = -(-keep // 16)
+    dst = np.arange(c.n_pages - len(lens) * per, c.n_pages, dtype=np.int32).reshape(len(lens), per)
+    acc = rng.random((len(lens), 16, 1500), dtype=np.float32)
+    d = Dev(c)
+    kept = torch.full((len(lens), 16, keep), -9, dtype=torch.int32, device="cuda")
+    out = torch.full((len(lens), 16, keep), -9.0, device="cuda")
+    q.qmv_kv_evict(d.h, dev(dst), keep, 4, 20, dev(acc), kept, out, d.lens)
+    k, a, n = ref.evict(c, dst, keep, 4, 20, acc)
+    assert np.array_equal(host(kept), k)
+    assert np.array_equal(host(out).view(np.uint32), a.view(np.uint32))
+    assert np.array_equal(host(d.lens), n)
+    assert np.array_equal(d.pool(), c.pool)
+
+
 # ---- together -----------------------------------------------------------------
 
 @pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
