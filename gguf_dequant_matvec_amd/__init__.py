@@ -187,6 +187,25 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _cache_stream(cache, stream, *tensors) -> int:
+    """The stream of a call over a cache of tensors, all of whose tensors must
+    be on the pages' GPU, the current one: a kernel cannot tell, it would fault.
+    Raw addresses are taken as they are."""
+    on = cache.device
+    if on is None:
+        return _stream(stream)
+    if on < 0:
+        raise ValueError("the cache's tensors are not on a GPU")
+    for a in tensors:
+        if a is not None and a.__class__ is not int and a.get_device() != on:
+            raise ValueError(f"a tensor on {a.device}, the cache on GPU {on}")
+    if _torch().cuda.current_device() != on:
+        raise ValueError(f"the cache is on GPU {on}, which is not the current one")
+    if stream is not None and not isinstance(stream, int) and stream.device_index != on:
+        raise ValueError(f"a stream of GPU {stream.device_index}, the cache on GPU {on}")
+    return _stream(stream)
+
+
 def _type(t) -> int:
     return TYPES[t] if isinstance(t, str) else int(t)
 
@@ -359,7 +378,8 @@ class KvCache:
     pages, `table` int32 [n_seq][table_ld], `seq_len` int32 [n_seq], all on the
     device.  Tensors are checked and kept alive; with raw addresses the counts
     have to be given.  Lengths and table are read when a call runs, so both
-    may be changed in place between calls."""
+    may be changed in place between calls.  The calls refuse tensors of another
+    device, and a cache that is not on the current one."""
 
     def __init__(self, t, n_kv_heads, head_dim, page_size, pages, table, seq_len, n_pages=None,
                  n_seq=None, table_ld=None):
@@ -388,12 +408,21 @@ class KvCache:
             if seq_len.dtype is not _torch().int32 or not seq_len.is_contiguous() or \
                     seq_len.numel() < n_seq:
                 raise ValueError("seq_len must be n_seq contiguous int32 values")
+        self.device = None if isinstance(pages, int) else pages.get_device()
+        for a in (table, seq_len):
+            if self.device is not None and not isinstance(a, int) and a.get_device() != self.device:
+                raise ValueError(f"pages on {pages.device}, but a tensor on {a.device}")
         self.type, self.n_kv_heads, self.head_dim, self.page_size = t, n_kv_heads, head_dim, page_size
         self.page_bytes, self.n_pages, self.n_seq, self.table_ld = page_bytes, n_pages, n_seq, table_ld
         self.pages, self.table, self.seq_len = pages, table, seq_len
         self._struct = _KvCacheStruct(t, n_kv_heads, head_dim, page_size, n_pages, _ptr(pages),
                                       _ptr(table), table_ld, _ptr(seq_len), n_seq)
         self._address = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):
+        if "_address" in self.__dict__:   # the calls go by the addresses taken above
+            raise AttributeError("a KvCache stays as it was made: change its tensors in place, or make another")
+        object.__setattr__(self, name, value)
 
 
 def qmv_kv_page_bytes(t, n_kv_heads, head_dim, page_size) -> int:
@@ -438,7 +467,7 @@ def qmv_kv_append(cache, n, k, v, start=None, ldk=None, ldv=None, stream=None):
     ldk, ldv = _f32_rows("k", k, ldk, n, width), _f32_rows("v", v, ldv, n, width)
     _check_start(cache, start)
     _call("qmv_kv_append", cache._address, n, _ptr(start), _ptr(k), ldk, _ptr(v), ldv,
-          _stream(stream))
+          _cache_stream(cache, stream, start, k, v))
 
 
 def qmv_attn_decode_workspace(cache, n, n_heads, max_len, window=0, sinks=0, with_acc=False) -> int:
@@ -464,7 +493,8 @@ def qmv_attn_decode(cache, n, n_heads, q, scale, out, max_len, window=0, sinks=0
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _call("qmv_attn_decode", cache._address, n, n_heads, _ptr(q), ldq, scale, window, sinks,
-          _ptr(out), max_len, _ptr(acc), ld_acc, _ptr(workspace), ws_bytes, _stream(stream))
+          _ptr(out), max_len, _ptr(acc), ld_acc, _ptr(workspace), ws_bytes,
+          _cache_stream(cache, stream, q, out, acc, workspace))
 
 
 def qmv_attn_prefill_workspace(cache, n, n_heads, max_len, window=0, sinks=0) -> int:
@@ -479,7 +509,8 @@ def qmv_attn_prefill(cache, n, n_heads, q, scale, out, max_len, start=None, wind
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _call("qmv_attn_prefill", cache._address, n, _ptr(start), n_heads, _ptr(q), ldq, scale, window,
-          sinks, _ptr(out), max_len, _ptr(workspace), ws_bytes, _stream(stream))
+          sinks, _ptr(out), max_len, _ptr(workspace), ws_bytes,
+          _cache_stream(cache, stream, start, q, out, workspace))
 
 
 def qmv_kv_evict(cache, dst_table, keep, first, recent, acc, kept, acc_out, len_out, dst_ld=None,
@@ -494,7 +525,8 @@ def qmv_kv_evict(cache, dst_table, keep, first, recent, acc, kept, acc_out, len_
     _check_dense("kept", kept, "int32", cache.n_seq * cache.n_kv_heads * max(keep, 0))
     _check_dense("len_out", len_out, "int32", cache.n_seq)
     _call("qmv_kv_evict", cache._address, _ptr(dst_table), dst_ld, keep, first, recent, _ptr(acc),
-          ld_acc, _ptr(kept), _ptr(acc_out), ld_out, _ptr(len_out), _stream(stream))
+          ld_acc, _ptr(kept), _ptr(acc_out), ld_out, _ptr(len_out),
+          _cache_stream(cache, stream, dst_table, acc, kept, acc_out, len_out))
 
 
 def qmv_probe_stream_read(buf, nbytes, sink, stream=None):

@@ -188,6 +188,27 @@ def test_binding_refusals():
         q.qmv_kv_evict(c, table, 8, 0, 0, z(2, 2, 64), z(2, 2, 8), z(2, 2, 8), lens, stream=0)
 
 
+def test_cache_of_host_tensors():
+    """Calls over tensors that are not on a GPU end on the host; a cache's
+    tensors cannot be exchanged behind its addresses."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    pages, table, lens = z(8 * 8192, dtype=torch.uint8), z(2, 4, dtype=torch.int32), z(2, dtype=torch.int32)
+    c = q.KvCache("f16", 2, 64, 16, pages, table, lens)
+    k, x = z(2, 128), z(2, 256)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        q.qmv_kv_append(c, 2, k, k, stream=0)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        q.qmv_attn_decode(c, 1, 4, x, 0.1, z(2, 256), 64, stream=0)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        q.qmv_attn_prefill(c, 2, 4, x, 0.1, z(2, 256), 64, stream=0)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        q.qmv_kv_evict(c, table, 8, 0, 0, z(2, 2, 64), z(2, 2, 8, dtype=torch.int32), z(2, 2, 8), lens, stream=0)
+    for name in ("table", "seq_len", "pages", "n_seq"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+
+
 # ---- the reference itself -------------------------------------------------------
 
 def test_reference_by_hand():

@@ -788,3 +788,22 @@ def test_results_repeat():
     c, _ = make_cache("bf16", 2, 64, 32, [3000, 411], 63)
     a = run_decode(c, 5, 8, with_acc=True)
     assert np.array_equal(a, run_decode(c, 5, 8, with_acc=True))
+
+
+def test_tensors_of_the_host_are_refused():
+    """A kernel cannot tell a host address: the binding refuses it before the launch."""
+    c, _ = make_cache("f16", 1, 64, 16, [40], 64)
+    d = Dev(c)
+    x, out = torch.zeros(1, 128, device="cuda"), torch.zeros(1, 128, device="cuda")
+    with pytest.raises(ValueError):
+        q.KvCache("f16", 1, 64, 16, d.pages, d.table.cpu(), d.lens)
+    with pytest.raises(ValueError):
+        q.KvCache("f16", 1, 64, 16, d.pages, d.table, d.lens.cpu())
+    with pytest.raises(ValueError):
+        q.qmv_kv_append(d.h, 1, x[:, :64], x[:, 64:].cpu())
+    with pytest.raises(ValueError):
+        q.qmv_attn_decode(d.h, 1, 2, x.cpu(), 0.125, out, 64)
+    with pytest.raises(ValueError):
+        q.qmv_attn_prefill(d.h, 1, 2, x, 0.125, out.cpu(), 64)
+    torch.cuda.synchronize()
+    assert not host(out).any()
