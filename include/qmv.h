@@ -371,7 +371,8 @@ qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *
  * depends on the positions it sees alone: what slots behind the last position
  * or hidden positions hold does not matter, NaN and infinities included (a
  * value that is not finite in V makes its column NaN or infinite in the rows
- * that see it; a hidden 8-bit V row of far larger scale may cost a row of the
+ * that see it, one in K or in a query leaves the rows concerned unspecified,
+ * most often NaN; a hidden 8-bit V row of far larger scale may cost a row of the
  * same call resolution, see qmv_attn_decode).  Lengths and table are read on the device when the
  * call runs, so a captured call follows them from replay to replay. */
 typedef enum {
@@ -444,7 +445,8 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * f32 throughout: queries and weights enter the matrix cores as sums of 16-bit
  * pieces (f16 hi + lo, bf16 in three), maximum, sum and output are f32.  f16
  * and 8-bit caches resolve weights (8-bit: weight times V row scale) down to
- * 2^-36 of the largest.  Results do not depend on anything but the arguments.
+ * 2^-36 of the largest, the latter for V row scales between 2^-100 and 2^100.
+ * Results do not depend on anything but the arguments.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is
  * 0), 16-byte aligned, no initial contents needed.  One launch, a second one
  * to join the pieces when the length is split or acc is given. */
