@@ -171,15 +171,16 @@ __device__ __forceinline__ Chunks visible_chunks(int pmin, int pmax, int window,
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Joins the pieces of output row prow: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// Joins the `count` pieces of output row prow, which are at `first`, first +
+// stride, ...: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 // One workgroup of 256 threads a row.  The pieces' factors go to LDS first; then HD / 4 lanes
 // read a piece (16 bytes each), 256 / (HD / 4) pieces at a time and four such
 // rounds in flight.  Bound by latency: 64 pieces of 128 columns, eight loads a
 // thread, 4.5 us.
-constexpr int kMaxPieces = 128;
+constexpr int kMaxPieces = 512;
 
 template <int HD>
-__device__ __forceinline__ void join_row(const AttnArgs &a, int64_t prow) {
+__device__ __forceinline__ void join_row(const AttnArgs &a, int64_t prow, int64_t first, int64_t stride, int count) {
     constexpr int L = HD / 4, G = 256 / L;
     const int tid = threadIdx.x, lane = tid & 63;
     __shared__ float s_r[kMaxPieces];
@@ -190,7 +191,7 @@ __device__ __forceinline__ void join_row(const AttnArgs &a, int64_t prow) {
 #pragma unroll
     for (int k = 0; k < kMaxPieces / 64; k++) {
         ml[k] = make_float2(kNoMax, 0.f);
-        if (lane + 64 * k < a.splits) ml[k] = a.part_ml[(lane + 64 * k) * a.part_rows + prow];
+        if (64 * k < count && lane + 64 * k < count) ml[k] = a.part_ml[first + (lane + 64 * k) * stride];
         mm = fmaxf(mm, ml[k].x);
     }
     for (int off = 32; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off));
@@ -199,16 +200,16 @@ __device__ __forceinline__ void join_row(const AttnArgs &a, int64_t prow) {
     for (int k = 0; k < kMaxPieces / 64; k++) {
         const float r = exp2_fast(ml[k].x - mm);
         l += r * ml[k].y;
-        if (tid < 64 && lane + 64 * k < a.splits) s_r[lane + 64 * k] = r;
+        if (tid < 64 && lane + 64 * k < count) s_r[lane + 64 * k] = r;
     }
     for (int off = 32; off; off >>= 1) l += __shfl_xor(l, off);
     __syncthreads();
     const int g = tid / L, d = tid % L;
     if (g < G) {
-        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o) + prow * L + d;
+        const f32x4 *src = reinterpret_cast<const f32x4 *>(a.part_o) + first * L + d;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-        for (int i = g; i < a.splits; i += G) o += src[i * a.part_rows * L] * s_r[i];
+        for (int i = g; i < count; i += G) o += src[i * stride * L] * s_r[i];
         s_o[g][d] = o;
     }
     __syncthreads();

@@ -107,6 +107,7 @@ static void fill_attn(AttnArgs &a, const AttnPlan &p, float scale, void *ws) {
     a.group = a.n_heads / a.c.n_kv;
     a.tiles = p.tiles;
     a.splits = p.splits;
+    a.parts = p.parts;
     a.part_rows = p.part_rows;
     a.part_ml = (float2 *)((uint8_t *)ws + p.ml_off);
     a.part_o = (float *)((uint8_t *)ws + p.o_off);
@@ -124,7 +125,7 @@ static qmv_status decode_plan(const qmv_kv_cache *c, int32_t n, int32_t n_heads,
     if ((int64_t)p.tiles * c->n_kv_heads > 65535) return QMV_ESHAPE;
     // the joining launch takes a workgroup of 256 threads a row, and for the
     // weights one for every 256 positions of a key-value head
-    int64_t blocks = p.splits > 1 || with_acc ? p.part_rows : 0;
+    int64_t blocks = p.slots > c->n_seq || with_acc ? p.part_rows : 0;
     if (with_acc) blocks += c->n_seq * c->n_kv_heads * ((max_len + 255) / 256);
     if (blocks >= (1ll << 24)) return QMV_ESHAPE;
     return QMV_OK;
@@ -164,6 +165,7 @@ qmv_status qmv_attn_decode(const qmv_kv_cache *cache, int32_t n, int32_t n_heads
     a.window = window;
     a.sinks = sinks;
     fill_attn(a, p, scale, workspace);
+    a.share = (int2 *)((uint8_t *)workspace + p.share_off);
     a.logits = (float *)((uint8_t *)workspace + p.logits_off);
     a.ld_logits = p.ld_logits;
     a.acc = acc;

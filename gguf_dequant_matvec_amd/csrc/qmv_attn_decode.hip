@@ -19,7 +19,7 @@
 // A wave takes every NW-th chunk of its workgroup's piece of the length, the NW
 // waves are joined through LDS, and the pieces by a second launch.
 // Measured: 32 sequences up to 8150 positions, 32 / 8 heads of 128, f16, 805 MB
-// of cache: 128 us (6.3 TB/s; a streaming read reaches 7.27) and 4.4 us for the
+// of cache: 130 us (6.2 TB/s; a streaming read of the same size reaches 7.1) and 4.4 us for the
 // join; one sequence of 131071 int8 positions, 277 MB: 55 and 4.5 us; 301
 // positions, 9 / 3 heads of 64: 6.0 us, a chain of latencies.
 #include "qmv_attn.h"
@@ -123,8 +123,93 @@ struct VTile {
     }
 };
 
-template <int TYPE, int HD, int RT, int NW, bool ACC>
-__global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
+// The sequences' chunks, one sequence behind the other, are divided evenly
+// among the workgroups of a head that fit the chip at once: a workgroup takes
+// the end of one sequence, whole ones, the start of another, as they come.
+// Equal numbers of pieces for all sequences would end with the longest one's,
+// and a workgroup that starts while others read costs about 5 us of waiting
+// for lengths, table and first rows.  A sequence counts kEnter chunks more for
+// that.  Workgroup p's piece of sequence s goes to slot p + s: the pairs are a
+// staircase, so slots are distinct, and a sequence's are neighbours.
+// Measured (32 / 8 heads of 128, f16), against equal numbers of pieces: 32
+// sequences of 354 to 8192 positions, 672 MB, 114 us against 134; 63 of 300
+// and one of 65536, 67 us against 582; 32 of 6144, 134 us against 133.
+constexpr int kEnter = 4, kMinPiece = 8;  // chunks
+
+struct Range {
+    int s, at, len;  // first sequence, the unit it starts at, its length
+    int lo, hi;      // the workgroup's units
+};
+
+__device__ __forceinline__ int clamp_len(int len, int limit) { return len < 0 ? 0 : len > limit ? limit : len; }
+
+template <int CK>
+__device__ __forceinline__ int units_of(const AttnArgs &a, int len) {
+    const int c = visible_chunks(len - (int)a.n, len - 1, a.window, a.sinks, CK).n;
+    return (c < 1 ? 1 : c) + kEnter;
+}
+
+// Inclusive prefix sum over the 64 lanes: within rows of 16, then across them.
+__device__ __forceinline__ int scan64(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast 15, 31
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
+
+template <int CK>
+__device__ __forceinline__ Range find_range(const AttnArgs &a, int p, int lane) {
+    const int n_seq = a.c.n_seq;
+    int len[4], upto[4];  // of 256 sequences: lengths, and sums of units up to each among its 64
+    auto load = [&](int base) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) len[k] = base + 64 * k + lane < n_seq ? a.c.seq_len[base + 64 * k + lane] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if (base + 64 * k >= n_seq) break;
+            len[k] = clamp_len(len[k], a.limit);
+            upto[k] = scan64(base + 64 * k + lane < n_seq ? units_of<CK>(a, len[k]) : 0);
+        }
+    };
+    int all = 0;
+    for (int base = 0; base < n_seq; base += 256) {
+        load(base);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (base + 64 * k < n_seq) all += __builtin_amdgcn_readlane(upto[k], 63);
+    }
+    int parts = all / kMinPiece;  // (a range is never empty)
+    parts = parts < 1 ? 1 : parts > a.parts ? a.parts : parts;
+    Range r{-1, 0, 0, 0, 0};
+    if (p >= parts) return r;
+    const int each = all / parts, more = all - each * parts;  // `more` of them take one unit more
+    r.lo = each * p + (p < more ? p : more);
+    r.hi = r.lo + each + (p < more ? 1 : 0);
+    int first = 0;
+    for (int base = 0; base < n_seq; base += 256) {
+        if (n_seq > 256) load(base);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if (base + 64 * k >= n_seq) break;
+            const uint64_t past = __ballot(first + upto[k] > r.lo);
+            if (past) {
+                const int who = __builtin_ctzll(past);
+                r.s = base + 64 * k + who;
+                r.len = __builtin_amdgcn_readlane(len[k], who);
+                r.at = first + (who > 0 ? __builtin_amdgcn_readlane(upto[k], who - 1) : 0);
+                return r;
+            }
+            first += __builtin_amdgcn_readlane(upto[k], 63);
+        }
+    }
+    return r;
+}
+
+template <int TYPE, int HD, int RT, int NW, bool ACC, bool RANGES>
+__global__ __launch_bounds__(NW * 64, RANGES && RT == 1 && HD <= 128 ? 2 : 1) void attn_decode(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
     constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
@@ -137,316 +222,384 @@ __global__ __launch_bounds__(NW * 64) void attn_decode(AttnArgs a) {
     // ordinary (16 x 8192 positions, 4 tiles: 259 against 334 us, one tile: 116
     // against 113).
     constexpr bool NT = RT == 1 && HD <= 128;
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, m = lane & 15, g = lane >> 4;
-    const int split = blockIdx.x, s = blockIdx.z;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
     const KvArgs &c = a.c;
-    const int len = kv_len(c, s, a.limit);
     const int n = (int)a.n;
     const int nrows = n * a.group;
     const int r0 = tile * 16 * RT;
-
-    // what the rows of this tile see, and the first chunk on its way
     const int last = r0 + 16 * RT < nrows ? r0 + 16 * RT - 1 : nrows - 1;
-    const int pmin = len - n + r0 / a.group, pmax = len - n + last / a.group;
-    const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, CK);
-    const int begin = (int)((int64_t)ch.n * split / a.splits), end = (int)((int64_t)ch.n * (split + 1) / a.splits);
-    const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
-    const int32_t *table = c.table + (int64_t)s * c.table_ld;
-    auto page_of = [&](int i, int grp) {  // page of a lane group's positions in chunk number i
-        if (i >= end) return -1;
-        const int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
-        if (pi > last_page) return -1;
-        const int pg = table[pi];
-        return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
-    };
-    float mrun[RT], lrun[RT];
-    f32x4 o[RT][DT];
-    // 8-bit: power of two that brings the row scales of V to at most 1, its
-    // logarithm (it enters with the exponent) and its inverse
-    float vmul = kVmulNone, vlog = TYPE == kKvI8 ? kVlogNone : 0.f, vback = 1.f / kVmulNone;
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        mrun[rt] = kNoMax;
-        lrun[rt] = 0.f;
-#pragma unroll
-        for (int t = 0; t < DT; t++) o[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    int s = blockIdx.z, at = 0, lo = 0, hi = 0, len = 0;
+    if constexpr (RANGES) {
+        const Range r = find_range<CK>(a, blockIdx.x, tid & 63);
+        // (uniform, which the compiler does not see)
+        s = __builtin_amdgcn_readfirstlane(r.s);
+        at = __builtin_amdgcn_readfirstlane(r.at);
+        lo = __builtin_amdgcn_readfirstlane(r.lo);
+        hi = __builtin_amdgcn_readfirstlane(r.hi);
+        len = __builtin_amdgcn_readfirstlane(r.len);
+        if (s < 0) return;
+    } else {
+        len = kv_len(c, s, a.limit);
     }
-
-    if (begin + wave < end) {
-        int i = begin + wave;
-        int kpage = page_of(i, m >> 2), vpage = page_of(i, g);
-        KTile<TYPE, HD> kt;
-        VTile<TYPE, HD> vt;
-        bool ok = vpage >= 0;  // the lane group's positions are in a page (not a hole)
-        kt.template load<NT>(c, h, ch.at(i), kpage, g, m);
-        vt.template load<NT>(c, h, ch.at(i), vpage, g, m);
-        kpage = page_of(i + NW, m >> 2);
-        vpage = page_of(i + NW, g);
-
-        // the rows
-        int pos[RT];
-        float qscale[RT];
-        U128 qf[RT][KS][NP];
+    for (;;) {  // the workgroup's sequences
+        // Taken as new each time: lane offsets kept from one sequence to the
+        // next would take 20 to 80 registers, and some variants would spill.
+        int lane = tid & 63;
+        if constexpr (RANGES) asm volatile("" : "+v"(lane));
+        const int m = lane & 15, g = lane >> 4;
+        // what the rows of this tile see, and the first chunk on its way
+        const int pmin = len - n + r0 / a.group, pmax = len - n + last / a.group;
+        const Chunks ch = visible_chunks(pmin, pmax, a.window, a.sinks, CK);
+        int begin, end, slot, units = 0, next = 0;
+        bool opens, closes;  // this piece is the sequence's first, its last
+        if constexpr (RANGES) {
+            units = units_of<CK>(a, len);
+            const int from = at + kEnter, all = units - kEnter;
+            opens = lo <= from;
+            closes = hi >= at + units;
+            begin = opens ? 0 : lo - from;
+            end = closes ? all : hi - from;
+            if (all != ch.n) {  // a tile whose rows see less than all rows do
+                begin = (int)((int64_t)begin * ch.n / all);
+                end = (int)((int64_t)end * ch.n / all);
+            }
+            slot = blockIdx.x + s;
+            if (s + 1 < c.n_seq) next = c.seq_len[s + 1];
+        } else {
+            const int piece = blockIdx.x;
+            opens = piece == 0;
+            closes = piece == a.splits - 1;
+            begin = (int)((int64_t)ch.n * piece / a.splits);
+            end = (int)((int64_t)ch.n * (piece + 1) / a.splits);
+            slot = s * a.splits + piece;
+        }
+        const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
+        const int32_t *table = c.table + (int64_t)s * c.table_ld;
+        auto page_of = [&](int i, int grp) {  // page of a lane group's positions in chunk number i
+            if (i >= end) return -1;
+            const int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
+            if (pi > last_page) return -1;
+            const int pg = table[pi];
+            return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
+        };
+        float mrun[RT], lrun[RT];
+        f32x4 o[RT][DT];
+        // 8-bit: power of two that brings the row scales of V to at most 1, its
+        // logarithm (it enters with the exponent) and its inverse
+        float vmul = kVmulNone, vlog = TYPE == kKvI8 ? kVlogNone : 0.f, vback = 1.f / kVmulNone;
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) {
-            const int rr = r0 + rt * 16 + m;
-            const bool live = rr < nrows;
-            const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
-            pos[rt] = live ? len - n + j : -1;
-            const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
-            float f[KS][8];
-            float big = 0.f;
+            mrun[rt] = kNoMax;
+            lrun[rt] = 0.f;
 #pragma unroll
-            for (int t = 0; t < KS; t++) {
-                const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
-                const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
-                const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    f[t][e] = live ? w[e] * a.q_sign : 0.f;
-                    big = fmaxf(big, fabsf(f[t][e]));
-                }
-            }
-            // f16 pieces: scale the row by a power of two so that its largest
-            // value is in [2^14, 2^15)
-            int sh = 0;
-            if constexpr (TYPE != kKvBF16) {
-                big = fmaxf(big, __shfl_xor(big, 16));
-                big = fmaxf(big, __shfl_xor(big, 32));
-                if (big > 0.f && big < __builtin_inff()) {
-                    sh = 15 - __builtin_amdgcn_frexp_expf(big);
-                    sh = sh > 100 ? 100 : sh;
-                }
-            }
-            qscale[rt] = logit_factor(a.scale_log2, sh);
-#pragma unroll
-            for (int t = 0; t < KS; t++) {
-#pragma unroll
-                for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
-                split8<Op>(f[t], qf[rt][t]);
-            }
+            for (int t = 0; t < DT; t++) o[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        for (;;) {
-            const bool more = i + NW < end;
-            const int kpage2 = page_of(i + 2 * NW, m >> 2), vpage2 = page_of(i + 2 * NW, g);
-            f32x4 sacc[RT][2 * SUB];
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                for (int ub = 0; ub < 2 * SUB; ub++) sacc[rt][ub] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int t = 0; t < KS; t++) {
-#pragma unroll
-                for (int ub = 0; ub < 2 * SUB; ub++) {
-                    const Vec kx = kt.template op<Vec>(ub >> 1, ub & 1, t);
-#pragma unroll
-                    for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                        for (int p = 0; p < NP; p++) sacc[rt][ub] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][ub]);
-                }
-            }
-            // the K registers are free: the next chunk's K flies during the
-            // softmax and the second product, its V during the next first one
-            if (more) kt.template load<NT>(c, h, ch.at(i + NW), kpage, g, m);
+        if (begin + wave < end) {
+            int i = begin + wave;
+            int kpage = page_of(i, m >> 2), vpage = page_of(i, g);
+            KTile<TYPE, HD> kt;
+            VTile<TYPE, HD> vt;
+            bool ok = vpage >= 0;  // the lane group's positions are in a page (not a hole)
+            kt.template load<NT>(c, h, ch.at(i), kpage, g, m);
+            vt.template load<NT>(c, h, ch.at(i), vpage, g, m);
+            kpage = page_of(i + NW, m >> 2);
+            vpage = page_of(i + NW, g);
 
-            const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
-            // a chunk that every row sees whole needs no masks
-            const int c0 = ch.at(i) * CK, c1 = c0 + CK - 1;
-            const bool whole = c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks) && __all(ok);
-            if constexpr (TYPE == kKvI8) {
+            // the rows
+            int pos[RT];
+            float qscale[RT];
+            U128 qf[RT][KS][NP];
+#pragma unroll
+            for (int rt = 0; rt < RT; rt++) {
+                const int rr = r0 + rt * 16 + m;
+                const bool live = rr < nrows;
+                const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
+                pos[rt] = live ? len - n + j : -1;
+                const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
+                float f[KS][8];
                 float big = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    if (!whole) {
-                        const bool any = ok && key0 + e <= pmax && (a.window <= 0 || key0 + e > pmin - a.window || key0 + e < a.sinks);
-                        vt.vs[e] = any ? vt.vs[e] : 0.f;
-                    }
-                    big = fmaxf(big, fabsf(vt.vs[e]));
-                }
-                if (__any(big * vmul > 1.f)) {
-                    big = 0.f;  // again, without infinities
+                for (int t = 0; t < KS; t++) {
+                    const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
+                    const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+                    const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int e = 0; e < 16; e++) big = fmaxf(big, fabsf(vt.vs[e]) < __builtin_inff() ? fabsf(vt.vs[e]) : 0.f);
-                    for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
-                    if (big * vmul > 1.f) {
-                        int ex = __builtin_amdgcn_frexp_expf(big);
-                        ex = ex > 120 ? 120 : ex;
-                        const float nm = ldexpf(1.f, -ex);
-                        const float r = nm / vmul;
-                        vmul = nm;
-                        vlog = (float)-ex;
-                        vback = ldexpf(1.f, ex);
+                    for (int e = 0; e < 8; e++) {
+                        f[t][e] = live ? w[e] * a.q_sign : 0.f;
+                        big = fmaxf(big, fabsf(f[t][e]));
+                    }
+                }
+                // f16 pieces: scale the row by a power of two so that its largest
+                // value is in [2^14, 2^15)
+                int sh = 0;
+                if constexpr (TYPE != kKvBF16) {
+                    big = fmaxf(big, __shfl_xor(big, 16));
+                    big = fmaxf(big, __shfl_xor(big, 32));
+                    if (big > 0.f && big < __builtin_inff()) {
+                        sh = 15 - __builtin_amdgcn_frexp_expf(big);
+                        sh = sh > 100 ? 100 : sh;
+                    }
+                }
+                qscale[rt] = logit_factor(a.scale_log2, sh);
+#pragma unroll
+                for (int t = 0; t < KS; t++) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
+                    split8<Op>(f[t], qf[rt][t]);
+                }
+            }
+
+            for (;;) {
+                const bool more = i + NW < end;
+                const int kpage2 = page_of(i + 2 * NW, m >> 2), vpage2 = page_of(i + 2 * NW, g);
+                f32x4 sacc[RT][2 * SUB];
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int ub = 0; ub < 2 * SUB; ub++) sacc[rt][ub] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int t = 0; t < KS; t++) {
+#pragma unroll
+                    for (int ub = 0; ub < 2 * SUB; ub++) {
+                        const Vec kx = kt.template op<Vec>(ub >> 1, ub & 1, t);
 #pragma unroll
                         for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-                            for (int t = 0; t < DT; t++) o[rt][t] *= r;
+                            for (int p = 0; p < NP; p++) sacc[rt][ub] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][ub]);
                     }
                 }
-            }
-            U128 pf[RT][SUB][NP];
+                // the K registers are free: the next chunk's K flies during the
+                // softmax and the second product, its V during the next first one
+                if (more) kt.template load<NT>(c, h, ch.at(i + NW), kpage, g, m);
+
+                const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
+                // a chunk that every row sees whole needs no masks
+                const int c0 = ch.at(i) * CK, c1 = c0 + CK - 1;
+                const bool whole = c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks) && __all(ok);
+                if constexpr (TYPE == kKvI8) {
+                    float big = 0.f;
 #pragma unroll
-            for (int rt = 0; rt < RT; rt++) {
-                float x[PER];
-#pragma unroll
-                for (int e = 0; e < PER; e++) {
-                    x[e] = sacc[rt][e >> 2][e & 3];
-                    if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
-                    if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
-                }
-                if constexpr (ACC) {
-                    const int rr = r0 + rt * 16 + m;
-                    if (rr < nrows) {
-                        float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0;
-#pragma unroll
-                        for (int e = 0; e < PER; e += 4)
-                            *reinterpret_cast<float4 *>(lp + e) = make_float4(x[e] * qscale[rt], x[e + 1] * qscale[rt], x[e + 2] * qscale[rt], x[e + 3] * qscale[rt]);
+                    for (int e = 0; e < 16; e++) {
+                        if (!whole) {
+                            const bool any = ok && key0 + e <= pmax && (a.window <= 0 || key0 + e > pmin - a.window || key0 + e < a.sinks);
+                            vt.vs[e] = any ? vt.vs[e] : 0.f;
+                        }
+                        big = fmaxf(big, fabsf(vt.vs[e]));
                     }
-                }
-                float mx = x[0];
+                    if (__any(big * vmul > 1.f)) {
+                        big = 0.f;  // again, without infinities
 #pragma unroll
-                for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
-                mx *= qscale[rt];
-                if (__any(mx > mrun[rt] + kSlack)) {
-                    mx = fmaxf(mx, __shfl_xor(mx, 16));
-                    mx = fmaxf(mx, __shfl_xor(mx, 32));
-                    const float mnew = fmaxf(mrun[rt], mx);
-                    const float r = exp2_fast(mrun[rt] - mnew);
-                    mrun[rt] = mnew;
-                    lrun[rt] *= r;
-#pragma unroll
-                    for (int t = 0; t < DT; t++) o[rt][t] *= r;
-                }
-                const float off = kBias - mrun[rt] + vlog;
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < PER; e++) {
-                    x[e] = exp2_fast(fmaf(x[e], qscale[rt], off));
-                    sum += x[e];
-                    if constexpr (TYPE == kKvI8) {
-                        const float w = x[e] * vt.vs[e];
-                        x[e] = whole || x[e] != 0.f ? w : 0.f;  // (a scale that the row does not see may be NaN)
-                    }
-                }
-                lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
-#pragma unroll
-                for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
-            }
-            if constexpr (TYPE != kKvI8) {
-                if (!whole) {
-                    uint32_t bad = 0;
-#pragma unroll
-                    for (int t = 0; t < DT; t++)
-#pragma unroll
-                        for (int j = 0; j < 4; j++) bad |= not_finite<Op>(vt.v[t][j]);
-                    if (__any(bad != 0)) {
-                        U128 seen[RT];
-#pragma unroll
-                        for (int rt = 0; rt < RT; rt++) seen[rt] = seen8(ok, pos[rt], key0, a.window, a.sinks);
-#pragma unroll
-                        for (int t = 0; t < DT; t++) {
-                            U128 marks;
-#pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                const uint32_t b = not_finite<Op>(vt.v[t][j]);
-                                vt.v[t][j] &= ~(b * 0xFFFFu);
-                                marks.w[j] = b * kHuge;
-                            }
+                        for (int e = 0; e < 16; e++) big = fmaxf(big, fabsf(vt.vs[e]) < __builtin_inff() ? fabsf(vt.vs[e]) : 0.f);
+                        for (int off = 32; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
+                        if (big * vmul > 1.f) {
+                            int ex = __builtin_amdgcn_frexp_expf(big);
+                            ex = ex > 120 ? 120 : ex;
+                            const float nm = ldexpf(1.f, -ex);
+                            const float r = nm / vmul;
+                            vmul = nm;
+                            vlog = (float)-ex;
+                            vback = ldexpf(1.f, ex);
 #pragma unroll
                             for (int rt = 0; rt < RT; rt++)
-                                o[rt][t] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][t]);
+#pragma unroll
+                                for (int t = 0; t < DT; t++) o[rt][t] *= r;
                         }
                     }
                 }
+                U128 pf[RT][SUB][NP];
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++) {
+                    float x[PER];
+#pragma unroll
+                    for (int e = 0; e < PER; e++) {
+                        x[e] = sacc[rt][e >> 2][e & 3];
+                        if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
+                        if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                    }
+                    if constexpr (ACC) {
+                        const int rr = r0 + rt * 16 + m;
+                        if (rr < nrows) {
+                            float *lp = a.logits + (((int64_t)s * c.n_kv + h) * nrows + rr) * a.ld_logits + key0;
+#pragma unroll
+                            for (int e = 0; e < PER; e += 4)
+                                *reinterpret_cast<float4 *>(lp + e) = make_float4(x[e] * qscale[rt], x[e + 1] * qscale[rt], x[e + 2] * qscale[rt], x[e + 3] * qscale[rt]);
+                        }
+                    }
+                    float mx = x[0];
+#pragma unroll
+                    for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
+                    mx *= qscale[rt];
+                    if (__any(mx > mrun[rt] + kSlack)) {
+                        mx = fmaxf(mx, __shfl_xor(mx, 16));
+                        mx = fmaxf(mx, __shfl_xor(mx, 32));
+                        const float mnew = fmaxf(mrun[rt], mx);
+                        const float r = exp2_fast(mrun[rt] - mnew);
+                        mrun[rt] = mnew;
+                        lrun[rt] *= r;
+#pragma unroll
+                        for (int t = 0; t < DT; t++) o[rt][t] *= r;
+                    }
+                    const float off = kBias - mrun[rt] + vlog;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < PER; e++) {
+                        x[e] = exp2_fast(fmaf(x[e], qscale[rt], off));
+                        sum += x[e];
+                        if constexpr (TYPE == kKvI8) {
+                            const float w = x[e] * vt.vs[e];
+                            x[e] = whole || x[e] != 0.f ? w : 0.f;  // (a scale that the row does not see may be NaN)
+                        }
+                    }
+                    lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
+#pragma unroll
+                    for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
+                }
+                if constexpr (TYPE != kKvI8) {
+                    if (!whole) {
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int t = 0; t < DT; t++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++) bad |= not_finite<Op>(vt.v[t][j]);
+                        if (__any(bad != 0)) {
+                            U128 seen[RT];
+#pragma unroll
+                            for (int rt = 0; rt < RT; rt++) seen[rt] = seen8(ok, pos[rt], key0, a.window, a.sinks);
+#pragma unroll
+                            for (int t = 0; t < DT; t++) {
+                                U128 marks;
+#pragma unroll
+                                for (int j = 0; j < 4; j++) {
+                                    const uint32_t b = not_finite<Op>(vt.v[t][j]);
+                                    vt.v[t][j] &= ~(b * 0xFFFFu);
+                                    marks.w[j] = b * kHuge;
+                                }
+#pragma unroll
+                                for (int rt = 0; rt < RT; rt++)
+                                    o[rt][t] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][t]);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < SUB; u++) {
+#pragma unroll
+                    for (int t = 0; t < DT; t++) {
+                        const Vec vx = vt.template op<Vec>(u, t);
+#pragma unroll
+                        for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                            for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
+                    }
+                }
+                if (more) vt.template load<NT>(c, h, ch.at(i + NW), vpage, g, m);
+                if (!more) break;
+                i += NW;
+                ok = vpage >= 0;
+                kpage = kpage2;
+                vpage = vpage2;
+            }
+        }
+
+        // join the waves: a common maximum, then the partial sums two by two
+        __shared__ float s_m[NW][RT * 16], s_l[NW][RT * 16];
+        __shared__ f32x4 s_o[2][RT * DT * 64];
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            lrun[rt] += __shfl_xor(lrun[rt], 16);
+            lrun[rt] += __shfl_xor(lrun[rt], 32);
+            if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; rt++) {
+            float mm = kNoMax;
+            for (int w = 0; w < NW; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
+            // (a NaN maximum cannot be: fmaxf drops NaN; a NaN sum stays)
+            const float r = exp2_fast(mrun[rt] - mm);
+            mrun[rt] = mm;
+            lrun[rt] *= r;
+            if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
+            const float ro = TYPE == kKvI8 ? r * vback : r;
+#pragma unroll
+            for (int t = 0; t < DT; t++) o[rt][t] *= ro;
+        }
+        for (int from = NW - 2; from >= 0; from -= 2) {
+            // waves from, from + 1 add to the two before them; last 1 to 0
+            const int w0 = from > 0 ? from : 1, n_from = from > 0 ? 2 : 1, to = from > 0 ? from - 2 : 0;
+            if (wave >= w0 && wave < w0 + n_from) {
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int t = 0; t < DT; t++) s_o[wave - w0][(rt * DT + t) * 64 + lane] = o[rt][t];
+            }
+            __syncthreads();
+            if (wave >= to && wave < to + n_from) {
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                    for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave - to][(rt * DT + t) * 64 + lane];
+            }
+            __syncthreads();
+        }
+        const bool direct = opens && closes && !ACC;
+        if (wave == 0) {
+            if (RANGES && blockIdx.y == 0 && lane == 0) {
+                if (opens) a.share[s].x = slot;
+                if (closes) a.share[s].y = slot;
             }
 #pragma unroll
-            for (int u = 0; u < SUB; u++) {
+            for (int rt = 0; rt < RT; rt++) {
+                const int rr = r0 + rt * 16 + m;
+                if (rr >= nrows) continue;
+                float l = 0.f;
+                for (int w = 0; w < NW; w++) l += s_l[w][rt * 16 + m];
+                float *dst;
+                float mul = 1.f;
+                if (direct) {
+                    const int j = rr / a.group, hg = rr % a.group;
+                    dst = a.out + (((int64_t)s * n + j) * a.n_heads + h * a.group + hg) * HD;
+                    mul = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
+                } else {
+                    const int64_t at = ((int64_t)slot * n + rr / a.group) * a.n_heads + h * a.group + rr % a.group;
+                    if (g == 0) a.part_ml[at] = make_float2(mrun[rt], l);
+                    dst = a.part_o + at * HD;
+                }
 #pragma unroll
                 for (int t = 0; t < DT; t++) {
-                    const Vec vx = vt.template op<Vec>(u, t);
-#pragma unroll
-                    for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                        for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
+                    const f32x4 v = o[rt][t] * mul;
+                    __builtin_memcpy(dst + 16 * t + 4 * g, &v, 16);
                 }
             }
-            if (more) vt.template load<NT>(c, h, ch.at(i + NW), vpage, g, m);
-            if (!more) break;
-            i += NW;
-            ok = vpage >= 0;
-            kpage = kpage2;
-            vpage = vpage2;
         }
+        if constexpr (!RANGES) return;
+        at += units;
+        s++;
+        if (s >= c.n_seq || at + kEnter >= hi) return;
+        len = clamp_len(__builtin_amdgcn_readfirstlane(next), a.limit);
+        __syncthreads();  // the joined waves' memory is used again
     }
+}
 
-    // join the waves: a common maximum, then the partial sums two by two
-    __shared__ float s_m[NW][RT * 16], s_l[NW][RT * 16];
-    __shared__ f32x4 s_o[2][RT * DT * 64];
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        lrun[rt] += __shfl_xor(lrun[rt], 16);
-        lrun[rt] += __shfl_xor(lrun[rt], 32);
-        if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        float mm = kNoMax;
-        for (int w = 0; w < NW; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
-        // (a NaN maximum cannot be: fmaxf drops NaN; a NaN sum stays)
-        const float r = exp2_fast(mrun[rt] - mm);
-        mrun[rt] = mm;
-        lrun[rt] *= r;
-        if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
-        const float ro = TYPE == kKvI8 ? r * vback : r;
-#pragma unroll
-        for (int t = 0; t < DT; t++) o[rt][t] *= ro;
-    }
-    for (int from = NW - 2; from >= 0; from -= 2) {
-        // waves from, from + 1 add to the two before them; last 1 to 0
-        const int w0 = from > 0 ? from : 1, n_from = from > 0 ? 2 : 1, to = from > 0 ? from - 2 : 0;
-        if (wave >= w0 && wave < w0 + n_from) {
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                for (int t = 0; t < DT; t++) s_o[wave - w0][(rt * DT + t) * 64 + lane] = o[rt][t];
-        }
-        __syncthreads();
-        if (wave >= to && wave < to + n_from) {
-#pragma unroll
-            for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave - to][(rt * DT + t) * 64 + lane];
-        }
-        __syncthreads();
-    }
-    if (wave != 0) return;
-    const bool direct = a.splits == 1 && !ACC;
-#pragma unroll
-    for (int rt = 0; rt < RT; rt++) {
-        const int rr = r0 + rt * 16 + m;
-        if (rr >= nrows) continue;
-        float l = 0.f;
-        for (int w = 0; w < NW; w++) l += s_l[w][rt * 16 + m];
-        float *dst;
-        float mul = 1.f;
-        if (direct) {
-            const int j = rr / a.group, hg = rr % a.group;
-            dst = a.out + (((int64_t)s * n + j) * a.n_heads + h * a.group + hg) * HD;
-            mul = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
-        } else {
-            const int64_t prow = ((int64_t)s * n + rr / a.group) * a.n_heads + h * a.group + rr % a.group;
-            const int64_t at = (int64_t)split * a.part_rows + prow;
-            if (g == 0) a.part_ml[at] = make_float2(mrun[rt], l);
-            dst = a.part_o + at * HD;
-        }
-#pragma unroll
-        for (int t = 0; t < DT; t++) {
-            const f32x4 v = o[rt][t] * mul;
-            __builtin_memcpy(dst + 16 * t + 4 * g, &v, 16);
-        }
-    }
+// First and last slot of sequence s.
+__device__ __forceinline__ int2 slots_of(const AttnArgs &a, int s) {
+    return a.parts ? a.share[s] : make_int2(s * a.splits, (s + 1) * a.splits - 1);
+}
+
+// Joins the pieces of row r of sequence s.
+template <int HD>
+__device__ __forceinline__ void join_pieces(const AttnArgs &a, int s, int r, int2 sh) {
+    const int64_t per = a.n * a.n_heads;
+    join_row<HD>(a, s * per + r, sh.x * per + r, per, sh.y - sh.x + 1);
+}
+
+template <int HD>
+__global__ __launch_bounds__(256) void attn_join_pieces(AttnArgs a) {
+    const int2 sh = slots_of(a, blockIdx.y);
+    if (sh.x != sh.y) join_pieces<HD>(a, blockIdx.y, blockIdx.x, sh);  // else the one workgroup wrote the row
 }
 
 // acc[s][h][key] += sum over the rows of 2^(x - m) / l, rows in order.
@@ -457,7 +610,8 @@ template <int TYPE, int HD>
 __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     constexpr int CK = kChunk<TYPE>;
     if (blockIdx.x < a.part_rows) {
-        join_row<HD>(a, blockIdx.x);
+        const uint32_t per = (uint32_t)(a.n * a.n_heads), s = blockIdx.x / per;
+        join_pieces<HD>(a, s, blockIdx.x % per, slots_of(a, s));
         return;
     }
     const int per = (a.limit + 255) / 256;  // workgroups a head
@@ -468,6 +622,9 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     if ((int64_t)block * 256 >= len) return;
     const int key = block * 256 + threadIdx.x;
     const int64_t head = (int64_t)s * a.c.n_kv + h;
+    const int2 sh = slots_of(a, s);
+    const int count = sh.y - sh.x + 1;
+    const int64_t per_seq = (int64_t)n * a.n_heads;
     __shared__ float s_m[16], s_r[16];
     float sum = 0.f;
     for (int r0 = 0; r0 < nrows; r0 += 16) {
@@ -475,13 +632,13 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
         const int row = threadIdx.x >> 4, l16 = threadIdx.x & 15;
         if (r0 + row < nrows) {
             const int rr = r0 + row;
-            const int64_t prow = ((int64_t)s * n + rr / a.group) * a.n_heads + h * a.group + rr % a.group;
+            const float2 *ml = a.part_ml + sh.x * per_seq + (int64_t)(rr / a.group) * a.n_heads + h * a.group + rr % a.group;
             float mm = kNoMax, l = 0.f;
-            for (int i = l16; i < a.splits; i += 16) mm = fmaxf(mm, a.part_ml[i * a.part_rows + prow].x);
+            for (int i = l16; i < count; i += 16) mm = fmaxf(mm, ml[i * per_seq].x);
             for (int off = 8; off; off >>= 1) mm = fmaxf(mm, __shfl_xor(mm, off, 16));
-            for (int i = l16; i < a.splits; i += 16) {
-                const float2 ml = a.part_ml[i * a.part_rows + prow];
-                l += exp2_fast(ml.x - mm) * ml.y;
+            for (int i = l16; i < count; i += 16) {
+                const float2 x = ml[i * per_seq];
+                l += exp2_fast(x.x - mm) * x.y;
             }
             for (int off = 8; off; off >>= 1) l += __shfl_xor(l, off, 16);
             if (l16 == 0) {
@@ -509,20 +666,27 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     if (key < len) a.acc[head * a.ld_acc + key] += sum;
 }
 
+template <int TYPE, int HD, int RT, int NW, bool RANGES>
+hipError_t launch_main_of(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    const dim3 grid(RANGES ? p.parts : p.splits, a.c.n_kv * p.tiles, RANGES ? 1 : a.c.n_seq);
+    if (a.acc) return launch_main(attn_decode<TYPE, HD, RT, NW, true, RANGES>, grid, dim3(NW * 64), 0, s, a);
+    return launch_main(attn_decode<TYPE, HD, RT, NW, false, RANGES>, grid, dim3(NW * 64), 0, s, a);
+}
+
 template <int TYPE, int HD, int RT, int NW>
 hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
-    const dim3 grid(p.splits, a.c.n_kv * p.tiles, a.c.n_seq);
-    hipError_t e;
-    if (a.acc)
-        e = launch_main(attn_decode<TYPE, HD, RT, NW, true>, grid, dim3(NW * 64), 0, s, a);
-    else
-        e = launch_main(attn_decode<TYPE, HD, RT, NW, false>, grid, dim3(NW * 64), 0, s, a);
+    hipError_t e = hipErrorInvalidValue;
+    if (!p.parts)
+        e = launch_main_of<TYPE, HD, RT, NW, false>(a, p, s);
+    else if constexpr (RT == 2 || NW == 4)  // 16-row tiles of eight waves are for short calls
+        e = launch_main_of<TYPE, HD, RT, NW, true>(a, p, s);
     if (e != hipSuccess) return e;
     if (a.acc) {
         const int64_t blocks = p.part_rows + (int64_t)a.c.n_seq * a.c.n_kv * ((a.limit + 255) / 256);
         return launch_aux(attn_join_weights<TYPE, HD>, dim3((uint32_t)blocks), dim3(256), 0, s, a, 16 * RT);
     }
-    return p.splits > 1 ? launch_attn_join(a, s) : hipSuccess;
+    if (p.slots == a.c.n_seq) return hipSuccess;
+    return launch_aux(attn_join_pieces<HD>, dim3((uint32_t)(a.n * a.n_heads), a.c.n_seq), dim3(256), 0, s, a);
 }
 
 // Whether the 256 registers that eight waves leave each lane hold the kernel's
@@ -579,27 +743,37 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
         if (w < most) most = w;
     }
     const int64_t chunks = (most + ck - 1) / ck;
-    const int64_t base = n_seq * n_kv * p.tiles;
     // Eight waves fit a compute unit of 256: two workgroups of four.  Sequences
-    // that may differ in length get twice that, for balance (the ragged batch
-    // above: 134 us with 512, 131 with 1024); one sequence or a window does
-    // not (131071 8-bit positions: 60 against 64 us), and tiles of 32 rows
-    // take one workgroup, of eight waves (the drafted tokens: 24 us against 26
-    // with 512 of four and 34 with 1024) or, where registers say so, of four.
-    const int64_t want = p.rt == 2 ? 256 : n_seq == 1 || window > 0 ? 512 : 1024;
+    // get twice as many, for balance; one sequence or a window does not (131071
+    // 8-bit positions: 60 against 64 us), and tiles of 32 rows take one
+    // workgroup, of eight waves (the drafted tokens: 24 us against 26 with 512
+    // of four and 34 with 1024) or, where registers say so, of four.
+    const int64_t heads = (int64_t)n_kv * p.tiles, base = n_seq * heads;
+    const int64_t fit = p.rt == 2 ? 256 : 512, want = p.rt == 2 || n_seq == 1 || window > 0 ? fit : 2 * fit;
     int64_t splits = (want + base - 1) / base;
     if (splits > chunks / 8) splits = chunks / 8;    // at least a chunk, with four waves two, per wave
     if (splits > 128) splits = 128;
     p.splits = splits < 1 ? 1 : (int)splits;
+    p.slots = (int)(n_seq * p.splits);
+    // Where such a piece may be long, lengths decide: evenly cut ranges.
+    const int waves = p.rt == 2 && eight_fit(type, hd, 2) ? 8 : 4;
+    if (n_seq > 1 && n_seq <= 1024 && chunks > 5 * waves * p.splits && chunks * n_seq < (1ll << 30) &&
+        p.part_rows < (1ll << 24)) {
+        p.parts = (int)((fit + heads - 1) / heads);
+        p.slots = (int)(p.parts + n_seq);
+    }
     // a launch of few, unsplit workgroups is a chain of latencies: eight waves
     // halve the chunks in it (301 positions, 3 heads: 7.3 -> 6.6 us)
-    p.waves = eight_fit(type, hd, p.rt) && (p.rt == 2 || (p.splits == 1 && base <= 256)) ? 8 : 4;
+    p.waves = eight_fit(type, hd, p.rt) && (p.rt == 2 || (p.slots == n_seq && base <= 256)) ? 8 : 4;
     size_t at = 0;
-    if (p.splits > 1 || with_acc) {
+    if (p.slots > n_seq || with_acc) {
+        const size_t pieces = (size_t)p.slots * n * n_kv * group;
         p.ml_off = at;
-        at = up256(at + sizeof(float2) * (size_t)p.splits * p.part_rows);
+        at = up256(at + sizeof(float2) * pieces);
         p.o_off = at;
-        at = up256(at + sizeof(float) * (size_t)p.splits * p.part_rows * hd);
+        at = up256(at + sizeof(float) * pieces * hd);
+        p.share_off = at;
+        at = up256(at + sizeof(int2) * n_seq);
     }
     if (with_acc) {
         p.ld_logits = (max_len + ck - 1) / ck * ck;

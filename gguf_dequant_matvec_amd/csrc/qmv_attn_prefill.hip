@@ -481,7 +481,7 @@ __global__ __launch_bounds__(256) void attn_join(AttnArgs a) {
         const int64_t row = prow / a.n_heads;
         if (row < a.start[0] || row >= a.start[a.c.n_seq]) return;
     }
-    join_row<HD>(a, prow);
+    join_row<HD>(a, prow, prow, a.part_rows, a.splits);
 }
 
 template <int TYPE, int HD>
@@ -492,7 +492,7 @@ hipError_t launch_typed(const AttnArgs &a, int64_t slots, hipStream_t s) {
     const dim3 grid(a.c.n_kv, (uint32_t)slots, a.splits);
     e = launch_main(attn_prefill<TYPE, HD>, grid, dim3(256), Lds<HD>::kTotal(TYPE), s, a);
     if (e != hipSuccess || a.splits == 1) return e;
-    return launch_attn_join(a, s);
+    return launch_aux(attn_join<HD>, dim3((uint32_t)a.part_rows), dim3(256), 0, s, a);
 }
 
 template <int TYPE>
@@ -509,17 +509,6 @@ hipError_t launch_type(const AttnArgs &a, int64_t slots, hipStream_t s) {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
-
-hipError_t launch_attn_join(const AttnArgs &a, hipStream_t s) {
-    const dim3 grid((uint32_t)a.part_rows);
-    switch (a.c.hd) {
-    case 64: return launch_aux(attn_join<64>, grid, dim3(256), 0, s, a);
-    case 96: return launch_aux(attn_join<96>, grid, dim3(256), 0, s, a);
-    case 128: return launch_aux(attn_join<128>, grid, dim3(256), 0, s, a);
-    case 256: return launch_aux(attn_join<256>, grid, dim3(256), 0, s, a);
-    default: return hipErrorInvalidValue;
-    }
-}
 
 AttnPlan attn_prefill_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int64_t rows,
                            int64_t max_len, int window, int sinks) {

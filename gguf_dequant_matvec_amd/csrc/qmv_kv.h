@@ -82,12 +82,15 @@ struct AttnArgs {
     int32_t n_heads, group;  // query heads, query heads per key-value head
     int32_t window, sinks;   // window 0: none
     int32_t limit;           // longest sequence (max_len, and what the table addresses)
-    int32_t tiles, splits;
+    int32_t tiles, splits;   // splits: pieces of each sequence's length
+    int32_t parts;           // decode, not 0: instead, workgroups of a head over all sequences
     float scale_log2;        // |scale| * log2(e), not zero
     float q_sign;            // what queries are multiplied by: the scale's sign (0 for scale 0)
-    float2 *part_ml;         // [splits][part_rows] running maximum and sum
-    float *part_o;           // [splits][part_rows][hd]
-    int64_t part_rows;       // rows * n_heads; piece i of output row r is at i * part_rows + r
+    float2 *part_ml;         // running maximum and sum of each piece of an output row
+    float *part_o;           // [hd] of each
+    int64_t part_rows;       // rows * n_heads; prompts: piece i of output row r is at i * part_rows + r
+    int2 *share;             // parts: first and last slot of each sequence; decode: the piece of a sequence's
+                             // row r in a slot is at slot * n * n_heads + r
     float *logits;           // [n_seq][n_kv][n * group][ld_logits], base-2 logits (weights wanted)
     int64_t ld_logits;
     float *acc;              // [n_seq][n_kv][ld_acc]
@@ -95,20 +98,19 @@ struct AttnArgs {
 };
 
 // How a call is cut: 16-row operand tiles per wave, row tiles per key-value
-// head, pieces of the cache's length, waves per workgroup; workspace offsets in bytes.
+// head, pieces of the cache's length (as in AttnArgs), slots for the pieces of
+// a decode call, waves per workgroup; workspace offsets in bytes.
 struct AttnPlan {
-    int rt, tiles, splits, waves;
+    int rt, tiles, splits, parts, slots, waves;
     int64_t part_rows;
     int64_t ld_logits;
-    size_t ml_off, o_off, logits_off, bytes;
+    size_t ml_off, o_off, share_off, logits_off, bytes;
 };
 AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int n,
                           int64_t max_len, int window, int sinks, bool with_acc);
 hipError_t launch_attn_decode(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s);
 AttnPlan attn_prefill_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int64_t rows,
                            int64_t max_len, int window, int sinks);
-// Joins the pieces of every row (out = the pieces' weighted sum).
-hipError_t launch_attn_join(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attn_prefill(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s);
 
 }  // namespace qmv

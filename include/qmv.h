@@ -436,8 +436,8 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * q: f32, row r at q + r * ldq, n_heads * head_dim values.  out: f32
  * [n_seq * n][n_heads * head_dim].  n_heads a multiple of n_kv_heads.
  * max_len: the longest seq_len of the call (longer ones are taken as max_len,
- * or as what a table row addresses); it sizes the workspace and decides into
- * how many pieces the length is split.  With acc, n_seq * n * n_heads +
+ * or as what a table row addresses); it sizes the workspace and decides whether
+ * lengths are split.  With acc, n_seq * n * n_heads +
  * n_seq * n_kv_heads * ceil(max_len / 256) < 2^24.
  * acc: NULL, or f32 [n_seq][n_kv_heads][ld_acc], ld_acc >= max_len: position
  * t of key-value head h gets, added, the weights w_t of the n tokens and of the
@@ -446,7 +446,8 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * pieces (f16 hi + lo, bf16 in three), maximum, sum and output are f32.  f16
  * and 8-bit caches resolve weights (8-bit: weight times V row scale) down to
  * 2^-36 of the largest, the latter for V row scales between 2^-100 and 2^100.
- * Results do not depend on anything but the arguments.
+ * Results do not depend on anything but the arguments; a row's last bits may
+ * depend on the call's other lengths, which decide where long ones are cut.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is
  * 0), 16-byte aligned, no initial contents needed.  One launch, a second one
  * to join the pieces when the length is split or acc is given. */

@@ -224,6 +224,75 @@ def test_decode_split(t, window, sinks):
     run_decode(c, 4, 8, window=window, sinks=sinks, with_acc=True)
 
 
+RAGGED = [2700, 0, 1, 64, 700, 31, 5200, 0, 0, 33] + [(37 * i) % 90 for i in range(30)]
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,heads,n,window,sinks", [(64, 16, 1, 0, 0), (64, 16, 5, 5000, 9), (64, 16, 16, 0, 0),
+                                                     (96, 8, 1, 5100, 0), (128, 8, 3, 0, 0), (64, 64, 11, 4900, 70)])
+def test_decode_ragged(t, hd, heads, n, window, sinks):
+    """Long sequences among short and empty ones: workgroups that take parts of
+    several sequences, tiles that see different chunks."""
+    c, _ = make_cache(t, 8, hd, 64, RAGGED, 71)
+    run_decode(c, n, heads, window=window, sinks=sinks, with_acc=n in (3, 5))
+
+
+@pytest.mark.parametrize("t", ["f16", "i8"])
+def test_decode_ragged_256_columns(t):
+    c, _ = make_cache(t, 8, 256, 64, RAGGED, 72)
+    run_decode(c, 2, 16, with_acc=True)
+
+
+@pytest.mark.parametrize("t", ["bf16", "i8"])
+@pytest.mark.parametrize("n", [1, 16])
+def test_decode_hundreds_ragged(t, n):
+    """More sequences than a wave has at a time, the long ones behind them; one key-value head."""
+    lens = [(61 * i) % 120 for i in range(600)]
+    lens[5], lens[257], lens[300], lens[599] = 1900, 0, 1300, 1700
+    c, _ = make_cache(t, 1, 64, 16, lens, 73)
+    run_decode(c, n, 3, with_acc=n == 1)
+    c.seq_len[:] = np.minimum(c.seq_len, 3)     # far fewer chunks than workgroups
+    run_decode(c, n, 3)
+
+
+def test_decode_ragged_follows_lengths():
+    """The same call captured once: each replay cuts by the lengths it finds."""
+    c, rng = make_cache("f16", 8, 64, 64, RAGGED, 74)
+    d = Dev(c)
+    x = dev(synth.normal(2, synth.T_X, (len(RAGGED), 16 * 64)))
+    out = torch.zeros(len(RAGGED), 16 * 64, device="cuda")
+    ws = workspace(q.qmv_attn_decode_workspace(d.h, 1, 16, c.cap))
+
+    def fn():
+        q.qmv_attn_decode(d.h, 1, 16, x, 0.125, out, c.cap, workspace=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fn()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fn()
+    full = np.array(RAGGED, np.int32)
+    for rep in range(4):
+        lens = np.minimum(full, [5200, 40, 2600, 0][rep]).astype(np.int32)
+        d.lens.copy_(dev(lens))
+        out.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        got = host(out).copy()
+        ws.fill_(0xFF)
+        out.fill_(7)
+        fn()
+        torch.cuda.synchronize()
+        assert np.array_equal(got, host(out)), rep
+        c.seq_len[:] = lens
+        want, tol, _, _ = ref.attention(c, np.arange(len(RAGGED) + 1), host(x).reshape(-1, 16, 64), 0.125, c.cap)
+        close(got.reshape(want.shape), want, tol, f"replay {rep}")
+
+
 @pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
 def test_decode_holes(t):
     """Positions in holes are not seen: released pages of a window, a row whose
