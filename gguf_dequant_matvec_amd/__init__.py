@@ -153,6 +153,7 @@ def _ptr(a) -> int:
 
 _torch_module = None
 _raw_stream = None   # () -> address of torch's current stream on the current device
+_raw_stream_on = None   # device -> address of torch's current stream there
 
 
 def _torch():
@@ -166,7 +167,7 @@ def _torch():
 def _find_raw_stream():
     """torch's current stream without building a Stream object for every call
     (0.6 us instead of 3.5 us of a small call's time); null without a GPU."""
-    global _raw_stream
+    global _raw_stream, _raw_stream_on
     import torch
     if not torch.cuda.is_available():
         return 0
@@ -175,6 +176,7 @@ def _find_raw_stream():
         _raw_stream = lambda: int(torch.cuda.current_stream().cuda_stream)  # noqa: E731
     else:
         device = torch.cuda.current_device
+        _raw_stream_on = get
         _raw_stream = lambda: get(device())  # noqa: E731
     return _raw_stream()
 
@@ -203,7 +205,7 @@ def _cache_stream(cache, stream, *tensors) -> int:
         raise ValueError(f"the cache is on GPU {on}, which is not the current one")
     if stream is not None and not isinstance(stream, int) and stream.device_index != on:
         raise ValueError(f"a stream of GPU {stream.device_index}, the cache on GPU {on}")
-    return _stream(stream)
+    return _raw_stream_on(on) if stream is None and _raw_stream_on is not None else _stream(stream)
 
 
 def _type(t) -> int:

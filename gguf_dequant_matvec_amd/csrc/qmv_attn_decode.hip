@@ -208,8 +208,12 @@ __device__ __forceinline__ Range find_range(const AttnArgs &a, int p, int lane) 
     return r;
 }
 
+// Workgroups of four waves and 16-row tiles that the registers of a compute
+// unit hold at once.
+constexpr int resident(int type, int hd) { return hd == 64 && type != kKvI8 ? 3 : 2; }
+
 template <int TYPE, int HD, int RT, int NW, bool ACC, bool RANGES>
-__global__ __launch_bounds__(NW * 64, RANGES && RT == 1 && HD <= 128 ? 2 : 1) void attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, RANGES && RT == 1 && HD <= 128 ? resident(TYPE, HD) : 1) void attn_decode(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
     constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
@@ -743,13 +747,15 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
         if (w < most) most = w;
     }
     const int64_t chunks = (most + ck - 1) / ck;
-    // Eight waves fit a compute unit of 256: two workgroups of four.  Sequences
-    // get twice as many, for balance; one sequence or a window does not (131071
+    // Workgroups for 256 compute units: as many as fit at once, of four waves
+    // two (three of 64 16-bit columns: 32 sequences of 6144 positions 74.2 ->
+    // 72.3 us, 1024 would be 80.6).  Equal numbers of pieces
+    // for several sequences get twice that, for balance; one sequence or a window does not (131071
     // 8-bit positions: 60 against 64 us), and tiles of 32 rows take one
     // workgroup, of eight waves (the drafted tokens: 24 us against 26 with 512
     // of four and 34 with 1024) or, where registers say so, of four.
     const int64_t heads = (int64_t)n_kv * p.tiles, base = n_seq * heads;
-    const int64_t fit = p.rt == 2 ? 256 : 512, want = p.rt == 2 || n_seq == 1 || window > 0 ? fit : 2 * fit;
+    const int64_t fit = 256 * (p.rt == 2 ? 1 : resident(type, hd)), want = p.rt == 2 || n_seq == 1 || window > 0 ? fit : 2 * fit;
     int64_t splits = (want + base - 1) / base;
     if (splits > chunks / 8) splits = chunks / 8;    // at least a chunk, with four waves two, per wave
     if (splits > 128) splits = 128;
