@@ -209,11 +209,11 @@ __device__ __forceinline__ Range find_range(const AttnArgs &a, int p, int lane) 
 }
 
 // Workgroups of four waves and 16-row tiles that the registers of a compute
-// unit hold at once.
-constexpr int resident(int type, int hd) { return hd == 64 && type != kKvI8 ? 3 : 2; }
+// unit hold at once (256 columns take more than half of them).
+constexpr int resident(int type, int hd) { return hd == 256 ? 1 : hd == 64 && type != kKvI8 ? 3 : 2; }
 
 template <int TYPE, int HD, int RT, int NW, bool ACC, bool RANGES>
-__global__ __launch_bounds__(NW * 64, RANGES && RT == 1 && HD <= 128 ? resident(TYPE, HD) : 1) void attn_decode(AttnArgs a) {
+__global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1) void attn_decode(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
     constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
@@ -747,23 +747,28 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
         if (w < most) most = w;
     }
     const int64_t chunks = (most + ck - 1) / ck;
-    // Workgroups for 256 compute units: as many as fit at once, of four waves
-    // two (three of 64 16-bit columns: 32 sequences of 6144 positions 74.2 ->
-    // 72.3 us, 1024 would be 80.6).  Equal numbers of pieces
-    // for several sequences get twice that, for balance; one sequence or a window does not (131071
-    // 8-bit positions: 60 against 64 us), and tiles of 32 rows take one
-    // workgroup, of eight waves (the drafted tokens: 24 us against 26 with 512
-    // of four and 34 with 1024) or, where registers say so, of four.
+    // Workgroups for 256 compute units: as many as fit at once, because a second
+    // round of them waits for its lengths, table and first rows again (16
+    // sequences of 8192 positions of 256 columns: one workgroup a unit 101 us,
+    // two 113; 32 of 6144 of 64 columns: three 72 us, two 74, four 81).  Tiles of
+    // 32 rows take one workgroup, of eight waves (the drafted tokens: 24 us
+    // against 26 with 512 of four and 34 with 1024) or, where registers say so,
+    // of four.
     const int64_t heads = (int64_t)n_kv * p.tiles, base = n_seq * heads;
-    const int64_t fit = 256 * (p.rt == 2 ? 1 : resident(type, hd)), want = p.rt == 2 || n_seq == 1 || window > 0 ? fit : 2 * fit;
-    int64_t splits = (want + base - 1) / base;
+    const int64_t fit = 256 * (p.rt == 2 ? 1 : resident(type, hd));
+    int64_t splits = (fit + base - 1) / base;
     if (splits > chunks / 8) splits = chunks / 8;    // at least a chunk, with four waves two, per wave
     if (splits > 128) splits = 128;
     p.splits = splits < 1 ? 1 : (int)splits;
     p.slots = (int)(n_seq * p.splits);
-    // Where such a piece may be long, lengths decide: evenly cut ranges.
+    // Where such a piece may be long, lengths decide: evenly cut ranges.  With
+    // sequences enough for all workgroups the grid's own order balances them
+    // better (512 of 768 to 1536 positions: 409 against 422 us; but 128 of 1 to
+    // 2048: 117 against 96), so the more there are, the longer the longest
+    // has to be.
     const int waves = p.rt == 2 && eight_fit(type, hd, 2) ? 8 : 4;
-    if (n_seq > 1 && n_seq <= 1024 && chunks > 5 * waves * p.splits && chunks * n_seq < (1ll << 30) &&
+    const int64_t long_chunks = base < fit ? 5 * waves * p.splits : 8 * waves * base / fit;
+    if (n_seq > 1 && n_seq <= 1024 && chunks >= long_chunks && chunks * n_seq < (1ll << 30) &&
         p.part_rows < (1ll << 24)) {
         p.parts = (int)((fit + heads - 1) / heads);
         p.slots = (int)(p.parts + n_seq);

@@ -237,6 +237,14 @@ def test_decode_ragged(t, hd, heads, n, window, sinks):
     run_decode(c, n, heads, window=window, sinks=sinks, with_acc=n in (3, 5))
 
 
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("hd,n,window,sinks", [(64, 11, 5000, 70), (64, 9, 0, 0), (128, 16, 5100, 3), (256, 5, 5000, 40)])
+def test_decode_ragged_tiles(t, hd, n, window, sinks):
+    """Several row tiles, whose rows see different chunks, of two key-value heads."""
+    c, _ = make_cache(t, 2, hd, 64, RAGGED, 75)
+    run_decode(c, n, 2 * (48 // n), window=window, sinks=sinks, with_acc=n == 9)
+
+
 @pytest.mark.parametrize("t", ["f16", "i8"])
 def test_decode_ragged_256_columns(t):
     c, _ = make_cache(t, 8, 256, 64, RAGGED, 72)
