@@ -223,8 +223,8 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
     // -> 136 us).  More rows come with drafted tokens, whose tiles may read
     // the same chunks: ordinary loads (8 x 8 tokens, window 4096: 34 against 37
     // us).  256 columns always take 16-row tiles, one or several of them:
-    // ordinary (16 x 8192 positions, 4 tiles: 259 against 334 us, one tile: 116
-    // against 113).
+    // ordinary (16 x 8192 positions, 4 tiles: 259 against 334 us, one tile, both
+    // with two workgroups a unit: 116 against 113).
     constexpr bool NT = RT == 1 && HD <= 128;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
