@@ -771,6 +771,7 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
     if (n_seq > 1 && n_seq <= 1024 && chunks >= long_chunks && chunks * n_seq < (1ll << 30) &&
         p.part_rows < (1ll << 24)) {
         p.parts = (int)((fit + heads - 1) / heads);
+        if (p.parts > kMaxPieces) p.parts = kMaxPieces;  // one sequence may take all of them
         p.slots = (int)(p.parts + n_seq);
     }
     // a launch of few, unsplit workgroups is a chain of latencies: eight waves

@@ -263,6 +263,13 @@ def test_decode_hundreds_ragged(t, n):
     run_decode(c, n, 3)
 
 
+@pytest.mark.parametrize("t,longest", [("f16", 90000), ("i8", 170000)])
+def test_decode_one_sequence_takes_all(t, longest):
+    """One key-value head: every workgroup of the launch is the long sequence's."""
+    c, _ = make_cache(t, 1, 64, 256, [longest, 10, 0], 76)
+    run_decode(c, 1, 2)
+
+
 def test_decode_ragged_follows_lengths():
     """The same call captured once: each replay cuts by the lengths it finds."""
     c, rng = make_cache("f16", 8, 64, 64, RAGGED, 74)
