@@ -440,12 +440,12 @@ def _f32_rows(name, a, ld, n, width):
         raise ValueError(f"{name} must be float32")
     if ld is None:
         shape, stride = a.shape, a.stride()
-        inner = width
+        inner = 1
         for i in range(len(shape) - 1, 0, -1):    # every dimension but the first is one row
-            if shape[i] > 1 and stride[i] != width // inner:
+            if shape[i] > 1 and stride[i] != inner:
                 raise ValueError(f"the rows of {name} must be contiguous")
-            inner //= max(shape[i], 1)
-        if len(shape) < 2 or shape[0] < n or inner != 1:
+            inner *= shape[i]
+        if len(shape) < 2 or shape[0] < n or inner != width:
             raise ValueError(f"{name} must be {n} rows of {width} values")
         ld = stride[0] if n > 1 else width
     return ld

@@ -188,6 +188,33 @@ def test_binding_refusals():
         q.qmv_kv_evict(c, table, 8, 0, 0, z(2, 2, 64), z(2, 2, 8), z(2, 2, 8), lens, stream=0)
 
 
+def test_binding_row_widths():
+    """Rows that are not exactly as wide as the call takes them: a kernel would
+    read past a single short row, and the neighbouring columns of a wider matrix."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    pages, table, lens = z(8 * 8192, dtype=torch.uint8), z(2, 4, dtype=torch.int32), z(2, dtype=torch.int32)
+    c = q.KvCache("f16", 2, 64, 16, pages, table, lens)
+    c1 = q.KvCache("f16", 2, 64, 16, pages, table, lens, n_seq=1)
+    wide = z(4, 512)
+    for a in (z(2, 100), z(2, 65), z(2, 127), z(2, 129), z(2, 192), z(2, 1, 100), z(2, 2, 63), z(2, 3, 43), wide[:, :100],
+              wide[:, :127], wide[:, :200], z(2, 128, 2)[:, :, 0], z(2, 0), z(2, 0, 128), z(2, 1, 2, 33)):
+        for k, v in ((a, z(2, 128)), (z(2, 128), a)):
+            with pytest.raises(ValueError, match="rows of"):
+                q.qmv_kv_append(c, 2, k, v, stream=0)
+    for a in (z(1, 100), z(1, 65), z(1, 129), z(1, 2, 33)):      # one row: the single-user step
+        with pytest.raises(ValueError, match="rows of"):
+            q.qmv_kv_append(c1, 1, a, z(1, 128), stream=0)
+        with pytest.raises(ValueError, match="rows of"):
+            q.qmv_attn_decode(c1, 1, 2, a, 0.1, z(1, 128), 64, stream=0)
+        with pytest.raises(ValueError, match="rows of"):
+            q.qmv_attn_prefill(c1, 1, 2, a, 0.1, z(1, 128), 64, stream=0)
+    # what is a row: any shape of the right size, in any wider matrix
+    for a in (z(2, 128), z(2, 2, 64), z(2, 1, 128), z(2, 2, 1, 64), wide[:, 100:228], wide[1:, :128], z(2, 2, 2, 32)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            q.qmv_kv_append(c, 2, a, a, stream=0)
+
+
 def test_cache_of_host_tensors():
     """Calls over tensors that are not on a GPU end on the host; a cache's
     tensors cannot be exchanged behind its addresses."""
