@@ -215,6 +215,23 @@ def test_binding_row_widths():
             q.qmv_kv_append(c, 2, a, a, stream=0)
 
 
+def test_binding_workspaces():
+    """A workspace is as many bytes as its tensor spans, in one piece."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    c = q.KvCache("f16", 2, 64, 16, z(8 * 8192, dtype=torch.uint8), z(2, 4, dtype=torch.int32), z(2, dtype=torch.int32))
+    x = z(2, 256)
+    for ws, kw in ((z(1).expand(1 << 20), {}), (z(64, 64)[:, :8], {}), (z(1 << 12)[::2], {}),
+                   (z(100), dict(ws_bytes=401)), (z(100)[50:], dict(ws_bytes=204))):
+        with pytest.raises(ValueError, match="workspace"):
+            q.qmv_attn_decode(c, 1, 4, x, 0.1, z(2, 256), 64, workspace=ws, stream=0, **kw)
+        with pytest.raises(ValueError, match="workspace"):
+            q.qmv_attn_prefill(c, 2, 4, x, 0.1, z(2, 256), 64, workspace=ws, stream=0, **kw)
+    for ws, kw in ((z(64, 64), {}), (z(100), dict(ws_bytes=400)), (z(100)[50:], dict(ws_bytes=200)), (None, {})):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            q.qmv_attn_decode(c, 1, 4, x, 0.1, z(2, 256), 64, workspace=ws, stream=0, **kw)
+
+
 def test_cache_of_host_tensors():
     """Calls over tensors that are not on a GPU end on the host; a cache's
     tensors cannot be exchanged behind its addresses."""
