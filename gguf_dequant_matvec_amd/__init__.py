@@ -464,6 +464,16 @@ def _check_dense(name, a, dtype, numel):
             raise ValueError(f"{name} must hold {numel} contiguous {dtype} values")
 
 
+def _workspace_bytes(workspace, ws_bytes):
+    """Bytes of a workspace: what its tensor spans, or fewer if the caller says so."""
+    if workspace is None or isinstance(workspace, int):
+        return 0 if ws_bytes is None else ws_bytes
+    have = workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous() or (ws_bytes is not None and ws_bytes > have):
+        raise ValueError(f"workspace must be contiguous and hold {have if ws_bytes is None else ws_bytes} bytes")
+    return have if ws_bytes is None else ws_bytes
+
+
 def qmv_kv_append(cache, n, k, v, start=None, ldk=None, ldv=None, stream=None):
     width = cache.n_kv_heads * cache.head_dim
     ldk, ldv = _f32_rows("k", k, ldk, n, width), _f32_rows("v", v, ldv, n, width)
@@ -492,8 +502,7 @@ def qmv_attn_decode(cache, n, n_heads, q, scale, out, max_len, window=0, sinks=0
     ldq = _f32_rows("q", q, ldq, cache.n_seq * n, n_heads * cache.head_dim)
     _check_dense("out", out, "float32", cache.n_seq * n * n_heads * cache.head_dim)
     ld_acc = _head_rows("acc", acc, ld_acc, cache)
-    if ws_bytes is None:
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_bytes = _workspace_bytes(workspace, ws_bytes)
     _call("qmv_attn_decode", cache._address, n, n_heads, _ptr(q), ldq, scale, window, sinks,
           _ptr(out), max_len, _ptr(acc), ld_acc, _ptr(workspace), ws_bytes,
           _cache_stream(cache, stream, q, out, acc, workspace))
@@ -508,8 +517,7 @@ def qmv_attn_prefill(cache, n, n_heads, q, scale, out, max_len, start=None, wind
     ldq = _f32_rows("q", q, ldq, n, n_heads * cache.head_dim)
     _check_dense("out", out, "float32", n * n_heads * cache.head_dim)
     _check_start(cache, start)
-    if ws_bytes is None:
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws_bytes = _workspace_bytes(workspace, ws_bytes)
     _call("qmv_attn_prefill", cache._address, n, _ptr(start), n_heads, _ptr(q), ldq, scale, window,
           sinks, _ptr(out), max_len, _ptr(workspace), ws_bytes,
           _cache_stream(cache, stream, start, q, out, workspace))
