@@ -433,11 +433,16 @@ def qmv_kv_page_bytes(t, n_kv_heads, head_dim, page_size) -> int:
 
 
 def _f32_rows(name, a, ld, n, width):
-    """Leading dimension of n rows of `width` f32 values."""
+    """Leading dimension of n rows of `width` f32 values: what the tensor's shape
+    says, or `ld` from its first value on, as far as its storage reaches."""
     if a is None or isinstance(a, int):
         return width if ld is None else ld
     if a.dtype is not _torch().float32:
         raise ValueError(f"{name} must be float32")
+    if ld is not None:
+        have = a.untyped_storage().nbytes() // 4 - a.storage_offset()
+        if (n - 1) * ld + width > have:
+            raise ValueError(f"{name} holds {have} values, not {n} rows {ld} apart")
     if ld is None:
         shape, stride = a.shape, a.stride()
         inner = 1
@@ -494,6 +499,8 @@ def _head_rows(name, a, ld, cache):
     if a.dtype is not _torch().float32 or a.dim() != 3 or not a.is_contiguous() or \
             a.shape[0] < cache.n_seq or a.shape[1] != cache.n_kv_heads:
         raise ValueError(f"{name} must be contiguous float32 [n_seq][n_kv_heads][positions]")
+    if ld is not None and ld != a.shape[2]:
+        raise ValueError(f"the heads of {name} have {a.shape[2]} positions, not {ld}")
     return a.shape[2]
 
 
@@ -529,6 +536,8 @@ def qmv_kv_evict(cache, dst_table, keep, first, recent, acc, kept, acc_out, len_
         if dst_table is None or dst_table.dim() != 2 or dst_table.shape[0] < cache.n_seq:
             raise ValueError("dst_table must be a matrix with a row per sequence")
         _check_dense("dst_table", dst_table, "int32", 0)
+        if dst_ld is not None and dst_ld != dst_table.shape[1]:
+            raise ValueError(f"the rows of dst_table have {dst_table.shape[1]} entries, not {dst_ld}")
         dst_ld = dst_table.shape[1]
     ld_acc = _head_rows("acc", acc, ld_acc, cache)
     ld_out = _head_rows("acc_out", acc_out, ld_out, cache)

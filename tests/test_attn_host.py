@@ -232,6 +232,38 @@ def test_binding_workspaces():
             q.qmv_attn_decode(c, 1, 4, x, 0.1, z(2, 256), 64, workspace=ws, stream=0, **kw)
 
 
+def test_binding_explicit_strides():
+    """Strides given beside a tensor: the rows must lie in its storage, and a
+    stride that the tensor's own shape says must be that."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    pages, table, lens = z(8 * 8192, dtype=torch.uint8), z(2, 4, dtype=torch.int32), z(2, dtype=torch.int32)
+    c = q.KvCache("f16", 2, 64, 16, pages, table, lens)
+    k = z(2, 128)
+    flat = z(1000)
+    for a, ld in ((flat, 873), (flat[1:], 872), (flat[900:], 128), (z(1, 100), 128), (z(4), 128), (flat.half(), 128)):
+        for kw in (dict(k=a, v=k, ldk=ld), dict(k=k, v=a, ldv=ld)):
+            with pytest.raises(ValueError, match="k must|v must|k holds|v holds"):
+                q.qmv_kv_append(c, 2, stream=0, **kw)
+    for a, ld in ((flat, 745), (z(1, 300), 256), (flat[600:], 256)):
+        with pytest.raises(ValueError, match="q holds"):
+            q.qmv_attn_decode(c, 1, 4, a, 0.1, z(2, 256), 64, ldq=ld, stream=0)
+        with pytest.raises(ValueError, match="q holds"):
+            q.qmv_attn_prefill(c, 2, 4, a, 0.1, z(2, 256), 64, ldq=ld, stream=0)
+    with pytest.raises(ValueError, match="acc"):
+        q.qmv_attn_decode(c, 1, 4, z(2, 256), 0.1, z(2, 256), 64, acc=z(2, 2, 64), ld_acc=80, stream=0)
+    acc, kept, acc_out, n = z(2, 2, 64), z(2, 2, 8, dtype=torch.int32), z(2, 2, 8), z(2, dtype=torch.int32)
+    for kw in (dict(dst_ld=5), dict(ld_acc=65), dict(ld_out=9)):
+        with pytest.raises(ValueError, match="dst_table|acc"):
+            q.qmv_kv_evict(c, table, 8, 0, 0, acc, kept, acc_out, n, stream=0, **kw)
+    # what fits
+    for a, ld in ((flat, 872), (flat, 128), (flat[744:], 128), (z(3, 512)[1:, 100:], 512)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            q.qmv_kv_append(c, 2, a, a, ldk=ld, ldv=ld, stream=0)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        q.qmv_kv_evict(c, table, 8, 0, 0, acc, kept, acc_out, n, dst_ld=4, ld_acc=64, ld_out=8, stream=0)
+
+
 def test_cache_of_host_tensors():
     """Calls over tensors that are not on a GPU end on the host; a cache's
     tensors cannot be exchanged behind its addresses."""
