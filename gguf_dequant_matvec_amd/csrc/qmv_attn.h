@@ -15,10 +15,13 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-// Probabilities are held as 2^kBias 2^(x - m), at most 2^(kBias + kSlack) =
-// 2^15 because m is moved as soon as a logit exceeds it by kSlack: f16 pieces
-// (largest 65504, smallest step 2^-24) then resolve weights down to 2^-36 of
-// the row's largest.
+// Probabilities are held as 2^bias 2^(x - m), at most 2^(bias + kSlack)
+// because m is moved as soon as a logit exceeds it by kSlack.  f16 pieces
+// (largest 65504, smallest step 2^-24): bias kBias, so at most 2^15, resolves
+// weights down to 2^-36 of the row's largest.  bf16 pieces have the exponents
+// of f32 and cached values up to its largest: there the bias keeps the sum of
+// all of a row's probabilities below 1, so that no sum of weighted values
+// leaves f32 (AttnArgs::bias; a cache of 2^13 positions: -19).
 constexpr float kBias = 11.f, kSlack = 4.f;
 constexpr float kNoMax = -1e30f;  // running maximum before any visible position: finite, so x - m never is inf - inf
 
@@ -86,6 +89,11 @@ __device__ __forceinline__ u32x4 load_stream(const uint8_t *p) {
     const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
     if constexpr (NT) return __builtin_nontemporal_load(q);
     return *q;
+}
+
+template <int TYPE>
+__device__ __forceinline__ float bias_of(const AttnArgs &a) {
+    return TYPE == kKvBF16 ? a.bias : kBias;
 }
 
 struct U128 { uint32_t w[4]; };

@@ -104,6 +104,8 @@ static void fill_attn(AttnArgs &a, const AttnPlan &p, float scale, void *ws) {
     const float f = (scale < 0.f ? -scale : scale) * 1.4426950408889634f;
     a.scale_log2 = scale == 0.f ? 1.f : f;
     a.q_sign = scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f;
+    // limit probabilities of at most 2^(bias + 4), the slack of the running maximum
+    a.bias = -5.f - (32 - __builtin_clz((unsigned)a.limit));
     a.group = a.n_heads / a.c.n_kv;
     a.tiles = p.tiles;
     a.splits = p.splits;

@@ -446,7 +446,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 #pragma unroll
                         for (int t = 0; t < DT; t++) o[rt][t] *= r;
                     }
-                    const float off = kBias - mrun[rt] + vlog;
+                    const float off = bias_of<TYPE>(a) - mrun[rt] + vlog;
                     float sum = 0.f;
 #pragma unroll
                     for (int e = 0; e < PER; e++) {
@@ -646,7 +646,7 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
             }
             for (int off = 8; off; off >>= 1) l += __shfl_xor(l, off, 16);
             if (l16 == 0) {
-                s_m[row] = mm - kBias;  // l carries 2^kBias
+                s_m[row] = mm - bias_of<TYPE>(a);  // l carries 2^bias
                 s_r[row] = l == 0.f ? 0.f : 1.f / l;
             }
         }

@@ -425,7 +425,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
                     for (int t = 0; t < DT; t++) o[t] *= r;
                 }
             }
-            const float off = kBias - mrun + vlog;
+            const float off = bias_of<TYPE>(a) - mrun + vlog;
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e++) {

@@ -442,10 +442,12 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * acc: NULL, or f32 [n_seq][n_kv_heads][ld_acc], ld_acc >= max_len: position
  * t of key-value head h gets, added, the weights w_t of the n tokens and of the
  * query heads that share h (what qmv_kv_evict ranks by).
- * f32 throughout: queries and weights enter the matrix cores as sums of 16-bit
- * pieces (f16 hi + lo, bf16 in three), maximum, sum and output are f32.  f16
+ * Queries and weights enter the matrix cores as sums of 16-bit pieces (f16 hi +
+ * lo, 22 bits; bf16 in three, 24 bits); maximum, sum and output are f32.  f16
  * and 8-bit caches resolve weights (8-bit: weight times V row scale) down to
- * 2^-36 of the largest, the latter for V row scales between 2^-100 and 2^100.
+ * 2^-36 of the largest, the latter for V row scales between 2^-100 and 2^100;
+ * bf16 caches resolve weights down to 2^-60 of the largest, with V of any
+ * finite value.
  * Results do not depend on anything but the arguments; a row's last bits may
  * depend on the call's other lengths, which decide where long ones are cut.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is

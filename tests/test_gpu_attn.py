@@ -891,3 +891,60 @@ def test_tensors_of_the_host_are_refused():
         q.qmv_attn_prefill(d.h, 1, 2, x, 0.125, out.cpu(), 64)
     torch.cuda.synchronize()
     assert not host(out).any()
+
+
+# ---- ends of the ranges ----------------------------------------------------------
+
+def _one_cache(t, hd, page, length, kv=1, seed=80, extra=0):
+    """A cache of one sequence and its rows, to be filled by the test."""
+    c, rng = make_cache(t, kv, hd, page, [length], seed, cap_pages=-(-(length + extra) // page))
+    return c, rng
+
+
+def _both(c, qh, scale, window=0, sinks=0, n_decode=(1,), max_len=None):
+    """Outputs of the last rows of qh by qmv_attn_decode, and of all by qmv_attn_prefill."""
+    d = Dev(c)
+    heads, max_len = qh.shape[1], max_len or c.cap
+    for m in (*n_decode, 0):
+        rows = qh[len(qh) - m:] if m else qh
+        m0 = len(rows)
+        out = torch.full((m0, heads * c.hd), -7.0, device="cuda")
+        if m:
+            ws = workspace(q.qmv_attn_decode_workspace(d.h, m, heads, max_len, window, sinks))
+            q.qmv_attn_decode(d.h, m, heads, dev(rows.reshape(m0, -1)), scale, out, max_len, window=window, sinks=sinks,
+                              workspace=ws)
+        else:
+            ws = workspace(q.qmv_attn_prefill_workspace(d.h, m0, heads, max_len, window, sinks))
+            q.qmv_attn_prefill(d.h, m0, heads, dev(rows.reshape(m0, -1)), scale, out, max_len, window=window, sinks=sinks,
+                               workspace=ws)
+        yield (f"decode n{m}" if m else f"prefill {m0}"), rows, host(out).reshape(m0, heads, c.hd)
+
+
+@pytest.mark.parametrize("hd,length,n", [(64, 1, 1), (64, 3, 3), (128, 300, 40), (64, 3000, 20), (256, 700, 20)])
+@pytest.mark.parametrize("exp", [-100, 100, 116, 125])
+def test_bf16_value_range(hd, length, n, exp):
+    """bf16 values up to the type's largest: sums of weighted values stay finite."""
+    c, rng = _one_cache("bf16", hd, 64, length)
+    k = rng.standard_normal((length, 1, hd), dtype=np.float32)
+    v = np.clip(rng.standard_normal((length, 1, hd), dtype=np.float32), -3, 3) * np.float32(2.0 ** exp)
+    _fill(c, 0, k, v)
+    qh = synth.normal(3, synth.T_X, (n, 4, hd), 1.5)
+    scale = float(np.float32(hd ** -0.5))
+    for what, rows, got in _both(c, qh, scale, n_decode=(1, min(n, 16))):
+        want, tol, _, _ = ref.attention(c, [0, len(rows)], rows, scale, c.cap)
+        close(got, want, tol, f"{what} 2^{exp}")
+
+
+@pytest.mark.parametrize("length", [1, 70, 5000])
+def test_bf16_largest_values(length):
+    """Every value the largest bf16: so is the mean, to rounding."""
+    c, rng = _one_cache("bf16", 64, 64, length)
+    top = np.array([0x7F7F], np.uint16).view(np.uint16)
+    _fill(c, 0, rng.standard_normal((length, 1, 64), dtype=np.float32), np.zeros((length, 1, 64), np.float32))
+    for pg in c.table[0]:
+        c.parts(pg, 0)[1][:] = top
+    qh = synth.normal(3, synth.T_X, (min(length, 20), 4, 64), 1.5)
+    scale = 0.125
+    for what, rows, got in _both(c, qh, scale, n_decode=(1, min(length, 16))):
+        want, tol, _, _ = ref.attention(c, [0, len(rows)], rows, scale, c.cap)
+        close(got, want, tol, f"{what} largest")
