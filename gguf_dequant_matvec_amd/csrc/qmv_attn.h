@@ -95,6 +95,13 @@ template <int TYPE>
 __device__ __forceinline__ float bias_of(const AttnArgs &a) {
     return TYPE == kKvBF16 ? a.bias : kBias;
 }
+// ... and of the sums that leave a wave.  8-bit ones take their factor back
+// first (weighted values of row scales up to 2^100 would not stay finite
+// with it).
+template <int TYPE>
+__device__ __forceinline__ float sum_bias_of(const AttnArgs &a) {
+    return TYPE == kKvF16 ? kBias : a.bias;
+}
 
 struct U128 { uint32_t w[4]; };
 template <class V>

@@ -3,6 +3,8 @@
 // copies or synchronises.
 #include <hip/hip_runtime.h>
 
+#include <math.h>
+
 #include "qmv.h"
 #include "qmv_internal.h"
 #include "qmv_kv.h"
@@ -106,6 +108,7 @@ static void fill_attn(AttnArgs &a, const AttnPlan &p, float scale, void *ws) {
     a.q_sign = scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f;
     // limit probabilities of at most 2^(bias + 4), the slack of the running maximum
     a.bias = -5.f - (32 - __builtin_clz((unsigned)a.limit));
+    a.unit = ldexpf(1.f, (int)a.bias - 11);
     a.group = a.n_heads / a.c.n_kv;
     a.tiles = p.tiles;
     a.splits = p.splits;

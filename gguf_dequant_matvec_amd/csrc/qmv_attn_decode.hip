@@ -526,10 +526,15 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
             const float r = exp2_fast(mrun[rt] - mm);
             mrun[rt] = mm;
             lrun[rt] *= r;
-            if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
-            const float ro = TYPE == kKvI8 ? r * vback : r;
+            if constexpr (TYPE == kKvI8) {
+                lrun[rt] *= a.unit;
+                const float back = vback * a.unit;  // a power of two (with r it might be subnormal and lose bits)
 #pragma unroll
-            for (int t = 0; t < DT; t++) o[rt][t] *= ro;
+                for (int t = 0; t < DT; t++) o[rt][t] *= back;
+            }
+            if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
+#pragma unroll
+            for (int t = 0; t < DT; t++) o[rt][t] *= r;
         }
         for (int from = NW - 2; from >= 0; from -= 2) {
             // waves from, from + 1 add to the two before them; last 1 to 0
@@ -646,7 +651,7 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
             }
             for (int off = 8; off; off >>= 1) l += __shfl_xor(l, off, 16);
             if (l16 == 0) {
-                s_m[row] = mm - bias_of<TYPE>(a);  // l carries 2^bias
+                s_m[row] = mm - sum_bias_of<TYPE>(a);  // l carries 2^that
                 s_r[row] = l == 0.f ? 0.f : 1.f / l;
             }
         }

@@ -454,10 +454,16 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
     lrun += __shfl_xor(lrun, 32);
     if (!live) return;
     const int64_t orow = row * a.n_heads + h * a.group + hg;
-    float mul = TYPE == kKvI8 ? vback : 1.f;
+    float mul = 1.f;
+    if constexpr (TYPE == kKvI8) {
+        lrun *= a.unit;
+        const float back = vback * a.unit;
+#pragma unroll
+        for (int t = 0; t < DT; t++) o[t] *= back;
+    }
     float *dst;
     if (a.splits == 1) {
-        mul = lrun == 0.f ? 0.f : mul / lrun;  // a row that sees nothing: zeros
+        mul = lrun == 0.f ? 0.f : 1.f / lrun;  // a row that sees nothing: zeros
         dst = a.out + orow * HD;
     } else {
         const int64_t at = (int64_t)split * a.part_rows + orow;

@@ -86,7 +86,9 @@ struct AttnArgs {
     int32_t parts;           // decode, not 0: instead, workgroups of a head over all sequences
     float scale_log2;        // |scale| * log2(e), not zero
     float q_sign;            // what queries are multiplied by: the scale's sign (0 for scale 0)
-    float bias;              // bf16: log2 of what probabilities are multiplied by, -(5 + bits of limit)
+    float bias;              // -(5 + bits of limit).  bf16: log2 of what probabilities are multiplied by;
+                             // 8-bit: of what the sums that leave a wave are
+    float unit;              // 8-bit: 2^(bias - kBias), from the probabilities' factor to that of the sums
     float2 *part_ml;         // running maximum and sum of each piece of an output row
     float *part_o;           // [hd] of each
     int64_t part_rows;       // rows * n_heads; prompts: piece i of output row r is at i * part_rows + r

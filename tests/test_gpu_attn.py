@@ -948,3 +948,21 @@ def test_bf16_largest_values(length):
     for what, rows, got in _both(c, qh, scale, n_decode=(1, min(length, 16))):
         want, tol, _, _ = ref.attention(c, [0, len(rows)], rows, scale, c.cap)
         close(got, want, tol, f"{what} largest")
+
+
+@pytest.mark.parametrize("length,n", [(1, 1), (64, 20), (2500, 20), (20000, 20)])
+@pytest.mark.parametrize("exp", [-100, 100])
+@pytest.mark.parametrize("flat", [True, False])
+def test_i8_scales_at_the_ends(length, n, exp, flat):
+    """8-bit V row scales at both ends of what the header names, every code the
+    largest; every position the same weight, or any."""
+    c, rng = _one_cache("i8", 64, 64, length)
+    k = rng.standard_normal((length, 1, 64), dtype=np.float32) * np.float32(not flat)
+    _fill(c, 0, k, np.full((length, 1, 64), 127.0, np.float32))
+    for pg in c.table[0]:
+        sc = c.parts(pg, 0)[2]
+        sc[1] = np.where(np.isnan(sc[1]), sc[1], np.float32(2.0 ** exp))
+    qh = synth.normal(3, synth.T_X, (n, 4, 64), 1.5)
+    for what, rows, got in _both(c, qh, 0.125, n_decode=(1, min(n, 16))):
+        want, tol, _, _ = ref.attention(c, [0, len(rows)], rows, 0.125, c.cap)
+        close(got, want, tol, f"{what} 2^{exp}")
