@@ -23,7 +23,26 @@ constexpr float kLog2e = 1.4426950408889634f;
 // all of a row's probabilities below 1, so that no sum of weighted values
 // leaves f32 (AttnArgs::bias; a cache of 2^13 positions: -19).
 constexpr float kBias = 11.f, kSlack = 4.f;
-constexpr float kNoMax = -1e30f;  // running maximum before any visible position: finite, so x - m never is inf - inf
+constexpr float kNoMax = -3.4028235e38f;  // running maximum before any visible position: finite, so x - m never is inf - inf
+
+// Prompts, which vector instructions bound: x factor - m is one fused operation
+// while the logits are small.  Past kFar the roundings of m and of bias - m,
+// 2^-24 of it each, would come into the exponent (beyond 2^24 they would be the
+// exponent): there x is rounded as the maximum was, and the difference taken
+// first.  (Decode holds the maximum of the unscaled x and takes (x - m) factor,
+// an instruction more, which memory hides.)
+constexpr float kFar = 1024.f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar && m > kNoMax; }
+__device__ __forceinline__ float past_max(float x, float factor, float m) {
+#pragma clang fp contract(off)
+    const float t = x * factor;
+    return t - m;
+}
+// Whether a logit is so far above the running maximum that this has to move.
+__device__ __forceinline__ bool above_max(float x, float m) {
+#pragma clang fp contract(off)
+    return x - m > kSlack;
+}
 
 // 8-bit V rows carry their scale into the probabilities; `vmul`, a power of
 // two, keeps the largest scale so far at most 1.  Before the first row:

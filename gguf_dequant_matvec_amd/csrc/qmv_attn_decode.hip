@@ -288,7 +288,9 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
             const int pg = table[pi];
             return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
         };
-        float mrun[RT], lrun[RT];
+        // (the maximum is that of the unscaled x: x - m then is exact where it
+        // matters, however large the logits, and the difference takes the factor)
+        float mrun[RT], lrun[RT], qscale[RT];
         f32x4 o[RT][DT];
         // 8-bit: power of two that brings the row scales of V to at most 1, its
         // logarithm (it enters with the exponent) and its inverse
@@ -296,6 +298,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 #pragma unroll
         for (int rt = 0; rt < RT; rt++) {
             mrun[rt] = kNoMax;
+            qscale[rt] = 1.f;
             lrun[rt] = 0.f;
 #pragma unroll
             for (int t = 0; t < DT; t++) o[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -314,7 +317,6 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 
             // the rows
             int pos[RT];
-            float qscale[RT];
             U128 qf[RT][KS][NP];
 #pragma unroll
             for (int rt = 0; rt < RT; rt++) {
@@ -435,22 +437,21 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                     float mx = x[0];
 #pragma unroll
                     for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
-                    mx *= qscale[rt];
-                    if (__any(mx > mrun[rt] + kSlack)) {
+                    if (__any((mx - mrun[rt]) * qscale[rt] > kSlack || (mrun[rt] == kNoMax && mx > kNoMax))) {
                         mx = fmaxf(mx, __shfl_xor(mx, 16));
                         mx = fmaxf(mx, __shfl_xor(mx, 32));
                         const float mnew = fmaxf(mrun[rt], mx);
-                        const float r = exp2_fast(mrun[rt] - mnew);
+                        const float r = exp2_fast((mrun[rt] - mnew) * qscale[rt]);
                         mrun[rt] = mnew;
                         lrun[rt] *= r;
 #pragma unroll
                         for (int t = 0; t < DT; t++) o[rt][t] *= r;
                     }
-                    const float off = bias_of<TYPE>(a) - mrun[rt] + vlog;
+                    const float off = bias_of<TYPE>(a) + vlog;
                     float sum = 0.f;
 #pragma unroll
                     for (int e = 0; e < PER; e++) {
-                        x[e] = exp2_fast(fmaf(x[e], qscale[rt], off));
+                        x[e] = exp2_fast(fmaf(x[e] - mrun[rt], qscale[rt], off));
                         sum += x[e];
                         if constexpr (TYPE == kKvI8) {
                             const float w = x[e] * vt.vs[e];
@@ -515,6 +516,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
         for (int rt = 0; rt < RT; rt++) {
             lrun[rt] += __shfl_xor(lrun[rt], 16);
             lrun[rt] += __shfl_xor(lrun[rt], 32);
+            if (mrun[rt] != kNoMax) mrun[rt] *= qscale[rt];
             if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
         }
         __syncthreads();
@@ -651,8 +653,8 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
             }
             for (int off = 8; off; off >>= 1) l += __shfl_xor(l, off, 16);
             if (l16 == 0) {
-                s_m[row] = mm - sum_bias_of<TYPE>(a);  // l carries 2^that
-                s_r[row] = l == 0.f ? 0.f : 1.f / l;
+                s_m[row] = mm;
+                s_r[row] = l == 0.f ? 0.f : exp2_fast(sum_bias_of<TYPE>(a)) / l;
             }
         }
         __syncthreads();

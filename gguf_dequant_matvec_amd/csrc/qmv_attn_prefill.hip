@@ -290,6 +290,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         }
     }
     float mrun = kNoMax, lrun = 0.f;
+    bool far = false;  // some row's maximum is
     float vmul = kVmulNone, vlog = TYPE == kKvI8 ? kVlogNone : 0.f, vback = 1.f / kVmulNone;  // as in the decode kernel
     f32x16 o[DT];
 #pragma unroll
@@ -401,11 +402,12 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
 #pragma unroll
             for (int e = 0; e < 16; e++) mx = fmaxf(mx, x[e]);
             mx *= qscale;
-            if (__any(mx > mrun + kSlack)) {
+            if (__any(above_max(mx, mrun))) {
                 mx = fmaxf(mx, __shfl_xor(mx, 32));
                 const float mnew = fmaxf(mrun, mx);
                 const float r = exp2_fast(mrun - mnew);
                 mrun = mnew;
+                far = far || __any(is_far(mnew));
                 lrun *= r;
 #pragma unroll
                 for (int t = 0; t < DT; t++) o[t] *= r;
@@ -425,11 +427,18 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
                     for (int t = 0; t < DT; t++) o[t] *= r;
                 }
             }
-            const float off = bias_of<TYPE>(a) - mrun + vlog;
+            if (far) {
+                const float off = bias_of<TYPE>(a) + vlog;
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[e] = exp2_fast(past_max(x[e], qscale, mrun) + off);
+            } else {
+                const float off = bias_of<TYPE>(a) - mrun + vlog;
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[e] = exp2_fast(fmaf(x[e], qscale, off));
+            }
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e++) {
-                x[e] = exp2_fast(fmaf(x[e], qscale, off));
                 sum += x[e];
                 if constexpr (TYPE == kKvI8) x[e] *= vs[e >> 2][e & 3];
             }

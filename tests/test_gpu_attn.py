@@ -966,3 +966,41 @@ def test_i8_scales_at_the_ends(length, n, exp, flat):
     for what, rows, got in _both(c, qh, 0.125, n_decode=(1, min(n, 16))):
         want, tol, _, _ = ref.attention(c, [0, len(rows)], rows, 0.125, c.cap)
         close(got, want, tol, f"{what} 2^{exp}")
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("size", [1e5, 1e8, 1e12, 1e30, 1e36])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_huge_logits(t, size, sign):
+    """Logits far beyond the exponent's range, of either sign: each row takes the
+    value of its largest one.
+
+    K holds sign * (1 + i / 128) in one column, so neighbouring logits differ by
+    size / 128 * log2 e, over 1000, and the other weights are zero.  The output is
+    then V of one position, off by the split of its weight (2^-22) and at most 16
+    roundings (2^-20): 1.25 * 2^-20 of |V|."""
+    length, n = 120, 50
+    c, rng = _one_cache(t, 64, 16, length)
+    order = rng.permutation(128)[:length]
+    k = np.zeros((length, 1, 64), np.float32)
+    k[:, 0, 0] = sign * (1 + order / 128.0)
+    v = rng.standard_normal((length, 1, 64), dtype=np.float32)
+    _fill(c, 0, k, v)
+    _, V, _ = c.rows(0, 0, length)
+    qh = np.zeros((n, 2, 64), np.float32)
+    qh[:, :, 0] = size
+    for what, rows, got in _both(c, qh, 1.0, n_decode=(1, 16)):
+        m = len(rows)
+        best = [int(np.argmax(k[:length - m + j + 1, 0, 0])) for j in range(m)]
+        want = V[best][:, None, :]
+        close(got, np.broadcast_to(want, got.shape), np.broadcast_to(np.abs(want) * 1.25 * 2.0 ** -20 + 1e-37, got.shape),
+              f"{what} {t} {sign * size}")
+    # the weights: one for each row's position
+    d = Dev(c)
+    out, acc = torch.empty(16, 128, device="cuda"), torch.zeros(1, 1, c.cap, device="cuda")
+    ws = workspace(q.qmv_attn_decode_workspace(d.h, 16, 2, c.cap, 0, 0, True))
+    q.qmv_attn_decode(d.h, 16, 2, dev(qh[-16:].reshape(16, -1)), 1.0, out, c.cap, acc=acc, workspace=ws)
+    want = np.zeros(c.cap)
+    for j in range(16):
+        want[int(np.argmax(k[:length - 16 + j + 1, 0, 0]))] += 2
+    close(host(acc).reshape(-1), want, want * 2.0 ** -20 + 1e-37, f"weights {t} {sign * size}")
