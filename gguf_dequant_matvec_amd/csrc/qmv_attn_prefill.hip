@@ -412,6 +412,13 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
 #pragma unroll
                 for (int t = 0; t < DT; t++) o[t] *= r;
             }
+            float mbase = mrun;
+            if (far) {
+                mbase = 0.f;
+                const float back = 1.f / qscale;
+#pragma unroll
+                for (int e = 0; e < 16; e++) x[e] = past_max(x[e], qscale, mrun) * back;
+            }
             if constexpr (TYPE == kKvI8) {
                 const f32x4 vm = *reinterpret_cast<const f32x4 *>(buf + Lds<HD>::kVmax);
                 const float vbig = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));  // the chunk's
@@ -427,18 +434,11 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
                     for (int t = 0; t < DT; t++) o[t] *= r;
                 }
             }
-            if (far) {
-                const float off = bias_of<TYPE>(a) + vlog;
-#pragma unroll
-                for (int e = 0; e < 16; e++) x[e] = exp2_fast(past_max(x[e], qscale, mrun) + off);
-            } else {
-                const float off = bias_of<TYPE>(a) - mrun + vlog;
-#pragma unroll
-                for (int e = 0; e < 16; e++) x[e] = exp2_fast(fmaf(x[e], qscale, off));
-            }
+            const float off = bias_of<TYPE>(a) - mbase + vlog;
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; e++) {
+                x[e] = exp2_fast(fmaf(x[e], qscale, off));
                 sum += x[e];
                 if constexpr (TYPE == kKvI8) x[e] *= vs[e >> 2][e & 3];
             }
