@@ -93,10 +93,11 @@ struct Stage {
             }
         }
     }
-    // live: positions of the 16 that some row may see; 8-bit: scales of the
-    // others, which may be anything, are left out.  whole: every row sees every
-    // position; where not, V values that are not finite leave marks and zeros.
-    __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live, bool whole) const {
+    // live: positions of the 16 that some row may see, but for those from h0 to
+    // before h1; 8-bit: scales of the others, which may be anything, are left
+    // out.  whole: every row sees every position; where not, V values that are
+    // not finite leave marks and zeros.
+    __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live, int h0, int h1, bool whole) const {
         if (!ok) live = 0;
         bool marked = false;
         if constexpr (TYPE == kKvI8) {
@@ -115,7 +116,8 @@ struct Stage {
                 *reinterpret_cast<u32x4 *>(vd + vslot(p, 0) * 16) = u32x4{e.x, e.y, f.x, f.y};
                 *reinterpret_cast<u32x4 *>(vd + vslot(p, 1) * 16) = u32x4{g.x, g.y, o.x, o.y};
             }
-            const float mine = (lane & 15) < live ? sc : 0.f;
+            const int at = lane & 15;
+            const float mine = at < live && (at < h0 || at >= h1) ? sc : 0.f;
             if (lane < 32) reinterpret_cast<float *>(buf + Lds<HD>::kScale)[(lane >> 4) * kBK + 16 * w + (lane & 15)] = mine;
             float big = fabsf(mine) < __builtin_inff() ? fabsf(mine) : 0.f;
             for (int off = 8; off; off >>= 1) big = fmaxf(big, __shfl_xor(big, off));
@@ -246,10 +248,12 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         const int pg = c.table[(int64_t)s * c.table_ld + pi];
         return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
     };
-    auto live_of = [&](int i) {  // how many of its 16 positions some row of the tile sees
+    auto live_of = [&](int i) {  // how many of its 16 positions are not behind what any row sees
         const int left = pmax + 1 - (ch.at(i) * kBK + 16 * wave);
         return left > 16 ? 16 : left < 0 ? 0 : left;
     };
+    // of these, behind the sinks and before every row's window: from .. to before
+    const int hid0 = a.sinks, hid1 = a.window > 0 ? pmin - a.window + 1 : 0;
     auto whole_of = [&](int i) {  // whether every row of the tile sees all of it
         const int c0 = ch.at(i) * kBK, c1 = c0 + kBK - 1;
         return c1 <= pmin && (a.window <= 0 || c0 > pmax - a.window || c1 < a.sinks);
@@ -299,7 +303,8 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
         for (int e = 0; e < 16; e++) o[t][e] = 0.f;
 
     page = __builtin_amdgcn_readfirstlane(page_of(begin + 1));
-    if (begin < end) st.store(buf_of(begin), ok_of(begin), wave, lane, live_of(begin), whole_of(begin));
+    if (begin < end) st.store(buf_of(begin), ok_of(begin), wave, lane, live_of(begin), hid0 - ch.at(begin) * kBK - 16 * wave,
+                               hid1 - ch.at(begin) * kBK - 16 * wave, whole_of(begin));
     for (int i = begin; i < end; i++) {
         const uint8_t *buf = buf_of(i);
         const bool more = i + 1 < end;
@@ -457,7 +462,8 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
             if constexpr (HD >= 128) __builtin_amdgcn_s_setprio(0);
         }
         page = __builtin_amdgcn_readfirstlane(next_page);
-        if (more) st.store(buf_of(i + 1), ok_of(i + 1), wave, lane, live_of(i + 1), whole_of(i + 1));
+        if (more) st.store(buf_of(i + 1), ok_of(i + 1), wave, lane, live_of(i + 1), hid0 - ch.at(i + 1) * kBK - 16 * wave,
+                          hid1 - ch.at(i + 1) * kBK - 16 * wave, whole_of(i + 1));
     }
 
     lrun += __shfl_xor(lrun, 32);

@@ -372,9 +372,10 @@ qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *
  * or hidden positions hold does not matter, NaN and infinities included (a
  * value that is not finite in V makes its column NaN or infinite in the rows
  * that see it, one in K or in a query leaves the rows concerned unspecified,
- * most often NaN; a hidden 8-bit V row of far larger scale may cost a row of the
- * same call resolution, see qmv_attn_decode).  Lengths and table are read on the device when the
- * call runs, so a captured call follows them from replay to replay. */
+ * most often NaN; an 8-bit V row of far larger scale that other new tokens of
+ * the same sequence see may cost a row resolution, see qmv_attn_decode).
+ * Lengths and table are read on the device when the call runs, so a captured
+ * call follows them from replay to replay. */
 typedef enum {
     QMV_KV_F16 = 1,   /* the GGUF ids of F16, I8 and BF16 */
     QMV_KV_I8 = 24,
@@ -444,10 +445,11 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * query heads that share h (what qmv_kv_evict ranks by).
  * Queries and weights enter the matrix cores as sums of 16-bit pieces (f16 hi +
  * lo, 22 bits; bf16 in three, 24 bits); maximum, sum and output are f32.  f16
- * and 8-bit caches resolve weights (8-bit: weight times V row scale) down to
- * 2^-36 of the largest, the latter for V row scales between 2^-100 and 2^100;
- * bf16 caches resolve weights down to 2^-60 of the largest, with V of any
- * finite value.
+ * caches resolve weights down to 2^-36 of the row's largest; 8-bit ones the
+ * products of weight and V row scale down to 2^-36 of the row's largest weight
+ * times the largest scale that any of the sequence's new tokens sees, for V row
+ * scales between 2^-100 and 2^100 (K row scales up to 2^97); bf16 ones weights
+ * down to 2^-60 of the largest, with V of any finite value.
  * Results do not depend on anything but the arguments; a row's last bits may
  * depend on the call's other lengths, which decide where long ones are cut.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is

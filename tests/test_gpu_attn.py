@@ -1004,3 +1004,29 @@ def test_huge_logits(t, size, sign):
     for j in range(16):
         want[int(np.argmax(k[:length - 16 + j + 1, 0, 0]))] += 2
     close(host(acc).reshape(-1), want, want * 2.0 ** -20 + 1e-37, f"weights {t} {sign * size}")
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128, 256])
+@pytest.mark.parametrize("bad", [1e12, 1e25, 1e30])
+@pytest.mark.parametrize("window,sinks,length,n", [(37, 3, 333, 9), (100, 0, 150, 1), (64, 5, 200, 60)])
+def test_i8_hidden_scales(hd, bad, window, sinks, length, n):
+    """A large finite V row scale at a position that no row of the call sees,
+    before the window, behind the sinks, or behind the last position."""
+    c, _ = make_cache("i8", 1, hd, 16, [length], 81, cap_pages=-(-length // 16) + 1)
+    qh = synth.normal(8, synth.T_X, (n, 4, hd), 1.0)
+    scale = float(np.float32(hd ** -0.5))
+    first = length - n - window + 1                # the first position in some row's window
+    for p in (first - 1, first - 2, first - 17, sinks, length):
+        pool = c.pool.copy()
+        pg, slot = c.where(0, p)
+        c.parts(pg, 0)[2][1, slot] = bad
+        for what, rows, got in _both(c, qh, scale, window, sinks, n_decode=(n,) if n <= 16 else ()):
+            want, tol, _, _ = _without(c, pool, rows, scale, window, sinks)
+            close(got, want, tol, f"{what} hd{hd} scale[{p}] = {bad}")
+        c.pool[:] = pool
+
+
+def _without(c, pool, rows, scale, window, sinks):
+    clean = ref.Cache(c.t, c.kv, c.hd, c.page, c.n_pages, c.table, c.seq_len)
+    clean.pool = pool
+    return ref.attention(clean, [0, len(rows)], rows, scale, c.cap, window, sinks)
