@@ -451,12 +451,10 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                     float sum = 0.f;
 #pragma unroll
                     for (int e = 0; e < PER; e++) {
+                        const bool hidden = TYPE == kKvI8 && !whole && x[e] == -__builtin_inff();
                         x[e] = exp2_fast(fmaf(x[e] - mrun[rt], qscale[rt], off));
                         sum += x[e];
-                        if constexpr (TYPE == kKvI8) {
-                            const float w = x[e] * vt.vs[e];
-                            x[e] = whole || x[e] != 0.f ? w : 0.f;  // (a scale that the row does not see may be NaN)
-                        }
+                        if constexpr (TYPE == kKvI8) x[e] = hidden ? 0.f : x[e] * vt.vs[e];  // (which may be NaN)
                     }
                     lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
 #pragma unroll

@@ -1030,3 +1030,32 @@ def _without(c, pool, rows, scale, window, sinks):
     clean = ref.Cache(c.t, c.kv, c.hd, c.page, c.n_pages, c.table, c.seq_len)
     clean.pool = pool
     return ref.attention(clean, [0, len(rows)], rows, scale, c.cap, window, sinks)
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("spot", [3, 40, 70, 119])
+@pytest.mark.parametrize("top", [10, 50, 100])
+@pytest.mark.parametrize("window", [0, 200])
+def test_seen_values_without_weight(t, bad, spot, top, window):
+    """A value that is not finite reaches every row that sees it, also where its
+    weight underflows to zero."""
+    length, n, hd = 120, 20, 64
+    c, rng = _one_cache(t, hd, 16, length, extra=100)
+    k = np.zeros((length, 1, hd), np.float32)
+    k[:, 0, 0] = np.where(np.arange(length) == top, 8.0, -8.0)      # all weight on one position
+    _fill(c, 0, k, rng.standard_normal((length, 1, hd), dtype=np.float32))
+    pg, slot = c.where(0, spot)
+    _, v, sc = c.parts(pg, 0)
+    if t == "i8":
+        sc[1, slot] = bad
+    else:
+        v[slot // 16, 5, slot % 16] = np.float16(bad) if t == "f16" else 0x7FC0 if np.isnan(bad) else 0x7F80
+    qh = np.zeros((n, 2, hd), np.float32)
+    qh[:, :, 0] = 100.0
+    for what, rows, got in _both(c, qh, 1.0, window, 0, n_decode=(1, 16)):
+        m = len(rows)
+        sees = spot <= length - m + np.arange(m)
+        cols = slice(None) if t == "i8" else slice(5, 6)
+        assert not np.isfinite(got[sees][:, :, cols]).any(), f"{what} {t} {bad} at {spot}, weight at {top}"
+        assert np.isfinite(got[~sees]).all(), f"{what} {t} {bad} at {spot}, weight at {top}"
