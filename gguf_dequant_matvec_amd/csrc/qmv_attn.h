@@ -3,6 +3,7 @@
 // visible chunks of a cache.
 #pragma once
 
+#include "qmv_attn_plan.h"
 #include "qmv_device.h"
 #include "qmv_kv.h"
 
@@ -14,7 +15,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr float kLog2e = 1.4426950408889634f;
 // Probabilities are held as 2^bias 2^(x - m), at most 2^(bias + kSlack)
 // because m is moved as soon as a logit exceeds it by kSlack.  f16 pieces
 // (largest 65504, smallest step 2^-24): bias kBias, so at most 2^15, resolves
@@ -22,7 +22,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 // of f32 and cached values up to its largest: there the bias keeps the sum of
 // all of a row's probabilities below 1, so that no sum of weighted values
 // leaves f32 (AttnArgs::bias; a cache of 2^13 positions: -19).
-constexpr float kBias = 11.f, kSlack = 4.f;
 constexpr float kNoMax = -3.4028235e38f;  // running maximum before any visible position: finite, so x - m never is inf - inf
 
 // Prompts, which vector instructions bound: x factor - m is one fused operation
@@ -211,8 +210,6 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // read a piece (16 bytes each), 256 / (HD / 4) pieces at a time and four such
 // rounds in flight.  Bound by latency: 64 pieces of 128 columns, eight loads a
 // thread, 4.5 us.
-constexpr int kMaxPieces = 512;
-
 template <int HD>
 __device__ __forceinline__ void join_row(const AttnArgs &a, int64_t prow, int64_t first, int64_t stride, int count) {
     constexpr int L = HD / 4, G = 256 / L;

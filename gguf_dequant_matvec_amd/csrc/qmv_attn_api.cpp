@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include "qmv.h"
+#include "qmv_attn_plan.h"
 #include "qmv_internal.h"
 #include "qmv_kv.h"
 
@@ -103,12 +104,12 @@ static qmv_status check_attn(const qmv_kv_cache *c, int32_t n_heads, int64_t max
 
 static void fill_attn(AttnArgs &a, const AttnPlan &p, float scale, void *ws) {
     // the kernels want a positive factor; the sign goes to the queries
-    const float f = (scale < 0.f ? -scale : scale) * 1.4426950408889634f;
+    const float f = (scale < 0.f ? -scale : scale) * kLog2e;
     a.scale_log2 = scale == 0.f ? 1.f : f;
     a.q_sign = scale == 0.f ? 0.f : scale < 0.f ? -1.f : 1.f;
-    // limit probabilities of at most 2^(bias + 4), the slack of the running maximum
-    a.bias = -5.f - (32 - __builtin_clz((unsigned)a.limit));
-    a.unit = ldexpf(1.f, (int)a.bias - 11);
+    // `limit` probabilities of at most 2^(bias + kSlack): less than 1 in all
+    a.bias = -1.f - kSlack - (32 - __builtin_clz((unsigned)a.limit));
+    a.unit = ldexpf(1.f, (int)(a.bias - kBias));
     a.group = a.n_heads / a.c.n_kv;
     a.tiles = p.tiles;
     a.splits = p.splits;

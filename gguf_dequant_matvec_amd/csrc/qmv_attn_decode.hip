@@ -30,7 +30,7 @@ namespace qmv {
 namespace {
 
 template <int TYPE>
-constexpr int kChunk = TYPE == kKvI8 ? 64 : 32;  // positions a wave takes at a time (16 KB at 128 columns)
+constexpr int kChunk = decode_chunk(TYPE);  // positions a wave takes at a time
 
 // Column of element j of the operand of step t in lane group g: 8-bit rows are
 // read in 16-byte pieces of two steps where 64 divides the row.
@@ -207,10 +207,6 @@ __device__ __forceinline__ Range find_range(const AttnArgs &a, int p, int lane) 
     }
     return r;
 }
-
-// Workgroups of four waves and 16-row tiles that the registers of a compute
-// unit hold at once (256 columns take more than half of them).
-constexpr int resident(int type, int hd) { return hd == 256 ? 1 : hd == 64 && type != kKvI8 ? 3 : 2; }
 
 template <int TYPE, int HD, int RT, int NW, bool ACC, bool RANGES>
 __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1) void attn_decode(AttnArgs a) {
@@ -698,12 +694,6 @@ hipError_t launch_typed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     return launch_aux(attn_join_pieces<HD>, dim3((uint32_t)(a.n * a.n_heads), a.c.n_seq), dim3(256), 0, s, a);
 }
 
-// Whether the 256 registers that eight waves leave each lane hold the kernel's
-// operands; four waves have 512.
-constexpr bool eight_fit(int type, int hd, int rt) {
-    return rt == 1 ? hd <= 128 : hd == 64 || (hd == 96 && type == kKvF16);
-}
-
 template <int TYPE, int HD, int RT>
 hipError_t launch_rt(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     // 32-row tiles take eight waves wherever they fit, 16-row tiles either
@@ -733,73 +723,7 @@ hipError_t launch_type(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     }
 }
 
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
 }  // namespace
-
-AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int n,
-                          int64_t max_len, int window, int sinks, bool with_acc) {
-    AttnPlan p{};
-    const int64_t rows = (int64_t)n * group;
-    p.rt = rows > 16 && hd <= 128 ? 2 : 1;
-    p.tiles = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
-    p.part_rows = n_seq * n_kv * rows;
-    // the most positions a tile reads, in chunks
-    const int ck = type == kKvI8 ? 64 : 32;
-    int64_t most = max_len;
-    if (window > 0) {
-        const int64_t w = (int64_t)window + n + sinks + 2 * ck;
-        if (w < most) most = w;
-    }
-    const int64_t chunks = (most + ck - 1) / ck;
-    // Workgroups for 256 compute units: as many as fit at once, because a second
-    // round of them waits for its lengths, table and first rows again (16
-    // sequences of 8192 positions of 256 columns: one workgroup a unit 101 us,
-    // two 113; 32 of 6144 of 64 columns: three 72 us, two 74, four 81).  Tiles of
-    // 32 rows take one workgroup, of eight waves (the drafted tokens: 24 us
-    // against 26 with 512 of four and 34 with 1024) or, where registers say so,
-    // of four.
-    const int64_t heads = (int64_t)n_kv * p.tiles, base = n_seq * heads;
-    const int64_t fit = 256 * (p.rt == 2 ? 1 : resident(type, hd));
-    int64_t splits = (fit + base - 1) / base;
-    if (splits > chunks / 8) splits = chunks / 8;    // at least a chunk, with four waves two, per wave
-    if (splits > 128) splits = 128;
-    p.splits = splits < 1 ? 1 : (int)splits;
-    p.slots = (int)(n_seq * p.splits);
-    // Where such a piece may be long, lengths decide: evenly cut ranges.  With
-    // sequences enough for all workgroups the grid's own order balances them
-    // better (512 of 768 to 1536 positions: 409 against 422 us; but 128 of 1 to
-    // 2048: 117 against 96), so the more there are, the longer the longest
-    // has to be.
-    const int waves = p.rt == 2 && eight_fit(type, hd, 2) ? 8 : 4;
-    const int64_t long_chunks = base < fit ? 5 * waves * p.splits : 8 * waves * base / fit;
-    if (n_seq > 1 && n_seq <= 1024 && chunks >= long_chunks && chunks * n_seq < (1ll << 30) &&
-        p.part_rows < (1ll << 24)) {
-        p.parts = (int)((fit + heads - 1) / heads);
-        if (p.parts > kMaxPieces) p.parts = kMaxPieces;  // one sequence may take all of them
-        p.slots = (int)(p.parts + n_seq);
-    }
-    // a launch of few, unsplit workgroups is a chain of latencies: eight waves
-    // halve the chunks in it (301 positions, 3 heads: 7.3 -> 6.6 us)
-    p.waves = eight_fit(type, hd, p.rt) && (p.rt == 2 || (p.slots == n_seq && base <= 256)) ? 8 : 4;
-    size_t at = 0;
-    if (p.slots > n_seq || with_acc) {
-        const size_t pieces = (size_t)p.slots * n * n_kv * group;
-        p.ml_off = at;
-        at = up256(at + sizeof(float2) * pieces);
-        p.o_off = at;
-        at = up256(at + sizeof(float) * pieces * hd);
-        p.share_off = at;
-        at = up256(at + sizeof(int2) * n_seq);
-    }
-    if (with_acc) {
-        p.ld_logits = (max_len + ck - 1) / ck * ck;
-        p.logits_off = at;
-        at = up256(at + sizeof(float) * (size_t)p.part_rows * p.ld_logits);
-    }
-    p.bytes = at;
-    return p;
-}
 
 hipError_t launch_attn_decode(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     switch (type) {

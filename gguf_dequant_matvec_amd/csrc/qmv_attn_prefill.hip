@@ -24,8 +24,6 @@ namespace qmv {
 
 namespace {
 
-constexpr int kBM = 128, kBK = 64;
-
 template <int HD>
 struct Lds {  // one buffer, bytes
     static constexpr int kRow = HD * 2;                 // K row
@@ -527,40 +525,7 @@ hipError_t launch_type(const AttnArgs &a, int64_t slots, hipStream_t s) {
     }
 }
 
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
 }  // namespace
-
-AttnPlan attn_prefill_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int64_t rows,
-                           int64_t max_len, int window, int sinks) {
-    AttnPlan p{};
-    (void)type;
-    // row tiles: at least these; with prompts of different lengths each
-    // sequence may add a partly filled one
-    const int64_t tiles = (rows * group + kBM - 1) / kBM;
-    p.tiles = (int)(tiles + n_seq);
-    p.part_rows = rows * n_kv * group;
-    int64_t most = max_len;
-    if (window > 0) {
-        const int64_t w = (int64_t)window + kBM / group + sinks + 2 * kBK;
-        if (w < most) most = w;
-    }
-    const int64_t chunks = (most + kBK - 1) / kBK;
-    const int64_t base = tiles * n_kv;
-    int64_t splits = 512 / base;                      // two workgroups per compute unit
-    if (splits > chunks / 4) splits = chunks / 4;     // at least four chunks each
-    if (splits > 64) splits = 64;
-    p.splits = splits < 1 ? 1 : (int)splits;
-    size_t at = 0;
-    if (p.splits > 1) {
-        p.ml_off = at;
-        at = up256(at + sizeof(float2) * (size_t)p.splits * p.part_rows);
-        p.o_off = at;
-        at = up256(at + sizeof(float) * (size_t)p.splits * p.part_rows * hd);
-    }
-    p.bytes = at;
-    return p;
-}
 
 hipError_t launch_attn_prefill(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
     const int64_t slots = a.start ? p.tiles : a.c.n_seq * ((a.n * a.group + kBM - 1) / kBM);

@@ -100,20 +100,8 @@ struct AttnArgs {
     int64_t ld_acc;
 };
 
-// How a call is cut: 16-row operand tiles per wave, row tiles per key-value
-// head, pieces of the cache's length (as in AttnArgs), slots for the pieces of
-// a decode call, waves per workgroup; workspace offsets in bytes.
-struct AttnPlan {
-    int rt, tiles, splits, parts, slots, waves;
-    int64_t part_rows;
-    int64_t ld_logits;
-    size_t ml_off, o_off, share_off, logits_off, bytes;
-};
-AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int n,
-                          int64_t max_len, int window, int sinks, bool with_acc);
+struct AttnPlan;
 hipError_t launch_attn_decode(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s);
-AttnPlan attn_prefill_plan(int type, int hd, int64_t n_seq, int n_kv, int group, int64_t rows,
-                           int64_t max_len, int window, int sinks);
 hipError_t launch_attn_prefill(int type, const AttnArgs &a, const AttnPlan &p, hipStream_t s);
 
 }  // namespace qmv

@@ -56,3 +56,28 @@ def test_abi_host_layer_under_asan_ubsan(tmp_path):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0")
     rc, out = run([exe], ROOT, env=env)
     assert rc == 0 and "ok" in out and "runtime error" not in out and "Sanitizer" not in out, out
+
+
+def test_attention_host_layer_under_asan_ubsan(tmp_path):
+    """The cache and attention calls' checks and plans (attn_sanitize_driver.cpp)."""
+    hipcc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not found")
+    host_san = []
+    for f in SAN:
+        host_san += ["-Xarch_host", f]
+    csrc = os.path.join(ROOT, "gguf_dequant_matvec_amd", "csrc")
+    common = ["-x", "hip", "-std=c++17", "-O1", "-g", "--offload-arch=gfx950", "-I" + os.path.join(ROOT, "include"),
+              "-I" + csrc, *host_san]
+    objs = []
+    for src in (os.path.join(csrc, "qmv_attn_api.cpp"), os.path.join(csrc, "qmv_attn_plan.cpp"),
+                os.path.join(ROOT, "tests", "attn_sanitize_driver.cpp")):
+        obj = str(tmp_path / (os.path.basename(src) + ".o"))
+        rc, out = run([hipcc, *common, "-c", src, "-o", obj], ROOT)
+        assert rc == 0, out
+        objs.append(obj)
+    exe = str(tmp_path / "attn_san")
+    rc, out = run([hipcc, "--offload-arch=gfx950", *host_san, *objs, "-o", exe], ROOT)
+    assert rc == 0, out
+    rc, out = run([exe], ROOT, env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+    assert rc == 0 and "ok" in out and "runtime error" not in out and "Sanitizer" not in out, out
