@@ -449,7 +449,8 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * products of weight and V row scale down to 2^-36 of the row's largest weight
  * times the largest scale that any of the sequence's new tokens sees, for V row
  * scales between 2^-100 and 2^100 (K row scales up to 2^97); bf16 ones weights
- * down to 2^-60 of the largest, with V of any finite value.
+ * down to 2^-60 of the largest, with V of any finite value (in steps of no more
+ * than 2^-143 max_len).
  * Results do not depend on anything but the arguments; a row's last bits may
  * depend on the call's other lengths, which decide where long ones are cut.
  * workspace: device, >= qmv_attn_decode_workspace() bytes (NULL when that is

@@ -1059,3 +1059,52 @@ def test_seen_values_without_weight(t, bad, spot, top, window):
         cols = slice(None) if t == "i8" else slice(5, 6)
         assert not np.isfinite(got[sees][:, :, cols]).any(), f"{what} {t} {bad} at {spot}, weight at {top}"
         assert np.isfinite(got[~sees]).all(), f"{what} {t} {bad} at {spot}, weight at {top}"
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("exp", [-100, 100])
+@pytest.mark.parametrize("flat", [True, False])
+def test_value_range_in_the_longest_call(t, exp, flat):
+    """Values at the ends of the range in calls whose max_len is the largest: the
+    range goes by the sequences' own lengths.  (f16: its own range.)"""
+    length, hd, page, n = 700, 64, 4096, 20
+    c, rng = make_cache(t, 1, hd, page, [length, 0], 82)
+    exp = exp if t != "f16" else exp // 10
+    k, v = (rng.standard_normal((length, 1, hd), dtype=np.float32) for _ in range(2))
+    _fill(c, 0, k * np.float32(not flat), v * np.float32(2.0 ** exp))
+    table = np.full((2, (1 << 30) // page), -1, np.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table, c.cap = table, 1 << 30
+    qh = synth.normal(3, synth.T_X, (2 * n, 4, hd), 1.5)
+    d = Dev(c)
+    for m, what in ((1, "decode"), (16, "decode"), (n, "prefill")):
+        rows = np.ascontiguousarray(qh[:2 * m])
+        out = torch.full((2 * m, 4 * hd), -7.0, device="cuda")
+        if what == "decode":
+            ws = workspace(q.qmv_attn_decode_workspace(d.h, m, 4, c.cap))
+            q.qmv_attn_decode(d.h, m, 4, dev(rows.reshape(2 * m, -1)), 0.125, out, c.cap, workspace=ws)
+        else:
+            ws = workspace(q.qmv_attn_prefill_workspace(d.h, 2 * m, 4, c.cap))
+            q.qmv_attn_prefill(d.h, 2 * m, 4, dev(rows.reshape(2 * m, -1)), 0.125, out, c.cap, workspace=ws)
+        want, tol, _, _ = ref.attention(c, [0, m, 2 * m], rows, 0.125, length)
+        close(host(out).reshape(want.shape), want, tol, f"{what} {t} m{m} 2^{exp}")
+
+
+@pytest.mark.parametrize("t", ["f16", "bf16", "i8"])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_other_rows_of_a_bad_query(t, bad, hd):
+    """A query that is not finite leaves its own row unspecified and no other."""
+    length, n = 200, 40
+    c, rng = make_cache(t, 1, hd, 16, [length], 83)
+    qh = synth.normal(3, synth.T_X, (n, 3, hd), 1.5)
+    scale = float(np.float32(hd ** -0.5))
+    want, tol, _, _ = ref.attention(c, [0, n], qh, scale, c.cap)
+    for i, j, col in ((n - 1, 0, 3), (n - 2, 2, 0), (n - 13, 1, hd - 1)):
+        x = qh.copy()
+        x[i, j, col] = bad
+        for what, rows, got in _both(c, x, scale, n_decode=(16,)):
+            m = len(rows)
+            rest = np.ones((m, 3), bool)
+            rest[i - (n - m), j] = False
+            close(got[rest], want[n - m:][rest], tol[n - m:][rest], f"{what} {t} query {i} {bad}")
