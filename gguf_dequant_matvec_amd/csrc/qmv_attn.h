@@ -37,11 +37,14 @@ __device__ __forceinline__ float past_max(float x, float factor, float m) {
     const float t = x * factor;
     return t - m;
 }
-// Whether a logit is so far above the running maximum that this has to move.
-__device__ __forceinline__ bool above_max(float x, float m) {
+// The difference of two rounded values: never one operation with the product
+// that x may come from, of which m knows the rounded value.
+__device__ __forceinline__ float minus(float x, float m) {
 #pragma clang fp contract(off)
-    return x - m > kSlack;
+    return x - m;
 }
+// Whether a logit is so far above the running maximum that this has to move.
+__device__ __forceinline__ bool above_max(float x, float m) { return minus(x, m) > kSlack; }
 
 // 8-bit V rows carry their scale into the probabilities; `vmul`, a power of
 // two, keeps the largest scale so far at most 1.  Before the first row:

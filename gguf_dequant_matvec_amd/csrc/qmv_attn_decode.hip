@@ -433,7 +433,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                     float mx = x[0];
 #pragma unroll
                     for (int e = 1; e < PER; e++) mx = fmaxf(mx, x[e]);
-                    if (__any((mx - mrun[rt]) * qscale[rt] > kSlack || (mrun[rt] == kNoMax && mx > kNoMax))) {
+                    if (__any(minus(mx, mrun[rt]) * qscale[rt] > kSlack || (mrun[rt] == kNoMax && mx > kNoMax))) {
                         mx = fmaxf(mx, __shfl_xor(mx, 16));
                         mx = fmaxf(mx, __shfl_xor(mx, 32));
                         const float mnew = fmaxf(mrun[rt], mx);
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 #pragma unroll
                     for (int e = 0; e < PER; e++) {
                         const bool hidden = TYPE == kKvI8 && !whole && x[e] == -__builtin_inff();
-                        x[e] = exp2_fast(fmaf(x[e] - mrun[rt], qscale[rt], off));
+                        x[e] = exp2_fast(fmaf(minus(x[e], mrun[rt]), qscale[rt], off));
                         sum += x[e];
                         if constexpr (TYPE == kKvI8) x[e] = hidden ? 0.f : x[e] * vt.vs[e];  // (which may be NaN)
                     }

@@ -416,7 +416,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
                 for (int t = 0; t < DT; t++) o[t] *= r;
             }
             float mbase = mrun;
-            if (__builtin_expect(far, 0)) {  // (else laid out in the way: bf16, 128 columns, 320 -> 329 us)
+            // (bf16 of 128 columns gains from the branch laid out of the way, 4096
+            // tokens 329 -> 321 us; others would keep a register in scratch for it)
+            if (TYPE == kKvBF16 && HD == 128 ? __builtin_expect(far, 0) : far) {
                 mbase = 0.f;
                 const float back = 1.f / qscale;
 #pragma unroll
