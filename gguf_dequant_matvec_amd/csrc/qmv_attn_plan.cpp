@@ -24,11 +24,13 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
         if (w < most) most = w;
     }
     const int64_t chunks = (most + ck - 1) / ck;
-    // Workgroups for 256 compute units: as many as fit at once, because a second
-    // round of them waits for its lengths, table and first rows again (16
-    // sequences of 8192 positions of 256 columns: one workgroup a unit 101 us,
-    // two 113; 32 of 6144 of 64 columns: three 72 us, two 74, four 81).  Tiles of
-    // 32 rows take one workgroup, of eight waves (the drafted tokens: 24 us
+    // Workgroups for 256 compute units: about as many as fit at once, because a
+    // second round of them waits for its lengths, table and first rows again (16
+    // sequences of 8192 positions of 256 columns: one workgroup a unit 104 us,
+    // two 110; 32 of 6144 of 64 columns: three 76 us, two 79, four 90).  Every
+    // sequence is cut into the same whole number of pieces, the next above, which
+    // for three or five to seven sequences is up to a tenth more than fit.  Tiles
+    // of 32 rows take one workgroup, of eight waves (the drafted tokens: 24 us
     // against 26 with 512 of four and 34 with 1024) or, where registers say so,
     // of four.
     const int64_t heads = (int64_t)n_kv * p.tiles, base = n_seq * heads;
@@ -40,8 +42,8 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
     p.slots = (int)(n_seq * p.splits);
     // Where such a piece may be long, lengths decide: evenly cut ranges.  With
     // sequences enough for all workgroups the grid's own order balances them
-    // better (512 of 768 to 1536 positions: 409 against 422 us; but 128 of 1 to
-    // 2048: 117 against 96), so the more there are, the longer the longest
+    // better (512 of 768 to 1536 positions: 421 against 431 us; but 128 of 1 to
+    // 2048: 123 against 108), so the more there are, the longer the longest
     // has to be.
     const int waves = p.rt == 2 && eight_fit(type, hd, 2) ? 8 : 4;
     const int64_t long_chunks = base < fit ? 5 * waves * p.splits : 8 * waves * base / fit;
@@ -88,8 +90,10 @@ AttnPlan attn_prefill_plan(int type, int hd, int64_t n_seq, int n_kv, int group,
         if (w < most) most = w;
     }
     const int64_t chunks = (most + kBK - 1) / kBK;
+    // two workgroups per compute unit (counted as if tiles ran on from sequence
+    // to sequence: few rows of many sequences are cut further than that)
     const int64_t base = tiles * n_kv;
-    int64_t splits = 512 / base;                      // two workgroups per compute unit
+    int64_t splits = 512 / base;
     if (splits > chunks / 4) splits = chunks / 4;     // at least four chunks each
     if (splits > 64) splits = 64;
     p.splits = splits < 1 ? 1 : (int)splits;

@@ -486,7 +486,9 @@ size_t qmv_attn_prefill_workspace(const qmv_kv_cache *cache, int64_t n, int32_t 
  * kept rows go, in their old order, to positions 0, 1, ... of the pages of
  * dst_table (int32 [n_seq][dst_ld], device; same pool, keep <= dst_ld *
  * page_size), which must share no page with the live ones; a hole there
- * drops what would go to it, and a row kept from a hole becomes zeros.  A
+ * drops what would go to it, and a row kept from a hole becomes zeros, which
+ * later calls see (logit 0, value 0) where they did not see the hole: positions
+ * whose pages were given back should not be among the protected ones.  A
  * sequence with seq_len <= keep is copied whole.  Afterwards the caller makes
  * dst_table the cache's table.
  * acc: f32 [n_seq][n_kv_heads][ld_acc]; seq_len is taken as at most ld_acc.
