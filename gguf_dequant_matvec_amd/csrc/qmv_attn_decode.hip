@@ -21,7 +21,7 @@
 // Measured (mean of 60 profiled launches): 32 sequences up to 8150 positions, 32
 // / 8 heads of 128, f16, 805 MB of cache: 136 us (5.9 TB/s; a streaming read of
 // the same size reaches 7.1) and 5.0 us for the join; one sequence of 131071
-// int8 positions, 277 MB: 62 and 4.8 us; 301 positions, 9 / 3 heads of 64: 6.6
+// int8 positions, 277 MB: 61 and 4.8 us; 301 positions, 9 / 3 heads of 64: 6.6
 // us, a chain of latencies.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
@@ -133,8 +133,8 @@ struct VTile {
 // that.  Workgroup p's piece of sequence s goes to slot p + s: the pairs are a
 // staircase, so slots are distinct, and a sequence's are neighbours.
 // Measured (32 / 8 heads of 128, f16), against equal numbers of pieces: 32
-// sequences of 354 to 8192 positions, evenly spaced, 561 MB, 99 us against 123;
-// 63 of 300 and one of 65536 among them, 69 us against 1163; 32 of 6144, 140 us
+// sequences of 354 to 8192 positions, evenly spaced, 561 MB, 98 us against 123;
+// 63 of 300 and one of 65536 among them, 68 us against 1161; 32 of 6144, 140 us
 // against 138.
 constexpr int kEnter = 4, kMinPiece = 8;  // chunks
 

@@ -42,8 +42,8 @@ AttnPlan attn_decode_plan(int type, int hd, int64_t n_seq, int n_kv, int group, 
     p.slots = (int)(n_seq * p.splits);
     // Where such a piece may be long, lengths decide: evenly cut ranges.  With
     // sequences enough for all workgroups the grid's own order balances them
-    // better (512 of 768 to 1536 positions: 421 against 431 us; but 128 of 1 to
-    // 2048: 123 against 108), so the more there are, the longer the longest
+    // better (512 of 768 to 1536 positions: 421 against 430 us; but 128 of 1 to
+    // 2048: 122 against 108), so the more there are, the longer the longest
     // has to be.
     const int waves = p.rt == 2 && eight_fit(type, hd, 2) ? 8 : 4;
     const int64_t long_chunks = base < fit ? 5 * waves * p.splits : 8 * waves * base / fit;

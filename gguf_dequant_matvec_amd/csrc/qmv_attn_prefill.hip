@@ -13,9 +13,9 @@
 // accumulators are 8 consecutive positions of its query, the operand layout
 // of P, and no value moves between lanes.  K rows are swizzled by 16-byte
 // pieces and V keeps the cache's block layout; both are read without bank
-// conflicts.  Measured: 4096 tokens, 32 / 8 heads of 128, f16: 250 - 263 us,
-// 1.05 - 1.1 PFLOP/s of operand work where library products reach 1.15; int8
-// prompts in a window of 1024, heads of 64: 258 - 269 us, bound by the softmax's
+// conflicts.  Measured: 4096 tokens, 32 / 8 heads of 128, f16: 250 - 274 us,
+// 1.0 - 1.1 PFLOP/s of operand work where library products reach 1.15; int8
+// prompts in a window of 1024, heads of 64: 258 - 273 us, bound by the softmax's
 // vector instructions.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
