@@ -38,11 +38,14 @@ OP_MOE = 2
 OP_GEMM_N = 3
 OP_SHORT_CONV = 4
 OP_GEMM = 5
-# types of a key-value cache (the GGUF ids of F16, I8 and BF16)
+# types of a key-value cache (the GGUF ids of F16, I8 and BF16; 4 bits have none)
 KV_F16 = 1
 KV_I8 = 24
 KV_BF16 = 30
-KV_TYPES = {"f16": KV_F16, "i8": KV_I8, "bf16": KV_BF16}
+KV_Q4 = 104
+KV_TYPES = {"f16": KV_F16, "i8": KV_I8, "bf16": KV_BF16, "q4": KV_Q4}
+# which columns turn together
+ROPE_PAIRS = {"halves": 0, "adjacent": 1}
 MAX_ATTN_N = 16
 MAX_KV_ROWS = 1 << 27
 MAX_K = 32768
@@ -62,7 +65,8 @@ EXPORTS = ["qmv_q8_0", "qmv_q4_k", "qmv_q6_k", "qmv_q4_0", "qmv_q4_1", "qmv_q5_0
            "qmv_quantize", "qmv_row_bytes", "qmv_workspace_bytes", "qmv_last_hip_error",
            "qmv_status_str", "qmv_probe_stream_read", "qmv_time_next_launch",
            "qmv_kv_page_bytes", "qmv_kv_append", "qmv_attn_decode", "qmv_attn_decode_workspace",
-           "qmv_attn_prefill", "qmv_attn_prefill_workspace", "qmv_kv_evict"]
+           "qmv_attn_prefill", "qmv_attn_prefill_workspace", "qmv_kv_evict", "qmv_kv_read",
+           "qmv_qk_norm_rope", "qmv_kv_append_rope", "qmv_kv_reserve", "qmv_kv_release"]
 
 
 class QmvError(RuntimeError):
@@ -120,6 +124,11 @@ def load():
         "qmv_attn_decode": [P, i32, i32, P, i64, cf, i32, i32, P, i64, P, i64, P, sz, P],
         "qmv_attn_prefill": [P, i64, P, i32, P, i64, cf, i32, i32, P, i64, P, sz, P],
         "qmv_kv_evict": [P, P, i64, i32, i32, i32, P, i64, P, P, i64, P, P],
+        "qmv_kv_read": [P, i64, P, P, i64, P, i64, P],
+        "qmv_qk_norm_rope": [P, i32, i64, P, i32, P, i64, P, i64, i32, P, i64, P, i64, P],
+        "qmv_kv_append_rope": [P, P, i64, P, i32, P, i64, P, i64, P, i64, P, i64, P],
+        "qmv_kv_reserve": [P, P, P, P, i64, P, P, P, P, P],
+        "qmv_kv_release": [P, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -485,6 +494,98 @@ def qmv_kv_append(cache, n, k, v, start=None, ldk=None, ldv=None, stream=None):
     _check_start(cache, start)
     _call("qmv_kv_append", cache._address, n, _ptr(start), _ptr(k), ldk, _ptr(v), ldv,
           _cache_stream(cache, stream, start, k, v))
+
+
+def qmv_kv_read(cache, n, k, v, start=None, ldk=None, ldv=None, stream=None):
+    width = cache.n_kv_heads * cache.head_dim
+    ldk, ldv = _f32_rows("k", k, ldk, n, width), _f32_rows("v", v, ldv, n, width)
+    _check_start(cache, start)
+    _call("qmv_kv_read", cache._address, n, _ptr(start), _ptr(k), ldk, _ptr(v), ldv,
+          _cache_stream(cache, stream, start, k, v))
+
+
+class _QkRopeStruct(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class QkRope:
+    """Norms of queries and keys and the rotation (qmv_qk_rope): `freq` float64
+    [rot_dim / 2], radians a position; `pairs` "halves" or "adjacent"; `q_norm`,
+    `k_norm` float32 [head_dim] or None.  Tensors are checked and kept alive; their
+    values are read when a call runs."""
+
+    def __init__(self, freq, rot_dim, pairs="halves", q_norm=None, k_norm=None, eps=1e-5):
+        pairs = ROPE_PAIRS[pairs] if isinstance(pairs, str) else int(pairs)
+        _check_dense("freq", freq, "float64", max(rot_dim, 0) // 2)
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            _check_dense(name, w, "float32", 0)
+        self.freq, self.rot_dim, self.pairs = freq, rot_dim, pairs
+        self.q_norm, self.k_norm, self.eps = q_norm, k_norm, eps
+        self.device = None
+        for a in (freq, q_norm, k_norm):
+            if a is not None and not isinstance(a, int):
+                if self.device is not None and a.get_device() != self.device:
+                    raise ValueError(f"a tensor on {a.device}, another on GPU {self.device}")
+                self.device = a.get_device()
+        if self.device is not None and self.device < 0:
+            raise ValueError("the rotation's tensors are not on a GPU")
+        self._struct = _QkRopeStruct(_ptr(freq), rot_dim, pairs, _ptr(q_norm), _ptr(k_norm), eps)
+        self._address = ctypes.addressof(self._struct)
+
+    def __setattr__(self, name, value):
+        if "_address" in self.__dict__:
+            raise AttributeError("a QkRope stays as it was made: change its tensors in place, or make another")
+        object.__setattr__(self, name, value)
+
+    def _check_width(self, head_dim):
+        for name, w in (("q_norm", self.q_norm), ("k_norm", self.k_norm)):
+            if w is not None and not isinstance(w, int) and w.numel() < head_dim:
+                raise ValueError(f"{name} must hold {head_dim} values")
+
+
+def qmv_qk_norm_rope(rope, head_dim, n, pos, n_heads=0, q=None, q_out=None, n_kv_heads=0, k=None, k_out=None,
+                     ldq=None, ldqo=None, ldk=None, ldko=None, stream=None):
+    rope._check_width(head_dim)
+    _check_dense("pos", pos, "int32", n)
+    lds = [_f32_rows(name, a, ld, n, heads * head_dim) if heads else 0 for name, a, ld, heads in
+           (("q", q, ldq, n_heads), ("q_out", q_out, ldqo, n_heads), ("k", k, ldk, n_kv_heads),
+            ("k_out", k_out, ldko, n_kv_heads))]
+    _call("qmv_qk_norm_rope", rope._address, head_dim, n, _ptr(pos), n_heads, _ptr(q), lds[0], _ptr(q_out), lds[1],
+          n_kv_heads, _ptr(k), lds[2], _ptr(k_out), lds[3], _cache_stream(rope, stream, pos, q, q_out, k, k_out))
+
+
+def qmv_kv_append_rope(cache, rope, n, n_heads, q, q_out, k, v, start=None, ldq=None, ldqo=None, ldk=None, ldv=None,
+                       stream=None):
+    rope._check_width(cache.head_dim)
+    width = cache.n_kv_heads * cache.head_dim
+    ldk, ldv = _f32_rows("k", k, ldk, n, width), _f32_rows("v", v, ldv, n, width)
+    ldq = _f32_rows("q", q, ldq, n, n_heads * cache.head_dim)
+    ldqo = _f32_rows("q_out", q_out, ldqo, n, n_heads * cache.head_dim)
+    _check_start(cache, start)
+    if rope.device is not None and cache.device is not None and rope.device != cache.device:
+        raise ValueError(f"the rotation on GPU {rope.device}, the cache on GPU {cache.device}")
+    _call("qmv_kv_append_rope", cache._address, rope._address, n, _ptr(start), n_heads, _ptr(q), ldq, _ptr(q_out),
+          ldqo, _ptr(k), ldk, _ptr(v), ldv, _cache_stream(cache, stream, start, q, q_out, k, v))
+
+
+def qmv_kv_reserve(cache, add, free_pages, free_count, n, granted, start, pos=None, slot=None, stream=None):
+    for name, a, dtype, numel in (("add", add, "int32", cache.n_seq), ("free_pages", free_pages, "int32", cache.n_pages),
+                                  ("free_count", free_count, "int32", 1), ("granted", granted, "int32", cache.n_seq),
+                                  ("pos", pos, "int32", n), ("slot", slot, "int64", n)):
+        _check_dense(name, a, dtype, numel)
+    _check_start(cache, start)
+    _call("qmv_kv_reserve", cache._address, _ptr(add), _ptr(free_pages), _ptr(free_count), n, _ptr(granted),
+          _ptr(start), _ptr(pos), _ptr(slot),
+          _cache_stream(cache, stream, add, free_pages, free_count, granted, start, pos, slot))
+
+
+def qmv_kv_release(cache, new_len, free_pages, free_count, stream=None):
+    for name, a, numel in (("new_len", new_len, cache.n_seq), ("free_pages", free_pages, cache.n_pages),
+                           ("free_count", free_count, 1)):
+        _check_dense(name, a, "int32", numel)
+    _call("qmv_kv_release", cache._address, _ptr(new_len), _ptr(free_pages), _ptr(free_count),
+          _cache_stream(cache, stream, new_len, free_pages, free_count))
 
 
 def qmv_attn_decode_workspace(cache, n, n_heads, max_len, window=0, sinks=0, with_acc=False) -> int:

@@ -31,6 +31,11 @@ ROW_FORMATS = ["Q2K", "Q3K", "Q4K", "Q5K", "Q6K", "Q40", "Q41", "Q50", "Q51", "Q
 ROW_MODES = ["kModeStore", "kModeArgmax", "kModeMoeGateUp", "kModeMoeDown", "kModeSiluUp",
              "kModeShortConv"]
 INST_SRC = "qmv_rows_inst.hip"
+# Bundles of neighbouring loads are off here: with a load's registers changed one
+# by one in a branch (scales that are not finite are cleared), the pass that
+# forms them loses track of the other ones, and a kernel read registers that were
+# in use for something else (-verify-machineinstrs reports it).
+EXTRA = {"qmv_attn_decode.hip": ["-mllvm", "-amdgpu-max-memory-clause=1"]}
 
 
 def hipcc() -> str:
@@ -61,7 +66,7 @@ def units():
                     out.append((os.path.join(CSRC, f), f"{f}.{mode}.{fmt}.o",
                                 [f"-DQMV_INST_FMT={fmt}", f"-DQMV_INST_MODE={mode}"]))
         else:
-            out.append((os.path.join(CSRC, f), f + ".o", []))
+            out.append((os.path.join(CSRC, f), f + ".o", EXTRA.get(f, [])))
     return out
 
 

@@ -121,7 +121,7 @@ __device__ __forceinline__ float bias_of(const AttnArgs &a) {
 // with it).
 template <int TYPE>
 __device__ __forceinline__ float sum_bias_of(const AttnArgs &a) {
-    return TYPE == kKvF16 ? kBias : a.bias;
+    return TYPE == kKvF16 || TYPE == kKvQ4 ? kBias : a.bias;
 }
 
 struct U128 { uint32_t w[4]; };
@@ -181,6 +181,35 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t v) {
     const uint32_t b = __builtin_amdgcn_perm(0x64646464u, u, 0x07030702u);
     return make_uint2(__builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, a) - bias),
                       __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, b) - bias));
+}
+
+// 4-bit codes to f16, exactly.  A dword has eight: its halves' codes at bits 4 j
+// are pair j.  At bits 6 .. 9 of the f16 16.0 a code u gives 16 + u; that times
+// the scale d, less 24 d, is (u - 8) d in one fused operation, whose result and
+// addend are f16 values since d has eight bits of significand and is at most
+// 2720 (the writer's rule).  Three instructions a pair.  Pairs of a dword of K
+// (bytes of columns 4 i .. 4 i + 3, and of those 16 further on): (0, 2), (16, 18),
+// (1, 3), (17, 19); of V: positions (0, 1), (2, 3) of a column in pairs 0 and 2,
+// of the column 16 further on in 1 and 3.
+__device__ __forceinline__ uint32_t q4_addend(uint32_t d2) {
+    const f16x2_t m = {(_Float16)-24.0f, (_Float16)-24.0f};
+    return __builtin_bit_cast(uint32_t, as_f16x2(d2) * m);
+}
+template <int PAIR>
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t d2, uint32_t addend) {
+    const uint32_t at6 = PAIR == 0 ? w << 6 : PAIR == 1 ? w << 2 : PAIR == 2 ? w >> 2 : w >> 6;
+    const f16x2_t u = as_f16x2((at6 & 0x03C003C0u) | 0x4C004C00u);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(u, as_f16x2(d2), as_f16x2(addend)));
+}
+__device__ __forceinline__ U128 q4_row8(uint32_t w, uint32_t d2) {  // a dword of K
+    const uint32_t c = q4_addend(d2);
+    return U128{{q4_pair<0>(w, d2, c), q4_pair<1>(w, d2, c), q4_pair<2>(w, d2, c), q4_pair<3>(w, d2, c)}};
+}
+// ... and eight values of a row in that order, its dword number D.
+__device__ __forceinline__ void q4_cols(const float *row, int D, float *f) {
+    const uint8_t *src = reinterpret_cast<const uint8_t *>(row + 32 * (D / 4) + 4 * (D % 4));
+    const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 64));
+    f[0] = x.x, f[1] = x.z, f[2] = y.x, f[3] = y.z, f[4] = x.y, f[5] = x.w, f[6] = y.y, f[7] = y.w;
 }
 
 // The chunks of `ck` positions that hold every position some query with

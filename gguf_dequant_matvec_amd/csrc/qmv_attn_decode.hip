@@ -34,7 +34,8 @@ template <int TYPE>
 constexpr int kChunk = decode_chunk(TYPE);  // positions a wave takes at a time
 
 // Column of element j of the operand of step t in lane group g: 8-bit rows are
-// read in 16-byte pieces of two steps where 64 divides the row.
+// read in 16-byte pieces of two steps where 64 divides the row.  (4-bit rows: the
+// order of q4_cols, dword HD / 32 g + t.)
 template <int TYPE, int HD>
 __device__ __forceinline__ constexpr int col_of(int t, int g) {
     return TYPE == kKvI8 && HD % 64 == 0 ? 64 * (t / 2) + 16 * g + 8 * (t % 2) : 32 * t + 8 * g;
@@ -121,6 +122,85 @@ struct VTile {
         } else {
             return as_vec<Vec>(U128{{v[t][0], v[t][1], v[t][2], v[t][3]}});
         }
+    }
+};
+
+// 4-bit rows: a lane's quarter of a row is HD / 32 dwords, and their scales; at
+// 128 columns the quarter is one block.
+template <int HD>
+struct KTile<kKvQ4, HD> {
+    static constexpr int R = kChunk<kKvQ4> / 16, W = HD / 32;
+    static constexpr int NB = HD == 96 ? 3 : HD == 256 ? 2 : 1;  // scales (96: one a dword, its blocks change inside)
+    uint32_t k[R][W];
+    uint16_t d[R][NB];
+
+    template <bool NT>
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
+        const int pos = chunk * kChunk<kKvQ4> + kChunk<kKvQ4> / 4 * (m >> 2);
+        const int slot = (pos & ((1 << c.page_shift) - 1)) + (m & 3);
+        const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
+        const uint8_t *kp = head + (int64_t)slot * (HD / 2) + 4 * W * g;
+        const uint16_t *dp = reinterpret_cast<const uint16_t *>(head + ((int64_t)HD << c.page_shift)) + (int64_t)slot * (HD / 32);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const uint8_t *row = kp + r * 4 * (HD / 2);
+            if constexpr (HD == 96) {
+                __builtin_memcpy(k[r], row, 12);
+            } else if constexpr (HD == 64) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(row);
+                k[r][0] = w.x, k[r][1] = w.y;
+            } else {
+#pragma unroll
+                for (int t = 0; t < W / 4; t++) {
+                    const u32x4 w = load_stream<NT>(row + 16 * t);
+                    k[r][4 * t] = w.x, k[r][4 * t + 1] = w.y, k[r][4 * t + 2] = w.z, k[r][4 * t + 3] = w.w;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NB; j++) d[r][j] = dp[r * 4 * (HD / 32) + (HD == 96 ? (3 * g + j) / 4 : W * g / 4 + j)];
+        }
+    }
+    template <class Vec>
+    __device__ __forceinline__ Vec op(int u, int b, int t) const {
+        const uint32_t s = d[2 * u + b][HD == 96 ? t : t / 4];
+        return as_vec<Vec>(q4_row8(k[2 * u + b][t], s | s << 16));
+    }
+};
+
+// ... V: a lane's piece is 16 positions of two columns, 16 apart; their scales
+// as pairs of positions.
+template <int HD>
+struct VTile<kKvQ4, HD> {
+    static constexpr int DT = HD / 16, NB = HD / 32;
+    uint32_t v[NB][4], d[NB][8];
+
+    template <bool NT>
+    __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
+        const int slot = (chunk * kChunk<kKvQ4> + kChunk<kKvQ4> / 4 * g) & ((1 << c.page_shift) - 1);
+        const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
+        const uint8_t *vp = head + ((int64_t)(HD / 2) << c.page_shift) + (int64_t)slot * (HD / 2) + 16 * m;
+        const uint8_t *dp = head + ((int64_t)(HD + HD / 16) << c.page_shift) + 2 * slot;
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+            const u32x4 w = load_stream<NT>(vp + 256 * b);
+            v[b][0] = w.x, v[b][1] = w.y, v[b][2] = w.z, v[b][3] = w.w;
+            const u32x4 *sp = reinterpret_cast<const u32x4 *>(dp + ((int64_t)(2 * b) << c.page_shift));
+            const u32x4 x = sp[0], y = sp[1];
+            d[b][0] = x.x, d[b][1] = x.y, d[b][2] = x.z, d[b][3] = x.w;
+            d[b][4] = y.x, d[b][5] = y.y, d[b][6] = y.z, d[b][7] = y.w;
+        }
+    }
+    template <class Vec>
+    __device__ __forceinline__ Vec op(int u, int t) const {
+        const int b = t / 2;
+        U128 x;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t w = v[b][2 * u + j / 2], s = d[b][4 * u + j], c = q4_addend(s);
+            x.w[j] = t % 2 == 0 ? (j % 2 == 0 ? q4_pair<0>(w, s, c) : q4_pair<2>(w, s, c))
+                                : (j % 2 == 0 ? q4_pair<1>(w, s, c) : q4_pair<3>(w, s, c));
+        }
+        return as_vec<Vec>(x);
     }
 };
 
@@ -327,9 +407,14 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                 float big = 0.f;
 #pragma unroll
                 for (int t = 0; t < KS; t++) {
-                    const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
-                    const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
-                    const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                    float w[8];
+                    if constexpr (TYPE == kKvQ4) {
+                        q4_cols(qp, KS * g + t, w);
+                    } else {
+                        const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + col_of<TYPE, HD>(t, g));
+                        const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+                        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         f[t][e] = live ? w[e] * a.q_sign : 0.f;
@@ -458,7 +543,38 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 #pragma unroll
                     for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
                 }
-                if constexpr (TYPE != kKvI8) {
+                if constexpr (TYPE == kKvQ4) {  // a 4-bit value is not finite where its block's scale is not
+                    if (!whole) {
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int b = 0; b < HD / 32; b++)
+#pragma unroll
+                            for (int j = 0; j < 8; j++) bad |= not_finite<Op>(vt.d[b][j]);
+                        if (__any(bad != 0)) {
+#pragma unroll
+                            for (int u = 0; u < SUB; u++) {
+                                U128 seen[RT];
+#pragma unroll
+                                for (int rt = 0; rt < RT; rt++) seen[rt] = seen8(ok, pos[rt], key0 + 8 * u, a.window, a.sinks);
+#pragma unroll
+                                for (int b = 0; b < HD / 32; b++) {
+                                    U128 marks;
+#pragma unroll
+                                    for (int j = 0; j < 4; j++) {
+                                        const uint32_t x = not_finite<Op>(vt.d[b][4 * u + j]);
+                                        vt.d[b][4 * u + j] &= ~(x * 0xFFFFu);
+                                        marks.w[j] = x * kHuge;
+                                    }
+#pragma unroll
+                                    for (int rt = 0; rt < RT; rt++) {
+                                        o[rt][2 * b] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][2 * b]);
+                                        o[rt][2 * b + 1] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][2 * b + 1]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                } else if constexpr (TYPE != kKvI8) {
                     if (!whole) {
                         uint32_t bad = 0;
 #pragma unroll
@@ -732,6 +848,7 @@ hipError_t launch_attn_decode(int type, const AttnArgs &a, const AttnPlan &p, hi
     case kKvF16: return launch_type<kKvF16>(a, p, s);
     case kKvBF16: return launch_type<kKvBF16>(a, p, s);
     case kKvI8: return launch_type<kKvI8>(a, p, s);
+    case kKvQ4: return launch_type<kKvQ4>(a, p, s);
     default: return hipErrorInvalidValue;
     }
 }

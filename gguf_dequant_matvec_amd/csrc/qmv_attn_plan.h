@@ -11,7 +11,7 @@ constexpr float kBias = 11.f, kSlack = 4.f;  // the kernels' probabilities (qmv_
 
 constexpr int kBM = 128, kBK = 64;  // prompts: rows a workgroup takes, positions a chunk
 // Decode: positions a wave takes at a time (16 KB at 128 columns).
-constexpr int decode_chunk(int type) { return type == kKvI8 ? 64 : 32; }
+constexpr int decode_chunk(int type) { return type == kKvI8 || type == kKvQ4 ? 64 : 32; }
 constexpr int kMaxPieces = 512;  // pieces of an output row that the join takes
 
 // Workgroups of four waves and 16-row tiles that the registers of a compute

@@ -53,13 +53,17 @@ __device__ __forceinline__ int vslot(int d, int p) { return 2 * d + (p ^ ((d >> 
 
 // A wave's 16 positions of a chunk on their way to LDS.  f16 and bf16 values
 // go straight from memory to LDS (each lane names the piece whose place its
-// slot of the wave's run of 1 KB is), 8-bit codes are widened on the way.
+// slot of the wave's run of 1 KB is), 8-bit codes are widened on the way, 4-bit
+// ones become f16 values (K in the order of q4_cols, which queries take too).
 template <int TYPE, int HD>
 struct Stage {
+    static constexpr bool REGS = TYPE == kKvI8 || TYPE == kKvQ4;
     static constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
-    static constexpr int PIECES = HD * SZ;  // 16-byte pieces of 16 K rows, and of a V block
+    static constexpr int PIECES = TYPE == kKvQ4 ? HD / 2 : HD * SZ;  // 16-byte pieces of 16 K rows, and of a V block
     static constexpr int N = (PIECES + 63) / 64;
-    u32x4 k[TYPE == kKvI8 ? N : 1], v[TYPE == kKvI8 ? N : 1];
+    u32x4 k[REGS ? N : 1], v[REGS ? N : 1];
+    uint16_t kd[TYPE == kKvQ4 ? N : 1];
+    u32x4 vd4[TYPE == kKvQ4 ? N : 1][2];  // scales of a V piece's 16 positions
     float sc;
     bool ok;
 
@@ -67,9 +71,22 @@ struct Stage {
         ok = page >= 0;
         const uint8_t *base = kv_head(c, page < 0 ? 0 : page, h);
         const int slot = pos & ((1 << c.page_shift) - 1);
-        const uint8_t *kp = base + (int64_t)slot * (HD * SZ);
-        const uint8_t *vp = base + ((int64_t)(HD * SZ) << c.page_shift) + (int64_t)slot * (HD * SZ);
-        if constexpr (TYPE == kKvI8) {
+        constexpr int RB = TYPE == kKvQ4 ? HD / 2 : HD * SZ;  // bytes of a row
+        const uint8_t *kp = base + (int64_t)slot * RB;
+        const uint8_t *vp = base + ((int64_t)RB << c.page_shift) + (int64_t)slot * RB;
+        if constexpr (TYPE == kKvQ4) {
+            const uint8_t *sp = base + ((int64_t)HD << c.page_shift);  // scales of K, [position][block], then V's, [block][position]
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int p = lane + 64 * i;
+                if (PIECES % 64 != 0 && p >= PIECES) continue;
+                k[i] = *reinterpret_cast<const u32x4 *>(kp + p * 16);
+                v[i] = *reinterpret_cast<const u32x4 *>(vp + p * 16);
+                kd[i] = reinterpret_cast<const uint16_t *>(sp)[(int64_t)slot * (HD / 32) + p];
+                const u32x4 *vs = reinterpret_cast<const u32x4 *>(sp + ((int64_t)(HD / 16 + p / 16 * 2) << c.page_shift) + 2 * slot);
+                vd4[i][0] = vs[0], vd4[i][1] = vs[1];
+            }
+        } else if constexpr (TYPE == kKvI8) {
 #pragma unroll
             for (int i = 0; i < N; i++) {
                 if (PIECES % 64 == 0 || lane + 64 * i < PIECES) {
@@ -98,7 +115,49 @@ struct Stage {
     __device__ __forceinline__ void store(uint8_t *buf, uint8_t *flag, int w, int lane, int live, int h0, int h1, bool whole) const {
         if (!ok) live = 0;
         bool marked = false;
-        if constexpr (TYPE == kKvI8) {
+        if constexpr (TYPE == kKvQ4) {
+            uint8_t *vbase = buf + Lds<HD>::kV + w * HD * 32;
+            uint32_t any = 0;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int p = lane + 64 * i;
+                if (PIECES % 64 != 0 && p >= PIECES) continue;
+                // K: a piece is a block of a row
+                const int pos = p / (HD / 32), at = p % (HD / 32) * 4, row = 16 * w + krow(pos);
+                uint8_t *kbase = buf + row * Lds<HD>::kRow;
+                const uint32_t s = kd[i], d2 = s | s << 16;
+#pragma unroll
+                for (int j = 0; j < 4; j++) *reinterpret_cast<U128 *>(kbase + kslot<HD>(row, at + j) * 16) = q4_row8(k[i][j], d2);
+                // V: a piece is 16 positions of columns d and d + 16
+                const int d = p / 16 * 32 + p % 16;
+#pragma unroll
+                for (int half = 0; half < 2; half++) {
+                    u32x4 sc4 = vd4[i][half];
+                    if (!whole || !ok) {
+                        uint32_t bits = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const uint32_t bad = not_finite<OpF16>(sc4[j]);
+                            sc4[j] &= ~(bad * 0xFFFFu);
+                            bits |= ((bad & 1) | (bad >> 15)) << (2 * j);
+                        }
+                        uint8_t *marks = buf + Lds<HD>::kMarks + (w * HD + d) * 2 + half;
+                        marks[0] = marks[32] = (uint8_t)bits;
+                        any |= bits;
+                    }
+                    U128 x, y;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const uint32_t codes = v[i][2 * half + j / 2], c = q4_addend(sc4[j]);
+                        x.w[j] = j % 2 == 0 ? q4_pair<0>(codes, sc4[j], c) : q4_pair<2>(codes, sc4[j], c);
+                        y.w[j] = j % 2 == 0 ? q4_pair<1>(codes, sc4[j], c) : q4_pair<3>(codes, sc4[j], c);
+                    }
+                    *reinterpret_cast<U128 *>(vbase + vslot(d, half) * 16) = x;
+                    *reinterpret_cast<U128 *>(vbase + vslot(d + 16, half) * 16) = y;
+                }
+            }
+            marked = __any(any != 0);
+        } else if constexpr (TYPE == kKvI8) {
 #pragma unroll
             for (int i = 0; i < N; i++) {
                 const int p = lane + 64 * i;
@@ -216,13 +275,17 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
     const bool live = rr < nrows && row >= 0 && row < a.rows;
     float f[KS][8];
     {
-        const float *qp = a.q + (live ? row : 0) * a.ldq + (int64_t)(h * a.group + (live ? hg : 0)) * HD + 8 * hh;
+        const float *qp = a.q + (live ? row : 0) * a.ldq + (int64_t)(h * a.group + (live ? hg : 0)) * HD + (TYPE == kKvQ4 ? 0 : 8 * hh);
 #pragma unroll
         for (int t = 0; t < KS; t++) {
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
-            const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
-            f[t][0] = x.x, f[t][1] = x.y, f[t][2] = x.z, f[t][3] = x.w;
-            f[t][4] = y.x, f[t][5] = y.y, f[t][6] = y.z, f[t][7] = y.w;
+            if constexpr (TYPE == kKvQ4) {
+                q4_cols(qp, 2 * t + hh, f[t]);
+            } else {
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(qp + 16 * t);
+                const float4 x = __builtin_bit_cast(float4, load16(src)), y = __builtin_bit_cast(float4, load16(src + 16));
+                f[t][0] = x.x, f[t][1] = x.y, f[t][2] = x.z, f[t][3] = x.w;
+                f[t][4] = y.x, f[t][5] = y.y, f[t][6] = y.z, f[t][7] = y.w;
+            }
         }
     }
     const int len = kv_len(c, s, a.limit);
@@ -535,6 +598,7 @@ hipError_t launch_attn_prefill(int type, const AttnArgs &a, const AttnPlan &p, h
     case kKvF16: return launch_type<kKvF16>(a, slots, s);
     case kKvBF16: return launch_type<kKvBF16>(a, slots, s);
     case kKvI8: return launch_type<kKvI8>(a, slots, s);
+    case kKvQ4: return launch_type<kKvQ4>(a, slots, s);
     default: return hipErrorInvalidValue;
     }
 }

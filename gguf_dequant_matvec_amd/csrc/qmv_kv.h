@@ -7,19 +7,26 @@
 
 namespace qmv {
 
-enum { kKvF16 = 1, kKvI8 = 24, kKvBF16 = 30 };
+enum { kKvF16 = 1, kKvI8 = 24, kKvBF16 = 30, kKvQ4 = 104 };
 
-inline bool kv_type_ok(int t) { return t == kKvF16 || t == kKvBF16 || t == kKvI8; }
+inline bool kv_type_ok(int t) { return t == kKvF16 || t == kKvBF16 || t == kKvI8 || t == kKvQ4; }
 inline bool kv_head_dim_ok(int hd) { return hd == 64 || hd == 96 || hd == 128 || hd == 256; }
 
 inline bool kv_page_size_ok(int p) { return p >= 16 && p <= 4096 && (p & (p - 1)) == 0; }
 
 constexpr int kVBlock = 16;  // positions of one V block
 
-// Bytes of one head's part of a page: K rows, V blocks, 8-bit row scales.
+// Bytes of one head's part of a page: K rows, V blocks, 8-bit row scales or
+// 4-bit block scales.
 __host__ __device__ inline int64_t kv_head_bytes(int type, int hd, int page_size) {
-    return type == kKvI8 ? 2ll * page_size * hd + 8ll * page_size : 4ll * page_size * hd;
+    return type == kKvI8   ? 2ll * page_size * hd + 8ll * page_size
+           : type == kKvQ4 ? (int64_t)page_size * hd / 8 * 9
+                           : 4ll * page_size * hd;
 }
+
+// Place of position p in a V block of a 4-bit cache: 0, 2, 1, 3 in each four (so
+// that the two halves of a masked dword are neighbouring positions); both ways.
+__host__ __device__ constexpr int kv_place4(int p) { return (p & ~3) | ((p & 1) << 1) | ((p >> 1) & 1); }
 
 // A cache as the kernels take it.
 struct KvArgs {
@@ -55,6 +62,9 @@ __device__ __forceinline__ uint8_t *kv_head(const KvArgs &c, int page, int h) {
 hipError_t launch_kv_append(int type, const KvArgs &c, int64_t n, const int32_t *start,
                             const float *k, int64_t ldk, const float *v, int64_t ldv,
                             hipStream_t s);
+
+hipError_t launch_kv_read(int type, const KvArgs &c, int64_t n, const int32_t *start, float *k,
+                          int64_t ldk, float *v, int64_t ldv, hipStream_t s);
 
 struct EvictArgs {
     const int32_t *dst;

@@ -3,6 +3,7 @@
 #include "qmv_device.h"
 #include "qmv_internal.h"
 #include "qmv_kv.h"
+#include "qmv_rope.h"
 
 #include <type_traits>
 
@@ -35,71 +36,144 @@ __device__ __forceinline__ int kv_code(float x, float d) {
     return (int)fminf(fmaxf(r, -127.f), 127.f);
 }
 
-template <int TYPE, int HD, int ROWS>
-__global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int32_t *start,
+// 4-bit blocks of 32 values: d is an eighth of the value of largest size (the
+// positive one of two), of the other sign, so that this value has the code -8.
+// It is rounded to eight bits of significand, then to f16: products of such a
+// scale and a code are f16 values, and so is 24 d for d of at most 2720, which
+// the readers use.
+__device__ __forceinline__ uint32_t kv_scale4(float hi, float lo, bool nan) {
+    if (nan) return 0x7E00;
+    const float v = (float)(__bf16)((hi >= -lo ? hi : lo) * -0.125f);
+    return __builtin_bit_cast(uint16_t, (_Float16)fminf(fmaxf(v, -2720.f), 2720.f));
+}
+__device__ __forceinline__ uint32_t kv_code4(float x, float d) {  // 0 .. 15
+    const float r = d != 0.f ? rintf(x / d) : 0.f;
+    return (uint32_t)(int)(fminf(fmaxf(r, -8.f), 7.f) + 8.f);
+}
+
+// Where row r goes: its sequence's position (-1: none), page (-1: nowhere) and slot.
+struct Place {
+    int pos, page, slot;
+};
+__device__ __forceinline__ Place kv_place(const KvArgs &c, int64_t r, int64_t n, const int32_t *start) {
+    Place at{-1, -1, 0};
+    if (r >= n) return at;
+    int seq = 0;
+    int64_t first = 0, next = 0;
+    if (start) {  // the last sequence that starts at or before r
+        int lo = 0, hi = c.n_seq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= r) lo = mid; else hi = mid;
+        }
+        seq = lo;
+        first = start[seq];
+        next = start[seq + 1];
+    } else {
+        const int64_t each = n / c.n_seq;
+        seq = (int)(r / each);
+        first = (int64_t)seq * each;
+        next = first + each;
+    }
+    const int64_t pos = (int64_t)c.seq_len[seq] - (next - r);
+    if (r >= first && r < next && pos >= 0 && pos < c.cap) {
+        at.pos = (int)pos;
+        at.page = kv_page(c, seq, (int)pos);
+        at.slot = (int)pos & ((1 << c.page_shift) - 1);
+    }
+    return at;
+}
+
+__device__ __forceinline__ void load_cols8(const float *p, float *f) {
+    const float4 a = __builtin_bit_cast(float4, load16(reinterpret_cast<const uint8_t *>(p)));
+    const float4 b = __builtin_bit_cast(float4, load16(reinterpret_cast<const uint8_t *>(p + 4)));
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// With ROPE the K rows are normed and turned on the way, and workgroups past
+// the key-value heads do the same to HB heads of the rows' queries.  A K row
+// then goes through LDS, because its pairs are half a row apart and the cache
+// wants eight neighbours.
+template <int TYPE, int HD, int ROWS, int ROPE>
+__global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRows q, int64_t n, const int32_t *start,
                                                  const float *__restrict__ k, int64_t ldk,
                                                  const float *__restrict__ v, int64_t ldv) {
-    constexpr int SZ = TYPE == kKvI8 ? 1 : 2;
+    constexpr int SZ = TYPE == kKvF16 || TYPE == kKvBF16 ? 2 : 1;
+    constexpr int VC = TYPE == kKvQ4 ? HD / 2 : HD;        // columns of a V block: a byte has two 4-bit codes
     constexpr int PIECES = HD / 8;                         // 8 columns a thread
     constexpr int N = (ROWS * PIECES + 255) / 256;         // pieces a thread
-    constexpr int VROW = HD + (TYPE == kKvI8 ? 4 : 2);     // padded row in LDS, values
-    typedef typename std::conditional<TYPE == kKvI8, int8_t, uint16_t>::type Val;
+    constexpr int VROW = VC + (SZ == 1 ? 4 : 2);           // padded row in LDS, values
+    constexpr int L = kRopeLanes<HD>, RN = (ROWS * L + 255) / 256;
+    constexpr int KROW = HD + 4;
+    constexpr int NB = HD / 32;                            // 4-bit blocks of a row
+    typedef typename std::conditional<SZ == 1, uint8_t, uint16_t>::type Val;
     __shared__ int s_page[ROWS], s_slot[ROWS];
     __shared__ bool s_run[ROWS];  // the row's aligned group of 8 positions is here, row by row
     __shared__ __align__(16) Val s_v[ROWS * VROW];
     __shared__ float s_d[2][ROWS];
     __shared__ float s_part[TYPE == kKvI8 ? 2 : 1][TYPE == kKvI8 ? ROWS * PIECES : 1];
+    __shared__ uint16_t s_d4[2][TYPE == kKvQ4 ? NB * ROWS : 1];
+    __shared__ int s_pos[ROPE ? ROWS : 1];
+    __shared__ __align__(16) float s_k[ROPE ? ROWS * KROW : 1];
     const int tid = threadIdx.x, h = blockIdx.y;
     const int64_t row0 = (int64_t)blockIdx.x * ROWS;
     const int rows = n - row0 < ROWS ? (int)(n - row0) : ROWS;
 
+    if constexpr (ROPE > 0) {
+        if (h >= c.n_kv) {
+            if (tid < ROWS) s_pos[tid] = kv_place(c, row0 + tid, n, start).pos;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < RN; i++) {
+                const int e = tid + 256 * i, r = e / L;
+                if (r < ROWS && s_pos[r] >= 0) rope_heads<HD, ROPE>(rope, q, rope.q_norm, row0 + r, s_pos[r], e % L, (h - c.n_kv) * ROPE);
+            }
+            return;
+        }
+    }
     float kf[N][8], vf[N][8];
+    Cols8 kx[ROPE ? RN : 1];
+    if constexpr (ROPE > 0) {
+#pragma unroll
+        for (int i = 0; i < RN; i++) {
+            const int e = tid + 256 * i, r = e / L;
+            kx[i] = rope_load(k + (row0 + (r < rows ? r : 0)) * ldk + (int64_t)h * HD, rope_lane<HD>(rope, e % L));
+        }
+    }
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const int e = tid + 256 * i, r = e / PIECES, p = e % PIECES;
         if (r < rows) {
-            const uint8_t *ks = reinterpret_cast<const uint8_t *>(k + (row0 + r) * ldk + (int64_t)h * HD + p * 8);
-            const uint8_t *vs = reinterpret_cast<const uint8_t *>(v + (row0 + r) * ldv + (int64_t)h * HD + p * 8);
-            const float4 a = __builtin_bit_cast(float4, load16(ks)), b = __builtin_bit_cast(float4, load16(ks + 16));
-            const float4 x = __builtin_bit_cast(float4, load16(vs)), y = __builtin_bit_cast(float4, load16(vs + 16));
-            kf[i][0] = a.x, kf[i][1] = a.y, kf[i][2] = a.z, kf[i][3] = a.w;
-            kf[i][4] = b.x, kf[i][5] = b.y, kf[i][6] = b.z, kf[i][7] = b.w;
-            vf[i][0] = x.x, vf[i][1] = x.y, vf[i][2] = x.z, vf[i][3] = x.w;
-            vf[i][4] = y.x, vf[i][5] = y.y, vf[i][6] = y.z, vf[i][7] = y.w;
+            if constexpr (ROPE == 0) load_cols8(k + (row0 + r) * ldk + (int64_t)h * HD + p * 8, kf[i]);
+            load_cols8(v + (row0 + r) * ldv + (int64_t)h * HD + p * 8, vf[i]);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; j++) kf[i][j] = vf[i][j] = 0.f;
         }
     }
     if (tid < ROWS) {
-        const int64_t r = row0 + tid;
-        int page = -1, slot = 0;
-        if (r < n) {
-            int seq = 0;
-            int64_t first = 0, next = 0;
-            if (start) {  // the last sequence that starts at or before r
-                int lo = 0, hi = c.n_seq;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (start[mid] <= r) lo = mid; else hi = mid;
-                }
-                seq = lo;
-                first = start[seq];
-                next = start[seq + 1];
-            } else {
-                const int64_t each = n / c.n_seq;
-                seq = (int)(r / each);
-                first = (int64_t)seq * each;
-                next = first + each;
-            }
-            const int64_t pos = (int64_t)c.seq_len[seq] - (next - r);
-            if (r >= first && r < next && pos >= 0 && pos < c.cap) {
-                page = kv_page(c, seq, (int)pos);
-                slot = (int)pos & ((1 << c.page_shift) - 1);
-            }
+        const Place at = kv_place(c, row0 + tid, n, start);
+        s_page[tid] = at.page;
+        s_slot[tid] = at.slot;
+        if constexpr (ROPE > 0) s_pos[tid] = at.pos;
+    }
+    if constexpr (ROPE > 0) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RN; i++) {
+            const int e = tid + 256 * i, r = e / L, p = e % L;
+            if (r >= ROWS) continue;
+            const RopeLane l = rope_lane<HD>(rope, p);
+            const Cols8 y = rope_apply<HD>(rope, l, rope_turn(rope, l, p, s_pos[r]), kx[i], rope.k_norm);
+            if (l.live) rope_store(s_k + r * KROW, l, y);
         }
-        s_page[tid] = page;
-        s_slot[tid] = slot;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int e = tid + 256 * i, r = e / PIECES, p = e % PIECES;
+            if (r < ROWS) load_cols8(s_k + r * KROW + p * 8, kf[i]);
+        }
     }
     if constexpr (TYPE == kKvI8) {
         // row maxima; a NaN anywhere makes the maximum NaN
@@ -144,25 +218,56 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int3
         if (r >= ROWS) continue;
         const int page = s_page[r];
         uint32_t w[4] = {0, 0, 0, 0}, x[4] = {0, 0, 0, 0};
+        if constexpr (TYPE == kKvQ4) {
+            // a block is four neighbouring lanes' (PIECES is a multiple of 4), the
+            // upper two's codes the high halves of the lower two's bytes
+            auto block = [&](const float *f, uint32_t *code, int which) {
+                float hi = f[0], lo = f[0];
+                int nan = f[0] != f[0];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            if constexpr (TYPE == kKvI8) {
-                w[j >> 2] |= (uint32_t)(kv_code(kf[i][j], s_d[0][r]) & 0xFF) << (8 * (j & 3));
-                x[j >> 2] |= (uint32_t)(kv_code(vf[i][j], s_d[1][r]) & 0xFF) << (8 * (j & 3));
-            } else {
-                w[j >> 1] |= kv_round<TYPE>(kf[i][j]) << (16 * (j & 1));
-                x[j >> 1] |= kv_round<TYPE>(vf[i][j]) << (16 * (j & 1));
+                for (int j = 1; j < 8; j++) hi = fmaxf(hi, f[j]), lo = fminf(lo, f[j]), nan |= f[j] != f[j];
+#pragma unroll
+                for (int off = 1; off < 4; off <<= 1) {
+                    hi = fmaxf(hi, __shfl_xor(hi, off)), lo = fminf(lo, __shfl_xor(lo, off));
+                    nan |= __shfl_xor(nan, off);
+                }
+                const uint32_t d = kv_scale4(hi, lo, nan != 0);
+                const float df = half_bits_to_float(d);
+#pragma unroll
+                for (int j = 0; j < 8; j++) code[j >> 2] |= kv_code4(f[j], df) << (8 * (j & 3));
+#pragma unroll
+                for (int j = 0; j < 2; j++) code[j] |= (uint32_t)__shfl_xor((int)code[j], 2) << 4;
+                if (p % 4 == 0) s_d4[which][(p / 4) * ROWS + r] = (uint16_t)d;
+            };
+            block(kf[i], w, 0);
+            block(vf[i], x, 1);
+            if (p % 4 >= 2) continue;
+            const int byte = p / 4 * 16 + p % 4 * 8;
+            uint32_t *sv = reinterpret_cast<uint32_t *>(s_v + r * VROW + byte);
+            sv[0] = x[0], sv[1] = x[1];
+            if (page < 0) continue;
+            *reinterpret_cast<uint2 *>(kv_head(c, page, h) + (int64_t)s_slot[r] * VC + byte) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if constexpr (TYPE == kKvI8) {
+                    w[j >> 2] |= (uint32_t)(kv_code(kf[i][j], s_d[0][r]) & 0xFF) << (8 * (j & 3));
+                    x[j >> 2] |= (uint32_t)(kv_code(vf[i][j], s_d[1][r]) & 0xFF) << (8 * (j & 3));
+                } else {
+                    w[j >> 1] |= kv_round<TYPE>(kf[i][j]) << (16 * (j & 1));
+                    x[j >> 1] |= kv_round<TYPE>(vf[i][j]) << (16 * (j & 1));
+                }
             }
-        }
-        uint32_t *sv = reinterpret_cast<uint32_t *>(s_v + r * VROW + p * 8);
+            uint32_t *sv = reinterpret_cast<uint32_t *>(s_v + r * VROW + p * 8);
 #pragma unroll
-        for (int j = 0; j < 2 * SZ; j++) sv[j] = x[j];
-        if (page < 0) continue;
-        uint8_t *dst = kv_head(c, page, h) + ((int64_t)s_slot[r] * HD + p * 8) * SZ;
-        if constexpr (TYPE == kKvI8)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 2 * SZ; j++) sv[j] = x[j];
+            if (page < 0) continue;
+            uint8_t *dst = kv_head(c, page, h) + ((int64_t)s_slot[r] * HD + p * 8) * SZ;
+            if constexpr (TYPE == kKvI8)
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
     if (tid < ROWS) {
         const int r8 = tid - (s_slot[tid] & 7);
@@ -179,27 +284,113 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, int64_t n, const int3
         }
     }
     __syncthreads();
+    if constexpr (TYPE == kKvQ4) {
+        for (int e = tid; e < 2 * NB * ROWS; e += 256) {
+            const int r = e % ROWS, b = e / ROWS % NB, which = e / (ROWS * NB);
+            if (s_page[r] < 0) continue;
+            uint16_t *sc = reinterpret_cast<uint16_t *>(kv_head(c, s_page[r], h) + page_size * HD);
+            const int64_t at = which ? (page_size * NB + b * page_size + s_slot[r]) : ((int64_t)s_slot[r] * NB + b);
+            sc[at] = s_d4[which][b * ROWS + r];
+        }
+    }
     // V: lanes run over columns; a whole group leaves with its first row
-    for (int e = tid; e < ROWS * HD; e += 256) {
-        const int r = e / HD, d = e % HD;
+    for (int e = tid; e < ROWS * VC; e += 256) {
+        const int r = e / VC, d = e % VC;
         const int page = s_page[r], slot = s_slot[r];
         if (page < 0) continue;
-        uint8_t *dst = kv_head(c, page, h) + page_size * HD * SZ +
-                       ((int64_t)(slot / kVBlock) * (HD * kVBlock) + d * kVBlock + slot % kVBlock) * SZ;
+        const int in16 = TYPE == kKvQ4 ? kv_place4(slot % kVBlock) : slot % kVBlock;
+        uint8_t *dst = kv_head(c, page, h) + page_size * VC * SZ +
+                       ((int64_t)(slot / kVBlock) * (VC * kVBlock) + d * kVBlock + in16) * SZ;
         if (!s_run[r]) {
             *reinterpret_cast<Val *>(dst) = s_v[r * VROW + d];
         } else if ((slot & 7) == 0) {
             uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const uint32_t b = TYPE == kKvI8 ? (uint8_t)s_v[(r + j) * VROW + d] : (uint16_t)s_v[(r + j) * VROW + d];
+                const uint32_t b = s_v[(r + (TYPE == kKvQ4 ? kv_place4(j) : j)) * VROW + d];
                 w[j / (4 / SZ)] |= b << (8 * SZ * (j % (4 / SZ)));
             }
-            if constexpr (TYPE == kKvI8)
+            if constexpr (SZ == 1)
                 *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
             else
                 *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+    }
+}
+
+// ---- reading back ---------------------------------------------------------------
+// A workgroup takes 16 consecutive rows of one key-value head.  K comes as it
+// goes out.  V's lanes run over the rows first (16 positions of a column are
+// neighbours in a block) and go through LDS.
+constexpr int kReadRows = 16;
+
+template <int TYPE>
+__device__ __forceinline__ float kv_value(const uint8_t *p, int64_t i) {
+    if constexpr (TYPE == kKvF16) return (float)reinterpret_cast<const _Float16 *>(p)[i];
+    if constexpr (TYPE == kKvBF16) return (float)reinterpret_cast<const __bf16 *>(p)[i];
+    return (float)reinterpret_cast<const int8_t *>(p)[i];
+}
+
+template <int TYPE, int HD>
+__global__ __launch_bounds__(256) void kv_read(KvArgs c, int64_t n, const int32_t *start, float *__restrict__ k,
+                                               int64_t ldk, float *__restrict__ v, int64_t ldv) {
+    constexpr int SZ = TYPE == kKvF16 || TYPE == kKvBF16 ? 2 : 1;
+    constexpr int VC = TYPE == kKvQ4 ? HD / 2 : HD, NB = HD / 32;
+    __shared__ int s_pos[kReadRows], s_page[kReadRows], s_slot[kReadRows];
+    __shared__ float s_v[kReadRows][HD + 1];
+    const int tid = threadIdx.x, h = blockIdx.y;
+    const int64_t row0 = (int64_t)blockIdx.x * kReadRows, page_size = 1ll << c.page_shift;
+    if (tid < kReadRows) {
+        const Place at = kv_place(c, row0 + tid, n, start);
+        s_pos[tid] = at.pos, s_page[tid] = at.page, s_slot[tid] = at.slot;
+    }
+    __syncthreads();
+    for (int e = tid; e < kReadRows * VC; e += 256) {
+        const int r = e % kReadRows, d = e / kReadRows, page = s_page[r], slot = s_slot[r];
+        const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h), *codes = head + page_size * VC * SZ;
+        const int64_t block = (int64_t)(slot / kVBlock) * (VC * kVBlock) + d * kVBlock;
+        if constexpr (TYPE == kKvQ4) {
+            const int b = d / 16, col = 32 * b + d % 16;
+            float x = 0.f, y = 0.f;
+            if (page >= 0) {
+                const uint32_t byte = codes[block + kv_place4(slot % kVBlock)];
+                const uint16_t *sc = reinterpret_cast<const uint16_t *>(head + page_size * HD);
+                const float f = half_bits_to_float(sc[page_size * NB + b * page_size + slot]);
+                x = f * (float)((int)(byte & 15) - 8), y = f * (float)((int)(byte >> 4) - 8);
+            }
+            s_v[r][col] = x, s_v[r][col + 16] = y;
+        } else {
+            float x = 0.f;
+            if (page >= 0) {
+                x = kv_value<TYPE>(codes, block + slot % kVBlock);
+                if constexpr (TYPE == kKvI8)
+                    x *= reinterpret_cast<const float *>(head + 2 * page_size * HD)[page_size + slot];
+            }
+            s_v[r][d] = x;
+        }
+    }
+    for (int e = tid; e < kReadRows * HD; e += 256) {
+        const int r = e / HD, d = e % HD, page = s_page[r], slot = s_slot[r];
+        if (s_pos[r] < 0) continue;
+        const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
+        float x = 0.f;
+        if (page >= 0) {
+            if constexpr (TYPE == kKvQ4) {
+                const int b = d / 32;
+                const uint32_t byte = head[(int64_t)slot * VC + 16 * b + d % 16];
+                x = half_bits_to_float(reinterpret_cast<const uint16_t *>(head + page_size * HD)[(int64_t)slot * NB + b]) *
+                    (float)((int)(byte >> (d % 32 / 16 * 4) & 15) - 8);
+            } else {
+                x = kv_value<TYPE>(head, (int64_t)slot * HD + d);
+                if constexpr (TYPE == kKvI8) x *= reinterpret_cast<const float *>(head + 2 * page_size * HD)[slot];
+            }
+        }
+        k[(row0 + r) * ldk + (int64_t)h * HD + d] = x;
+    }
+    __syncthreads();
+    for (int e = tid; e < kReadRows * HD; e += 256) {
+        const int r = e / HD, d = e % HD;
+        if (s_pos[r] >= 0) v[(row0 + r) * ldv + (int64_t)h * HD + d] = s_v[r][d];
     }
 }
 
@@ -386,8 +577,12 @@ __global__ __launch_bounds__(kSelThreads) void kv_evict_select(KvArgs c, EvictAr
 // TB/s; a plain copy runs at 4.98).
 constexpr int kMove = 64;
 
-template <int SZ, int HD>
+// KIND: 2 for 16-bit values, 1 for 8-bit codes, 0 for 4-bit ones, two columns a
+// byte and the positions of a block in kv_place4's order.
+template <int KIND, int HEAD_DIM>
 __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
+    constexpr int SZ = KIND == 2 ? 2 : 1;
+    constexpr int HD = KIND == 0 ? HEAD_DIM / 2 : HEAD_DIM;  // values (bytes) of a row
     constexpr int ROW = HD * SZ;                         // bytes of a K row
     constexpr int KP = kMove * ROW / 16;                 // 16-byte pieces of the K rows
     constexpr int KN = (KP + 255) / 256;
@@ -453,6 +648,7 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
     }
     const int blocks = s_blocks;
     uint4 vw[GROUP][VN];
+    auto place = [](int i) { return KIND == 0 ? kv_place4(i) : i; };
     auto load_group = [&](int g0) {
 #pragma unroll
         for (int k = 0; k < GROUP; k++) {
@@ -504,10 +700,10 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
             if (u >= OUT) continue;
 #pragma unroll
             for (int x = 0; x < PER; x++) {
-                const int k = s_ord[i + x] - g0;
-                if (i + x < cnt && k >= 0 && k < GROUP) {
+                const int to = i + place(x), k = s_ord[to] - g0;
+                if (to < cnt && k >= 0 && k < GROUP) {
                     const Val *col = reinterpret_cast<const Val *>(s_v + (k * HD + d) * PAD);
-                    out[j][x * SZ / 4] |= (uint32_t)col[s_src[i + x] % kVBlock] << (8 * SZ * (x % (4 / SZ)));
+                    out[j][x * SZ / 4] |= (uint32_t)col[place(s_src[to] % kVBlock)] << (8 * SZ * (x % (4 / SZ)));
                 }
             }
         }
@@ -524,10 +720,24 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
         } else {  // positions past the new length stay as they were
 #pragma unroll
             for (int x = 0; x < PER; x++)
-                if (i + x < cnt) reinterpret_cast<Val *>(dst)[x] = (Val)(out[j][x * SZ / 4] >> (8 * SZ * (x % (4 / SZ))));
+                if (i + place(x) < cnt) reinterpret_cast<Val *>(dst)[x] = (Val)(out[j][x * SZ / 4] >> (8 * SZ * (x % (4 / SZ))));
         }
     }
-    if (SZ == 1 && tid < 2 * kMove) {
+    if constexpr (KIND == 0) {
+        constexpr int NB = HEAD_DIM / 32;
+        for (int j = tid; j < 2 * NB * kMove; j += 256) {
+            const int i = j % kMove, b = j / kMove % NB, which = j / (kMove * NB);
+            if (i >= cnt || s_dst[i / kVBlock] < 0) continue;
+            auto at = [&](int page, int slot) {
+                uint16_t *sc = reinterpret_cast<uint16_t *>(kv_head(c, page, h) + page_size * HEAD_DIM);
+                return sc + (which ? page_size * NB + b * page_size + slot : (int64_t)slot * NB + b);
+            };
+            uint16_t d = 0;
+            if (s_page[i] >= 0) d = *at(s_page[i], s_src[i] & pmask);
+            *at(s_dst[i / kVBlock], (i0 + i) & pmask) = d;
+        }
+    }
+    if (KIND == 1 && tid < 2 * kMove) {
         const int i = tid % kMove, which = tid / kMove;
         if (i < cnt && s_dst[i / kVBlock] >= 0) {
             float f = 0.f;
@@ -538,29 +748,70 @@ __global__ __launch_bounds__(256) void kv_evict_move(KvArgs c, EvictArgs e) {
     }
 }
 
-template <int HD, int ROWS>
-hipError_t append_rows(int type, const KvArgs &c, int64_t n, const int32_t *start, const float *k,
-                       int64_t ldk, const float *v, int64_t ldv, hipStream_t s) {
-    const dim3 grid((uint32_t)((n + ROWS - 1) / ROWS), c.n_kv);
-    if (type == kKvF16)
-        return launch_main(kv_append<kKvF16, HD, ROWS>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
-    if (type == kKvBF16)
-        return launch_main(kv_append<kKvBF16, HD, ROWS>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
-    return launch_main(kv_append<kKvI8, HD, ROWS>, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv);
+struct AppendCall {
+    int type;
+    const KvArgs &c;
+    const RopeArgs &rope;
+    const HeadRows &q;
+    int64_t n;
+    const int32_t *start;
+    const float *k;
+    int64_t ldk;
+    const float *v;
+    int64_t ldv;
+    hipStream_t s;
+};
+
+template <int HD, int ROWS, int ROPE>
+hipError_t append_rows(const AppendCall &a) {
+    const dim3 grid((uint32_t)((a.n + ROWS - 1) / ROWS), a.c.n_kv + (ROPE ? (a.q.heads + ROPE - 1) / (ROPE ? ROPE : 1) : 0));
+    auto launch = [&](auto kernel) {
+        return launch_main(kernel, grid, dim3(256), 0, a.s, a.c, a.rope, a.q, a.n, a.start, a.k, a.ldk, a.v, a.ldv);
+    };
+    switch (a.type) {
+    case kKvF16: return launch(kv_append<kKvF16, HD, ROWS, ROPE>);
+    case kKvBF16: return launch(kv_append<kKvBF16, HD, ROWS, ROPE>);
+    case kKvQ4: return launch(kv_append<kKvQ4, HD, ROWS, ROPE>);
+    default: return launch(kv_append<kKvI8, HD, ROWS, ROPE>);
+    }
 }
 
 template <int HD>
-hipError_t append_hd(int type, const KvArgs &c, int64_t n, const int32_t *start, const float *k,
-                     int64_t ldk, const float *v, int64_t ldv, hipStream_t s) {
+hipError_t append_hd(const AppendCall &a, bool rope) {
     // 32 rows once that still gives two workgroups per compute unit (6808 rows
     // of 8 heads of 128: 20.8 us, with 16 rows 23.5, with 64 rows 23.6)
-    if (n * c.n_kv >= 32 * 512) return append_rows<HD, 32>(type, c, n, start, k, ldk, v, ldv, s);
-    return append_rows<HD, 16>(type, c, n, start, k, ldk, v, ldv, s);
+    const bool many = a.n * a.c.n_kv >= 32 * 512;
+    if (rope) return many ? append_rows<HD, 32, 4>(a) : append_rows<HD, 16, 1>(a);
+    return many ? append_rows<HD, 32, 0>(a) : append_rows<HD, 16, 0>(a);
+}
+
+hipError_t append_call(const AppendCall &a, bool rope) {
+    switch (a.c.hd) {
+    case 64: return append_hd<64>(a, rope);
+    case 96: return append_hd<96>(a, rope);
+    case 128: return append_hd<128>(a, rope);
+    case 256: return append_hd<256>(a, rope);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+template <int HD>
+hipError_t read_hd(int type, const KvArgs &c, int64_t n, const int32_t *start, float *k, int64_t ldk, float *v,
+                   int64_t ldv, hipStream_t s) {
+    const dim3 grid((uint32_t)((n + kReadRows - 1) / kReadRows), c.n_kv);
+    auto launch = [&](auto kernel) { return launch_main(kernel, grid, dim3(256), 0, s, c, n, start, k, ldk, v, ldv); };
+    switch (type) {
+    case kKvF16: return launch(kv_read<kKvF16, HD>);
+    case kKvBF16: return launch(kv_read<kKvBF16, HD>);
+    case kKvQ4: return launch(kv_read<kKvQ4, HD>);
+    default: return launch(kv_read<kKvI8, HD>);
+    }
 }
 
 template <int HD>
 hipError_t move_hd(int type, const KvArgs &c, const EvictArgs &e, hipStream_t s) {
     const dim3 grid((e.keep + kMove - 1) / kMove, c.n_kv, c.n_seq);
+    if (type == kKvQ4) return launch_main(kv_evict_move<0, HD>, grid, dim3(256), 0, s, c, e);
     if (type == kKvI8) return launch_main(kv_evict_move<1, HD>, grid, dim3(256), 0, s, c, e);
     return launch_main(kv_evict_move<2, HD>, grid, dim3(256), 0, s, c, e);
 }
@@ -570,11 +821,22 @@ hipError_t move_hd(int type, const KvArgs &c, const EvictArgs &e, hipStream_t s)
 hipError_t launch_kv_append(int type, const KvArgs &c, int64_t n, const int32_t *start,
                             const float *k, int64_t ldk, const float *v, int64_t ldv,
                             hipStream_t s) {
+    return append_call({type, c, RopeArgs{}, HeadRows{}, n, start, k, ldk, v, ldv, s}, false);
+}
+
+hipError_t launch_kv_append_rope(int type, const KvArgs &c, const RopeArgs &r, int64_t n, const int32_t *start,
+                                 const HeadRows &q, const float *k, int64_t ldk, const float *v, int64_t ldv,
+                                 hipStream_t s) {
+    return append_call({type, c, r, q, n, start, k, ldk, v, ldv, s}, true);
+}
+
+hipError_t launch_kv_read(int type, const KvArgs &c, int64_t n, const int32_t *start, float *k, int64_t ldk, float *v,
+                          int64_t ldv, hipStream_t s) {
     switch (c.hd) {
-    case 64: return append_hd<64>(type, c, n, start, k, ldk, v, ldv, s);
-    case 96: return append_hd<96>(type, c, n, start, k, ldk, v, ldv, s);
-    case 128: return append_hd<128>(type, c, n, start, k, ldk, v, ldv, s);
-    case 256: return append_hd<256>(type, c, n, start, k, ldk, v, ldv, s);
+    case 64: return read_hd<64>(type, c, n, start, k, ldk, v, ldv, s);
+    case 96: return read_hd<96>(type, c, n, start, k, ldk, v, ldv, s);
+    case 128: return read_hd<128>(type, c, n, start, k, ldk, v, ldv, s);
+    case 256: return read_hd<256>(type, c, n, start, k, ldk, v, ldv, s);
     default: return hipErrorInvalidValue;
     }
 }

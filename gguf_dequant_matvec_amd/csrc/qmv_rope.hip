@@ -1,0 +1,63 @@
+// Norms of queries and keys for each head and the rotation of the position, on
+// plain rows.
+#include "qmv_internal.h"
+#include "qmv_rope.h"
+
+namespace qmv {
+
+namespace {
+
+// A lane group takes HB heads of one row: their angles are the same, so cosines
+// and sines are found once for HB.  The first chunks of heads are Q's, the
+// others K's.  Bound by memory, every value read and written once, or for few
+// rows by latency.
+// (16 rows at least: the most rows a call may have, in workgroups of eight, would
+// be more threads than a launch takes.)
+template <int HD>
+constexpr int kRopeRows = HD == 64 ? 32 : 16;
+
+template <int HD, int HB>
+__global__ __launch_bounds__(256) void qk_norm_rope(RopeArgs a, int64_t n, const int32_t *pos, HeadRows q, HeadRows k) {
+    constexpr int L = kRopeLanes<HD>, R = 256 / L;
+    const int p = threadIdx.x % L, q_chunks = (q.heads + HB - 1) / HB, chunk = blockIdx.y;
+#pragma unroll
+    for (int i = 0; i < kRopeRows<HD>; i += R) {
+        const int64_t row = (int64_t)blockIdx.x * kRopeRows<HD> + i + threadIdx.x / L;
+        const int at = row < n ? pos[row] : -1;
+        if (at < 0) continue;
+        if (chunk < q_chunks)
+            rope_heads<HD, HB>(a, q, a.q_norm, row, at, p, chunk * HB);
+        else
+            rope_heads<HD, HB>(a, k, a.k_norm, row, at, p, (chunk - q_chunks) * HB);
+    }
+}
+
+template <int HD, int HB>
+hipError_t launch_heads(const RopeArgs &r, int64_t n, const int32_t *pos, const HeadRows &q, const HeadRows &k,
+                        hipStream_t s) {
+    constexpr int R = kRopeRows<HD>;
+    const dim3 grid((uint32_t)((n + R - 1) / R), (q.heads + HB - 1) / HB + (k.heads + HB - 1) / HB);
+    return launch_main(qk_norm_rope<HD, HB>, grid, dim3(256), 0, s, r, n, pos, q, k);
+}
+
+template <int HD>
+hipError_t launch_hd(const RopeArgs &r, int64_t n, const int32_t *pos, const HeadRows &q, const HeadRows &k,
+                     hipStream_t s) {
+    if (n * (q.heads + k.heads) * kRopeLanes<HD> >= 4 * 256 * 1024) return launch_heads<HD, 4>(r, n, pos, q, k, s);
+    return launch_heads<HD, 1>(r, n, pos, q, k, s);
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(const RopeArgs &r, int hd, int64_t n, const int32_t *pos, const HeadRows &q,
+                               const HeadRows &k, hipStream_t s) {
+    switch (hd) {
+    case 64: return launch_hd<64>(r, n, pos, q, k, s);
+    case 96: return launch_hd<96>(r, n, pos, q, k, s);
+    case 128: return launch_hd<128>(r, n, pos, q, k, s);
+    case 256: return launch_hd<256>(r, n, pos, q, k, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace qmv

@@ -352,12 +352,27 @@ qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *
  *   QMV_KV_I8: int8 codes with one f32 scale per row (the head_dim values of
  *     one position and head): scale = max|x| / 127, code = round(x / scale)
  *     (to nearest even), 0 if the row is zero; value = scale * code.
+ *   QMV_KV_Q4: 4-bit codes with one f16 scale per block of 32 values of a row.
+ *     With v the block's value of largest size (the positive one where both
+ *     signs have it): d = -v / 8, rounded to 8 bits of significand (bf16), kept
+ *     within +-2720 and rounded to f16; code = x / d rounded to nearest even (of
+ *     the f32 quotient), within -8 .. 7, 0 if d is 0; value = d * code.  Values
+ *     beyond 7 * 2720 (8 * 2720 where d's sign is the other) and infinities
+ *     saturate; a NaN makes its block's scale, and so the block, NaN.  Scales
+ *     that a caller writes into pages have to keep the two limits (8 bits of
+ *     significand, 2720), or values are rounded.
  *
  * A page holds, for each key-value head in turn, the bytes
  *   K  [page_size][head_dim]            rows of the positions,
  *   V  [page_size / 16][head_dim][16]   blocks of 16 positions, each column's
  *                                       16 values next to each other,
  *   QMV_KV_I8 only: f32 K scale[page_size], f32 V scale[page_size];
+ * and with QMV_KV_Q4, whose bytes hold two codes (as code + 8), columns 32 b + c
+ * in the low and 32 b + c + 16 in the high half, c < 16:
+ *   K  [page_size][head_dim / 2]
+ *   V  [page_size / 16][head_dim / 2][16], each four positions in the order 0,
+ *      2, 1, 3
+ *   f16 K scale[page_size][head_dim / 32], V scale[head_dim / 32][page_size];
  * qmv_kv_page_bytes() bytes in all.  Position p of sequence s is slot
  * p % page_size of page table[s * table_ld + p / page_size].  A table entry
  * outside 0 .. n_pages - 1 is a hole: appending there writes nothing, and
@@ -379,7 +394,8 @@ qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *
 typedef enum {
     QMV_KV_F16 = 1,   /* the GGUF ids of F16, I8 and BF16 */
     QMV_KV_I8 = 24,
-    QMV_KV_BF16 = 30
+    QMV_KV_BF16 = 30,
+    QMV_KV_Q4 = 104   /* a layout of this library: no GGUF id */
 } qmv_kv_type;
 
 /* A cache.  The struct is in HOST memory and read during the call only; its
@@ -422,6 +438,97 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
                          const float *k, int64_t ldk, const float *v, int64_t ldv,
                          hipStream_t stream);
 
+/* ---- read rows back from the cache ------------------------------------------
+ * What qmv_kv_append with the same n and start would write, read instead: row r
+ * gets the f32 values that the cache holds for its position (zeros from a
+ * hole), n_kv_heads * head_dim of them at k + r * ldk and v + r * ldv.  Rows
+ * without a place in the cache are left as they were.  For a cache that is to
+ * be kept elsewhere or turned to other positions, and to see what a type's
+ * rounding leaves.  One launch. */
+qmv_status qmv_kv_read(const qmv_kv_cache *cache, int64_t n, const int32_t *start, float *k,
+                       int64_t ldk, float *v, int64_t ldv, hipStream_t stream);
+
+/* ---- norms of queries and keys, and the rotation of the position --------------
+ * BebeLM page, section "核心算子" (RMS norm; rotary positions of queries and
+ * keys before the cache).  For each row and head, x f32[head_dim]:
+ *   y = x / sqrt(mean(x^2) + eps) * norm        (norm NULL: y = x)
+ *   for i < rot_dim / 2, the pair (a, b) of columns (i, i + rot_dim / 2) with
+ *   QMV_ROPE_HALVES, (2 i, 2 i + 1) with QMV_ROPE_ADJACENT, t = pos * freq[i]:
+ *     a' = a cos t - b sin t,  b' = a sin t + b cos t
+ * and columns from rot_dim on pass as they are.  Sums and products are f32 (x^2
+ * has to stay in its range); the angle and its whole turns are taken in 64
+ * bits, so positions may be as far as 2^30. */
+typedef enum { QMV_ROPE_HALVES = 0, QMV_ROPE_ADJACENT = 1 } qmv_rope_pairs;
+
+/* The struct is in HOST memory and read during the call only; its pointers are
+ * device memory: q_norm, k_norm f32[head_dim] (4-byte aligned) or NULL, freq
+ * f64[rot_dim / 2], radians a position (8-byte aligned; any base and scaling
+ * that a model has).  rot_dim a multiple of 8 up to head_dim, 0: no rotation;
+ * eps >= 0. */
+typedef struct {
+    const double *freq;
+    int32_t rot_dim;
+    int32_t pairs;        /* qmv_rope_pairs */
+    const float *q_norm;
+    const float *k_norm;
+    float eps;
+} qmv_qk_rope;
+
+/* Rows of queries and keys (either may be left out: 0 heads) to rows: row r at
+ * q + r * ldq with n_heads * head_dim values, and so for q_out, k and k_out.
+ * pos: device int32[n]; a row at a negative position is left out (its outputs
+ * stay as they were).  q_out may be q (ldqo = ldq) and k_out k: then rows are
+ * turned in place; outputs must not overlap inputs otherwise.  head_dim 64, 96,
+ * 128 or 256; n <= QMV_MAX_KV_ROWS; n_heads, n_kv_heads <= 32767.  One launch. */
+qmv_status qmv_qk_norm_rope(const qmv_qk_rope *rope, int32_t head_dim, int64_t n, const int32_t *pos,
+                            int32_t n_heads, const float *q, int64_t ldq, float *q_out, int64_t ldqo,
+                            int32_t n_kv_heads, const float *k, int64_t ldk, float *k_out, int64_t ldko,
+                            hipStream_t stream);
+
+/* The same for new tokens of a cache: K is normed, turned to the positions that
+ * its rows take there and stored as qmv_kv_append would store it, V as it is,
+ * and Q goes to q_out (which may be q).  n, start, k and v as in qmv_kv_append;
+ * the queries of rows that have no place in the cache (positions below 0, rows
+ * of no sequence) are left out.  n_heads + n_kv_heads <= 65535.  One launch. */
+qmv_status qmv_kv_append_rope(const qmv_kv_cache *cache, const qmv_qk_rope *rope, int64_t n,
+                              const int32_t *start, int32_t n_heads, const float *q, int64_t ldq,
+                              float *q_out, int64_t ldqo, const float *k, int64_t ldk, const float *v,
+                              int64_t ldv, hipStream_t stream);
+
+/* ---- pages taken and given back on the GPU -------------------------------------
+ * A cache's free pages as a stack in device memory: free_pages int32[n_pages],
+ * the first *free_count (int32, device) of them free, taken from the end.  A page
+ * belongs to one sequence.  Both calls write the cache's table and seq_len,
+ * which the struct has as constant for the calls that read them; pages
+ * themselves are not touched.  Calls on one cache or stack follow each other on
+ * one stream.
+ *
+ * qmv_kv_reserve: sequence s wants add[s] more tokens (0 or less: none).  In
+ * order of the sequences each that can gets all of them, its seq_len grown by
+ * add[s] and the pages behind its last one entered in the table; granted[s] =
+ * add[s].  One that cannot is left as it is, granted[s] = 0: seq_len is below 0,
+ * or with add[s] past what a table row addresses (such a sequence asks for
+ * nothing below); the pages asked for up to and with it are more than there
+ * are, and it asks for some; or the tokens asked for up to and with it are more
+ * than n.  start int32[n_seq + 1]: sums of granted, the rows as qmv_kv_append,
+ * qmv_kv_append_rope and qmv_attn_prefill take them.  pos int32[n], slot
+ * int64[n], each may be NULL: the position of row r and its place in the pool,
+ * page * page_size + its slot there (-1 in a hole); -1 for both behind the last
+ * row.  n <= QMV_MAX_KV_ROWS.  One launch, a second one for the rows where n is
+ * above 4096.
+ *
+ * qmv_kv_release: sequence s is cut to new_len[s] tokens where it has more (a
+ * negative new_len leaves it as it is): seq_len becomes new_len, the table
+ * entries behind the page of its last token -1, and the pages that they named
+ * (holes none) go back on the stack, so that the first of the first sequence is
+ * on top: reserving the same again enters the same pages.  The stack holds at
+ * most n_pages; what would go beyond is lost.  One launch. */
+qmv_status qmv_kv_reserve(const qmv_kv_cache *cache, const int32_t *add, const int32_t *free_pages,
+                          int32_t *free_count, int64_t n, int32_t *granted, int32_t *start, int32_t *pos,
+                          int64_t *slot, hipStream_t stream);
+qmv_status qmv_kv_release(const qmv_kv_cache *cache, const int32_t *new_len, int32_t *free_pages,
+                          int32_t *free_count, hipStream_t stream);
+
 /* Most new tokens per sequence in one qmv_attn_decode call. */
 #define QMV_MAX_ATTN_N 16
 
@@ -445,7 +552,7 @@ qmv_status qmv_kv_append(const qmv_kv_cache *cache, int64_t n, const int32_t *st
  * query heads that share h (what qmv_kv_evict ranks by).
  * Queries and weights enter the matrix cores as sums of 16-bit pieces (f16 hi +
  * lo, 22 bits; bf16 in three, 24 bits); maximum, sum and output are f32.  f16
- * caches resolve weights down to 2^-36 of the row's largest; 8-bit ones the
+ * and 4-bit caches resolve weights down to 2^-36 of the row's largest; 8-bit ones the
  * products of weight and V row scale down to 2^-36 of the row's largest weight
  * times the largest scale that any of the sequence's new tokens sees, for V row
  * scales between 2^-100 and 2^100 (K row scales up to 2^97); bf16 ones weights
