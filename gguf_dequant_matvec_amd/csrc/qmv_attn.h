@@ -197,8 +197,12 @@ __device__ __forceinline__ uint32_t q4_addend(uint32_t d2) {
 }
 template <int PAIR>
 __device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t d2, uint32_t addend) {
+    // (the constants in registers, so that mask and exponent are one instruction)
+    uint32_t sixteen, mask;
+    asm("v_mov_b32 %0, %1" : "=v"(sixteen) : "i"(0x4C004C00));
+    asm("s_mov_b32 %0, %1" : "=s"(mask) : "i"(0x03C003C0));
     const uint32_t at6 = PAIR == 0 ? w << 6 : PAIR == 1 ? w << 2 : PAIR == 2 ? w >> 2 : w >> 6;
-    const f16x2_t u = as_f16x2((at6 & 0x03C003C0u) | 0x4C004C00u);
+    const f16x2_t u = as_f16x2((at6 & mask) | sixteen);
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(u, as_f16x2(d2), as_f16x2(addend)));
 }
 __device__ __forceinline__ U128 q4_row8(uint32_t w, uint32_t d2) {  // a dword of K

@@ -359,12 +359,17 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
         }
         const int last_page = len > 0 ? (len - 1) >> c.page_shift : 0;
         const int32_t *table = c.table + (int64_t)s * c.table_ld;
-        auto page_of = [&](int i, int grp) {  // page of a lane group's positions in chunk number i
-            if (i >= end) return -1;
+        // Page of a lane group's positions in chunk number i, by the table's entry.
+        // The entry is loaded two chunks ahead and looked at only where the page is
+        // wanted: a branch or a comparison behind the load would wait for it, and with
+        // it for all that was asked for before.
+        auto entry_of = [&](int i, int grp) {
             const int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
-            if (pi > last_page) return -1;
-            const int pg = table[pi];
-            return (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
+            return table[pi < last_page ? pi : last_page];
+        };
+        auto page_of = [&](int i, int grp, int pg) {
+            const int pi = (ch.at(i) * CK + PER * grp) >> c.page_shift;
+            return i < end && pi <= last_page && (uint32_t)pg < (uint32_t)c.n_pages ? pg : -1;
         };
         // (the maximum is that of the unscaled x: x - m then is exact where it
         // matters, however large the logits, and the difference takes the factor)
@@ -384,14 +389,15 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 
         if (begin + wave < end) {
             int i = begin + wave;
-            int kpage = page_of(i, m >> 2), vpage = page_of(i, g);
+            int kentry = entry_of(i, m >> 2), ventry = entry_of(i, g);
+            const int kpage = page_of(i, m >> 2, kentry), vpage = page_of(i, g, ventry);
             KTile<TYPE, HD> kt;
             VTile<TYPE, HD> vt;
             bool ok = vpage >= 0;  // the lane group's positions are in a page (not a hole)
             kt.template load<NT>(c, h, ch.at(i), kpage, g, m);
             vt.template load<NT>(c, h, ch.at(i), vpage, g, m);
-            kpage = page_of(i + NW, m >> 2);
-            vpage = page_of(i + NW, g);
+            kentry = entry_of(i + NW, m >> 2);
+            ventry = entry_of(i + NW, g);
 
             // the rows
             int pos[RT];
@@ -443,7 +449,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 
             for (;;) {
                 const bool more = i + NW < end;
-                const int kpage2 = page_of(i + 2 * NW, m >> 2), vpage2 = page_of(i + 2 * NW, g);
+                const int kentry2 = entry_of(i + 2 * NW, m >> 2), ventry2 = entry_of(i + 2 * NW, g);
                 f32x4 sacc[RT][2 * SUB];
 #pragma unroll
                 for (int rt = 0; rt < RT; rt++)
@@ -462,7 +468,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                 }
                 // the K registers are free: the next chunk's K flies during the
                 // softmax and the second product, its V during the next first one
-                if (more) kt.template load<NT>(c, h, ch.at(i + NW), kpage, g, m);
+                if (more) kt.template load<NT>(c, h, ch.at(i + NW), page_of(i + NW, m >> 2, kentry), g, m);
 
                 const int key0 = ch.at(i) * CK + PER * g;  // the lane group's first position
                 // a chunk that every row sees whole needs no masks
@@ -612,12 +618,13 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                             for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
                     }
                 }
-                if (more) vt.template load<NT>(c, h, ch.at(i + NW), vpage, g, m);
+                const int next_vpage = page_of(i + NW, g, ventry);
+                if (more) vt.template load<NT>(c, h, ch.at(i + NW), next_vpage, g, m);
                 if (!more) break;
                 i += NW;
-                ok = vpage >= 0;
-                kpage = kpage2;
-                vpage = vpage2;
+                ok = next_vpage >= 0;
+                kentry = kentry2;
+                ventry = ventry2;
             }
         }
 
