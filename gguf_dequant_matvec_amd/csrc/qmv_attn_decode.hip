@@ -167,40 +167,46 @@ struct KTile<kKvQ4, HD> {
     }
 };
 
-// ... V: a lane's piece is 16 positions of two columns, 16 apart; their scales
-// as pairs of positions.
+// ... V: a lane's piece is 16 positions of two columns, 16 apart.  All 16 lanes of
+// a group want the same scales, eight dwords of pairs of positions a block: each
+// lane loads its share of them (two dwords at 128 columns instead of 32), and they
+// are handed round through LDS when they are wanted.
 template <int HD>
 struct VTile<kKvQ4, HD> {
     static constexpr int DT = HD / 16, NB = HD / 32;
-    uint32_t v[NB][4], d[NB][8];
+    static constexpr int W = (NB + 1) / 2;  // dwords of scales a lane has: W m .. W m + W - 1 of the 8 NB
+    uint32_t v[NB][4], d[W];
 
     template <bool NT>
     __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
         const int slot = (chunk * kChunk<kKvQ4> + kChunk<kKvQ4> / 4 * g) & ((1 << c.page_shift) - 1);
         const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
         const uint8_t *vp = head + ((int64_t)(HD / 2) << c.page_shift) + (int64_t)slot * (HD / 2) + 16 * m;
-        const uint8_t *dp = head + ((int64_t)(HD + HD / 16) << c.page_shift) + 2 * slot;
+        const int at = W * m < 8 * NB ? W * m : 0;  // (96 columns: 12 lanes have all)
+        const uint8_t *dp = head + ((int64_t)(HD + HD / 16 + 2 * (at / 8)) << c.page_shift) + 2 * slot + 4 * (at % 8);
 #pragma unroll
         for (int b = 0; b < NB; b++) {
             const u32x4 w = load_stream<NT>(vp + 256 * b);
             v[b][0] = w.x, v[b][1] = w.y, v[b][2] = w.z, v[b][3] = w.w;
-            const u32x4 *sp = reinterpret_cast<const u32x4 *>(dp + ((int64_t)(2 * b) << c.page_shift));
-            const u32x4 x = sp[0], y = sp[1];
-            d[b][0] = x.x, d[b][1] = x.y, d[b][2] = x.z, d[b][3] = x.w;
-            d[b][4] = y.x, d[b][5] = y.y, d[b][6] = y.z, d[b][7] = y.w;
         }
+        __builtin_memcpy(d, __builtin_assume_aligned(dp, 4 * W), 4 * W);
     }
+    // the lane's share to the group's [8 NB] dwords
+    __device__ __forceinline__ void share(uint32_t *group, int m) const {
+        if (HD != 96 || W * m < 8 * NB) __builtin_memcpy(__builtin_assume_aligned(group + W * m, 4 * W), d, 4 * W);
+    }
+    // operands of tiles 2 b and 2 b + 1
     template <class Vec>
-    __device__ __forceinline__ Vec op(int u, int t) const {
-        const int b = t / 2;
-        U128 x;
+    __device__ __forceinline__ void op2(const uint32_t *group, int u, int b, Vec &x, Vec &y) const {
+        const U128 s = *reinterpret_cast<const U128 *>(group + 8 * b + 4 * u);
+        U128 p, q;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const uint32_t w = v[b][2 * u + j / 2], s = d[b][4 * u + j], c = q4_addend(s);
-            x.w[j] = t % 2 == 0 ? (j % 2 == 0 ? q4_pair<0>(w, s, c) : q4_pair<2>(w, s, c))
-                                : (j % 2 == 0 ? q4_pair<1>(w, s, c) : q4_pair<3>(w, s, c));
+            const uint32_t w = v[b][2 * u + j / 2], c = q4_addend(s.w[j]);
+            p.w[j] = j % 2 == 0 ? q4_pair<0>(w, s.w[j], c) : q4_pair<2>(w, s.w[j], c);
+            q.w[j] = j % 2 == 0 ? q4_pair<1>(w, s.w[j], c) : q4_pair<3>(w, s.w[j], c);
         }
-        return as_vec<Vec>(x);
+        x = as_vec<Vec>(p), y = as_vec<Vec>(q);
     }
 };
 
@@ -290,11 +296,44 @@ __device__ __forceinline__ Range find_range(const AttnArgs &a, int p, int lane) 
     return r;
 }
 
-template <int TYPE, int HD, int RT, int NW, bool ACC, bool RANGES>
-__global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1) void attn_decode(AttnArgs a) {
+// 4-bit rows take more instructions a byte than others, so that more waves are
+// wanted; the operands of their queries, which every chunk needs once and in the
+// same order, lie in LDS, where each lane finds its own, and not in registers.
+constexpr bool queries_in_lds(int type, int hd, int rt, int nw) {
+    return type == kKvQ4 && hd <= 128 && rt == 1 && nw == 4;
+}
+
+// PACK, 4-bit caches with few rows: the operand's 16 columns hold more than the
+// rows.  2 (at most 8 rows): both f16 pieces of a row's queries, and of its
+// probabilities, in columns of their own, so that each product is one matrix
+// instruction and not two, and a column's sum is completed by its neighbour's.
+// 4 (at most 4 rows): besides, each column's lanes take half of their 16
+// positions' probabilities (the other half's are zeros in it).  The outputs'
+// columns are added at the end.  Column m: row pack_row, piece pack_piece, half
+// m / 8 (PACK 4); the neighbour of the other piece is m + 8, or 7 - m within
+// eight, the DPP patterns that cost nothing beside the addition.
+template <int PACK>
+__device__ __forceinline__ int pack_row(int m) {
+    return PACK == 4 ? (m & 4 ? 3 - (m & 3) : m & 3) : PACK == 2 ? m & 7 : m;
+}
+template <int PACK>
+__device__ __forceinline__ int pack_piece(int m) { return PACK == 4 ? (m >> 2) & 1 : m >> 3; }
+// a where the mask's bits are set, else b.  (Said with a condition, it becomes a
+// choice of an address, and the array goes to memory.)
+__device__ __forceinline__ float pick(uint32_t mask, float a, float b) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, a) & mask) | (__builtin_bit_cast(uint32_t, b) & ~mask));
+}
+template <int PACK>
+__device__ __forceinline__ float pack_add(float x) {
+    return x + dpp_f32<PACK == 4 ? kDppHalfMirror : kDppRowRor8>(x);
+}
+
+template <int TYPE, int HD, int RT, int NW, int PACK, bool ACC, bool RANGES>
+__global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE, HD, RT, NW) ? resident(TYPE, HD) : 1) void attn_decode(AttnArgs a) {
     typedef typename KvOp<TYPE>::Op Op;
     typedef typename Op::Vec Vec;
-    constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = Op::kPieces;
+    constexpr int CK = kChunk<TYPE>, SUB = CK / 32, PER = CK / 4, NP = PACK ? 1 : Op::kPieces;
+    static_assert(!PACK || (TYPE == kKvQ4 && RT == 1), "pieces in columns");
     constexpr int KS = HD / 32, DT = HD / 16;
     // With at most 16 rows a head's cache is read by one workgroup, once:
     // nontemporal loads (32 sequences up to 8150 positions of 128 columns: 148
@@ -304,6 +343,9 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
     // ordinary (16 x 8192 positions, 4 tiles: 259 against 334 us, one tile, both
     // with two workgroups a unit: 116 against 113).
     constexpr bool NT = RT == 1 && HD <= 128;
+    constexpr bool QL = queries_in_lds(TYPE, HD, RT, NW);
+    __shared__ U128 s_q[QL ? NW : 1][QL ? KS * NP : 1][QL ? 64 : 1];
+    __shared__ __align__(16) uint32_t s_d4[TYPE == kKvQ4 ? NW : 1][4][TYPE == kKvQ4 ? HD / 4 : 1];  // scales of a chunk's V
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
     const KvArgs &c = a.c;
@@ -401,10 +443,10 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 
             // the rows
             int pos[RT];
-            U128 qf[RT][KS][NP];
+            U128 qf[RT][QL ? 1 : KS][NP];
 #pragma unroll
             for (int rt = 0; rt < RT; rt++) {
-                const int rr = r0 + rt * 16 + m;
+                const int rr = r0 + rt * 16 + pack_row<PACK>(m);
                 const bool live = rr < nrows;
                 const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
                 pos[rt] = live ? len - n + j : -1;
@@ -443,7 +485,18 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                 for (int t = 0; t < KS; t++) {
 #pragma unroll
                     for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
-                    split8<Op>(f[t], qf[rt][t]);
+                    if constexpr (PACK > 0) {
+                        U128 both[Op::kPieces];
+                        split8<Op>(f[t], both);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) qf[0][QL ? 0 : t][0].w[j] = pack_piece<PACK>(m) ? both[1].w[j] : both[0].w[j];
+                    } else {
+                        split8<Op>(f[t], qf[rt][QL ? 0 : t]);
+                    }
+                    if constexpr (QL) {
+#pragma unroll
+                        for (int p = 0; p < NP; p++) s_q[wave][t * NP + p][lane] = qf[0][0][p];
+                    }
                 }
             }
 
@@ -457,13 +510,17 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                     for (int ub = 0; ub < 2 * SUB; ub++) sacc[rt][ub] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int t = 0; t < KS; t++) {
+                    if constexpr (QL) {
+#pragma unroll
+                        for (int p = 0; p < NP; p++) qf[0][0][p] = s_q[wave][t * NP + p][lane];
+                    }
 #pragma unroll
                     for (int ub = 0; ub < 2 * SUB; ub++) {
                         const Vec kx = kt.template op<Vec>(ub >> 1, ub & 1, t);
 #pragma unroll
                         for (int rt = 0; rt < RT; rt++)
 #pragma unroll
-                            for (int p = 0; p < NP; p++) sacc[rt][ub] = Op::mfma16(kx, as_vec<Vec>(qf[rt][t][p]), sacc[rt][ub]);
+                            for (int p = 0; p < NP; p++) sacc[rt][ub] = Op::mfma16(kx, as_vec<Vec>(qf[rt][QL ? 0 : t][p]), sacc[rt][ub]);
                     }
                 }
                 // the K registers are free: the next chunk's K flies during the
@@ -511,6 +568,7 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
 #pragma unroll
                     for (int e = 0; e < PER; e++) {
                         x[e] = sacc[rt][e >> 2][e & 3];
+                        if constexpr (PACK > 0) x[e] = pack_add<PACK>(x[e]);
                         if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
                         if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
                     }
@@ -538,25 +596,49 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                     }
                     const float off = bias_of<TYPE>(a) + vlog;
                     float sum = 0.f;
+                    constexpr int MINE = PACK == 4 ? PER / 2 : PER;  // of them the lane takes
+                    const uint32_t upper = m & 8 ? ~0u : 0u;
+                    if constexpr (PACK == 4) {
 #pragma unroll
-                    for (int e = 0; e < PER; e++) {
+                        for (int e = 0; e < MINE; e++) x[e] = pick(upper, x[MINE + e], x[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < MINE; e++) {
                         const bool hidden = TYPE == kKvI8 && !whole && x[e] == -__builtin_inff();
                         x[e] = exp2_fast(fmaf(minus(x[e], mrun[rt]), qscale[rt], off));
                         sum += x[e];
                         if constexpr (TYPE == kKvI8) x[e] = hidden ? 0.f : x[e] * vt.vs[e];  // (which may be NaN)
                     }
                     lrun[rt] += TYPE == kKvI8 ? sum * vback : sum;
+                    if constexpr (PACK > 0) {
 #pragma unroll
-                    for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
+                        for (int u = 0; u < MINE / 8; u++) {
+                            U128 both[Op::kPieces];
+                            split8<Op>(x + 8 * u, both);
+#pragma unroll
+                            for (int j = 0; j < 4; j++) {
+                                const uint32_t w = pack_piece<PACK>(m) ? both[1].w[j] : both[0].w[j];
+                                if constexpr (PACK == 4) {
+                                    pf[0][0][0].w[j] = w & ~upper;
+                                    pf[0][1][0].w[j] = w & upper;
+                                } else {
+                                    pf[0][u][0].w[j] = w;
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
+                    }
                 }
                 if constexpr (TYPE == kKvQ4) {  // a 4-bit value is not finite where its block's scale is not
                     if (!whole) {
                         uint32_t bad = 0;
 #pragma unroll
-                        for (int b = 0; b < HD / 32; b++)
-#pragma unroll
-                            for (int j = 0; j < 8; j++) bad |= not_finite<Op>(vt.d[b][j]);
+                        for (int j = 0; j < VTile<TYPE, HD>::W; j++) bad |= not_finite<Op>(vt.d[j]);
                         if (__any(bad != 0)) {
+                            vt.share(s_d4[wave][g], m);
+                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
                             for (int u = 0; u < SUB; u++) {
                                 U128 seen[RT];
@@ -564,13 +646,9 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                                 for (int rt = 0; rt < RT; rt++) seen[rt] = seen8(ok, pos[rt], key0 + 8 * u, a.window, a.sinks);
 #pragma unroll
                                 for (int b = 0; b < HD / 32; b++) {
-                                    U128 marks;
+                                    U128 marks = *reinterpret_cast<const U128 *>(&s_d4[wave][g][8 * b + 4 * u]);
 #pragma unroll
-                                    for (int j = 0; j < 4; j++) {
-                                        const uint32_t x = not_finite<Op>(vt.d[b][4 * u + j]);
-                                        vt.d[b][4 * u + j] &= ~(x * 0xFFFFu);
-                                        marks.w[j] = x * kHuge;
-                                    }
+                                    for (int j = 0; j < 4; j++) marks.w[j] = not_finite<Op>(marks.w[j]) * kHuge;
 #pragma unroll
                                     for (int rt = 0; rt < RT; rt++) {
                                         o[rt][2 * b] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][2 * b]);
@@ -578,8 +656,13 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                                     }
                                 }
                             }
+                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                            for (int j = 0; j < VTile<TYPE, HD>::W; j++) vt.d[j] &= ~(not_finite<Op>(vt.d[j]) * 0xFFFFu);
                         }
                     }
+                    vt.share(s_d4[wave][g], m);
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 } else if constexpr (TYPE != kKvI8) {
                     if (!whole) {
                         uint32_t bad = 0;
@@ -609,13 +692,23 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
                 }
 #pragma unroll
                 for (int u = 0; u < SUB; u++) {
-#pragma unroll
-                    for (int t = 0; t < DT; t++) {
-                        const Vec vx = vt.template op<Vec>(u, t);
+                    auto add = [&](const Vec &vx, int t) {
 #pragma unroll
                         for (int rt = 0; rt < RT; rt++)
 #pragma unroll
                             for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
+                    };
+                    if constexpr (TYPE == kKvQ4) {
+#pragma unroll
+                        for (int b = 0; b < HD / 32; b++) {
+                            Vec x, y;
+                            vt.template op2<Vec>(s_d4[wave][g], u, b, x, y);
+                            add(x, 2 * b);
+                            add(y, 2 * b + 1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < DT; t++) add(vt.template op<Vec>(u, t), t);
                     }
                 }
                 const int next_vpage = page_of(i + NW, g, ventry);
@@ -628,6 +721,16 @@ __global__ __launch_bounds__(NW * 64, RANGES && RT == 1 ? resident(TYPE, HD) : 1
             }
         }
 
+        if constexpr (PACK > 0) {
+            if constexpr (PACK == 4) lrun[0] += dpp_f32<kDppRowRor8>(lrun[0]);
+#pragma unroll
+            for (int t = 0; t < DT; t++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    o[0][t][e] = pack_add<PACK>(o[0][t][e]);
+                    if constexpr (PACK == 4) o[0][t][e] += dpp_f32<kDppRowRor8>(o[0][t][e]);
+                }
+        }
         // join the waves: a common maximum, then the partial sums two by two
         __shared__ float s_m[NW][RT * 16], s_l[NW][RT * 16];
         __shared__ f32x4 s_o[2][RT * DT * 64];
@@ -796,11 +899,21 @@ __global__ __launch_bounds__(256) void attn_join_weights(AttnArgs a, int rt16) {
     if (key < len) a.acc[head * a.ld_acc + key] += sum;
 }
 
+template <int TYPE, int HD, int RT, int NW, int PACK, bool RANGES>
+hipError_t launch_packed(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
+    const dim3 grid(RANGES ? p.parts : p.splits, a.c.n_kv * p.tiles, RANGES ? 1 : a.c.n_seq);
+    if (a.acc) return launch_main(attn_decode<TYPE, HD, RT, NW, PACK, true, RANGES>, grid, dim3(NW * 64), 0, s, a);
+    return launch_main(attn_decode<TYPE, HD, RT, NW, PACK, false, RANGES>, grid, dim3(NW * 64), 0, s, a);
+}
+
 template <int TYPE, int HD, int RT, int NW, bool RANGES>
 hipError_t launch_main_of(const AttnArgs &a, const AttnPlan &p, hipStream_t s) {
-    const dim3 grid(RANGES ? p.parts : p.splits, a.c.n_kv * p.tiles, RANGES ? 1 : a.c.n_seq);
-    if (a.acc) return launch_main(attn_decode<TYPE, HD, RT, NW, true, RANGES>, grid, dim3(NW * 64), 0, s, a);
-    return launch_main(attn_decode<TYPE, HD, RT, NW, false, RANGES>, grid, dim3(NW * 64), 0, s, a);
+    if constexpr (TYPE == kKvQ4 && RT == 1) {
+        const int64_t rows = a.n * a.group;
+        if (rows <= 4) return launch_packed<TYPE, HD, RT, NW, 4, RANGES>(a, p, s);
+        if (rows <= 8) return launch_packed<TYPE, HD, RT, NW, 2, RANGES>(a, p, s);
+    }
+    return launch_packed<TYPE, HD, RT, NW, 0, RANGES>(a, p, s);
 }
 
 template <int TYPE, int HD, int RT, int NW>

@@ -16,7 +16,10 @@ constexpr int kMaxPieces = 512;  // pieces of an output row that the join takes
 
 // Workgroups of four waves and 16-row tiles that the registers of a compute
 // unit hold at once (256 columns take more than half of them).
-constexpr int resident(int type, int hd) { return hd == 256 ? 1 : hd == 64 && type != kKvI8 ? 3 : 2; }
+constexpr int resident(int type, int hd) {
+    if (hd == 256) return 1;
+    return type == kKvQ4 || (hd == 64 && type != kKvI8) ? 3 : 2;
+}
 
 // Whether the 256 registers that eight waves leave each lane hold the kernel's
 // operands; four waves have 512.
