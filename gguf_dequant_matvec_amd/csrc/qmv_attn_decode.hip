@@ -136,11 +136,12 @@ struct KTile<kKvQ4, HD> {
 
     template <bool NT>
     __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
-        const int pos = chunk * kChunk<kKvQ4> + kChunk<kKvQ4> / 4 * (m >> 2);
-        const int slot = (pos & ((1 << c.page_shift) - 1)) + (m & 3);
+        // the chunk's first slot is the wave's, the rest the lane's for all chunks
+        const int mask = (1 << c.page_shift) - 1, s0 = chunk * kChunk<kKvQ4> & mask;
+        const int mine = (kChunk<kKvQ4> / 4 * (m >> 2) & mask) + (m & 3);
         const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
-        const uint8_t *kp = head + (int64_t)slot * (HD / 2) + 4 * W * g;
-        const uint16_t *dp = reinterpret_cast<const uint16_t *>(head + ((int64_t)HD << c.page_shift)) + (int64_t)slot * (HD / 32);
+        const uint8_t *kp = head + (int64_t)(s0 + mine) * (HD / 2) + 4 * W * g;
+        const uint16_t *dp = reinterpret_cast<const uint16_t *>(head + ((int64_t)HD << c.page_shift)) + (int64_t)(s0 + mine) * (HD / 32);
 #pragma unroll
         for (int r = 0; r < R; r++) {
             const uint8_t *row = kp + r * 4 * (HD / 2);
@@ -179,11 +180,12 @@ struct VTile<kKvQ4, HD> {
 
     template <bool NT>
     __device__ __forceinline__ void load(const KvArgs &c, int h, int chunk, int page, int g, int m) {
-        const int slot = (chunk * kChunk<kKvQ4> + kChunk<kKvQ4> / 4 * g) & ((1 << c.page_shift) - 1);
+        const int mask = (1 << c.page_shift) - 1, s0 = chunk * kChunk<kKvQ4> & mask;
+        const int mine = kChunk<kKvQ4> / 4 * g & mask;
         const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
-        const uint8_t *vp = head + ((int64_t)(HD / 2) << c.page_shift) + (int64_t)slot * (HD / 2) + 16 * m;
+        const uint8_t *vp = head + ((int64_t)(HD / 2) << c.page_shift) + (int64_t)(s0 + mine) * (HD / 2) + 16 * m;
         const int at = W * m < 8 * NB ? W * m : 0;  // (96 columns: 12 lanes have all)
-        const uint8_t *dp = head + ((int64_t)(HD + HD / 16 + 2 * (at / 8)) << c.page_shift) + 2 * slot + 4 * (at % 8);
+        const uint8_t *dp = head + ((int64_t)(HD + HD / 16 + 2 * (at / 8)) << c.page_shift) + 2 * (s0 + mine) + 4 * (at % 8);
 #pragma unroll
         for (int b = 0; b < NB; b++) {
             const u32x4 w = load_stream<NT>(vp + 256 * b);
@@ -569,8 +571,18 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                     for (int e = 0; e < PER; e++) {
                         x[e] = sacc[rt][e >> 2][e & 3];
                         if constexpr (PACK > 0) x[e] = pack_add<PACK>(x[e]);
-                        if constexpr (TYPE == kKvI8) x[e] *= vt.ks[e];
-                        if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                        if constexpr (TYPE == kKvI8) {
+                            x[e] *= vt.ks[e];
+                            if (!whole) x[e] = ok && sees(pos[rt], key0 + e, a.window, a.sinks) ? x[e] : -__builtin_inff();
+                        }
+                    }
+                    // (one branch: inside the loop above it is one for every position.  The
+                    // 8-bit kernel keeps those: 131071 positions 54 us, with one 64)
+                    if (TYPE != kKvI8 && !whole) {
+                        const int top = ok ? pos[rt] : -1, low = a.window > 0 ? pos[rt] - a.window : -1;
+#pragma unroll
+                        for (int e = 0; e < PER; e++)
+                            x[e] = (key0 + e <= top) & ((key0 + e > low) | (key0 + e < a.sinks)) ? x[e] : -__builtin_inff();
                     }
                     if constexpr (ACC) {
                         const int rr = r0 + rt * 16 + m;
@@ -692,23 +704,28 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                 }
 #pragma unroll
                 for (int u = 0; u < SUB; u++) {
-                    auto add = [&](const Vec &vx, int t) {
-#pragma unroll
-                        for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                            for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
-                    };
                     if constexpr (TYPE == kKvQ4) {
 #pragma unroll
                         for (int b = 0; b < HD / 32; b++) {
                             Vec x, y;
                             vt.template op2<Vec>(s_d4[wave][g], u, b, x, y);
-                            add(x, 2 * b);
-                            add(y, 2 * b + 1);
+#pragma unroll
+                            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                                for (int p = 0; p < NP; p++) {
+                                    o[rt][2 * b] = Op::mfma16(x, as_vec<Vec>(pf[rt][u][p]), o[rt][2 * b]);
+                                    o[rt][2 * b + 1] = Op::mfma16(y, as_vec<Vec>(pf[rt][u][p]), o[rt][2 * b + 1]);
+                                }
                         }
                     } else {
 #pragma unroll
-                        for (int t = 0; t < DT; t++) add(vt.template op<Vec>(u, t), t);
+                        for (int t = 0; t < DT; t++) {
+                            const Vec vx = vt.template op<Vec>(u, t);
+#pragma unroll
+                            for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                                for (int p = 0; p < NP; p++) o[rt][t] = Op::mfma16(vx, as_vec<Vec>(pf[rt][u][p]), o[rt][t]);
+                        }
                     }
                 }
                 const int next_vpage = page_of(i + NW, g, ventry);
