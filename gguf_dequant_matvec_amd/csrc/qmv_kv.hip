@@ -46,9 +46,27 @@ __device__ __forceinline__ uint32_t kv_scale4(float hi, float lo, bool nan) {
     const float v = (float)(__bf16)((hi >= -lo ? hi : lo) * -0.125f);
     return __builtin_bit_cast(uint16_t, (_Float16)fminf(fmaxf(v, -2720.f), 2720.f));
 }
-__device__ __forceinline__ uint32_t kv_code4(float x, float d) {  // 0 .. 15
-    const float r = d != 0.f ? rintf(x / d) : 0.f;
-    return (uint32_t)(int)(fminf(fmaxf(r, -8.f), 7.f) + 8.f);
+__device__ __forceinline__ uint32_t kv_clamp4(float r) { return (uint32_t)(int)(fminf(fmaxf(r, -8.f), 7.f) + 8.f); }
+// Codes 0 .. 15 of eight values, four bytes a dword.  x times 1 / d is off from the
+// quotient by less than 2^-19 where the code is not clamped; only where it is that
+// near to a border between two codes does the division itself decide, for all
+// eight (a division is ten instructions: 6808 rows of 8 heads of 128 26.6 us).
+__device__ __forceinline__ void kv_codes4(const float *x, float d, uint32_t *code) {
+    const float inv = d != 0.f ? 1.f / d : 0.f;
+    float r[8];
+    bool near = false;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float y = x[j] * inv;
+        r[j] = rintf(y);
+        near |= fabsf(y - r[j]) > 0.5f - 0x1p-18f;
+    }
+    if (near && d != 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) r[j] = rintf(x[j] / d);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) code[j >> 2] |= kv_clamp4(r[j]) << (8 * (j & 3));
 }
 
 // Where row r goes: its sequence's position (-1: none), page (-1: nowhere) and slot.
@@ -116,18 +134,32 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRo
     __shared__ uint16_t s_d4[2][TYPE == kKvQ4 ? NB * ROWS : 1];
     __shared__ int s_pos[ROPE ? ROWS : 1];
     __shared__ __align__(16) float s_k[ROPE ? ROWS * KROW : 1];
-    const int tid = threadIdx.x, h = blockIdx.y;
-    const int64_t row0 = (int64_t)blockIdx.x * ROWS;
+    const int tid = threadIdx.x;
+    int h = blockIdx.y;
+    int64_t row0 = (int64_t)blockIdx.x * ROWS;
+    if constexpr (ROPE > 1) {
+        // many rows of many heads: neighbouring workgroups, which start together,
+        // take neighbouring heads of the same rows (6808 rows of 32 / 8 heads of 128,
+        // 307 MB: 79 -> 70 us)
+        const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        h = (int)(id % gridDim.y);
+        row0 = id / gridDim.y * ROWS;
+    }
     const int rows = n - row0 < ROWS ? (int)(n - row0) : ROWS;
 
     if constexpr (ROPE > 0) {
         if (h >= c.n_kv) {
+            const int h0 = (h - c.n_kv) * ROPE;
             if (tid < ROWS) s_pos[tid] = kv_place(c, row0 + tid, n, start).pos;
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < RN; i++) {
                 const int e = tid + 256 * i, r = e / L;
-                if (r < ROWS && s_pos[r] >= 0) rope_heads<HD, ROPE>(rope, q, rope.q_norm, row0 + r, s_pos[r], e % L, (h - c.n_kv) * ROPE);
+                if (r >= ROWS || s_pos[r] < 0) continue;
+                const RopeLane l = rope_lane<HD>(rope, e % L);
+                RopeHeads<HD, ROPE> heads;
+                heads.load(q, l, row0 + r, h0);
+                heads.finish(rope, q, rope.q_norm, l, row0 + r, s_pos[r], e % L, h0);
             }
             return;
         }
@@ -233,8 +265,7 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRo
                 }
                 const uint32_t d = kv_scale4(hi, lo, nan != 0);
                 const float df = half_bits_to_float(d);
-#pragma unroll
-                for (int j = 0; j < 8; j++) code[j >> 2] |= kv_code4(f[j], df) << (8 * (j & 3));
+                kv_codes4(f, df, code);
 #pragma unroll
                 for (int j = 0; j < 2; j++) code[j] |= (uint32_t)__shfl_xor((int)code[j], 2) << 4;
                 if (p % 4 == 0) s_d4[which][(p / 4) * ROWS + r] = (uint16_t)d;
@@ -319,10 +350,10 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRo
 }
 
 // ---- reading back ---------------------------------------------------------------
-// A workgroup takes 16 consecutive rows of one key-value head.  K comes as it
-// goes out.  V's lanes run over the rows first (16 positions of a column are
-// neighbours in a block) and go through LDS.
-constexpr int kReadRows = 16;
+// A workgroup takes 32 consecutive rows of one key-value head, four columns a
+// thread at a time.  K goes out as it comes.  V's lanes run over the rows first
+// (16 positions of a column are neighbours in a block) and go through LDS.
+constexpr int kReadRows = 32;
 
 template <int TYPE>
 __device__ __forceinline__ float kv_value(const uint8_t *p, int64_t i) {
@@ -336,8 +367,10 @@ __global__ __launch_bounds__(256) void kv_read(KvArgs c, int64_t n, const int32_
                                                int64_t ldk, float *__restrict__ v, int64_t ldv) {
     constexpr int SZ = TYPE == kKvF16 || TYPE == kKvBF16 ? 2 : 1;
     constexpr int VC = TYPE == kKvQ4 ? HD / 2 : HD, NB = HD / 32;
+    constexpr int VN = kReadRows * VC / 256, N4 = kReadRows * HD / 4 / 256;  // V values (bytes) and pieces a thread
+    constexpr int VROW = HD + 4;
     __shared__ int s_pos[kReadRows], s_page[kReadRows], s_slot[kReadRows];
-    __shared__ float s_v[kReadRows][HD + 1];
+    __shared__ __align__(16) float s_v[kReadRows * VROW];
     const int tid = threadIdx.x, h = blockIdx.y;
     const int64_t row0 = (int64_t)blockIdx.x * kReadRows, page_size = 1ll << c.page_shift;
     if (tid < kReadRows) {
@@ -345,52 +378,68 @@ __global__ __launch_bounds__(256) void kv_read(KvArgs c, int64_t n, const int32_
         s_pos[tid] = at.pos, s_page[tid] = at.page, s_slot[tid] = at.slot;
     }
     __syncthreads();
-    for (int e = tid; e < kReadRows * VC; e += 256) {
-        const int r = e % kReadRows, d = e / kReadRows, page = s_page[r], slot = s_slot[r];
-        const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h), *codes = head + page_size * VC * SZ;
-        const int64_t block = (int64_t)(slot / kVBlock) * (VC * kVBlock) + d * kVBlock;
+    // (slots of rows without a page are read from page 0, and not used)
+    const int rv = tid % kReadRows, v_page = s_page[rv], v_slot = s_slot[rv];
+    const uint8_t *v_head = kv_head(c, v_page < 0 ? 0 : v_page, h);
+    const int in16 = TYPE == kKvQ4 ? kv_place4(v_slot % kVBlock) : v_slot % kVBlock;
+    const uint8_t *v_codes = v_head + page_size * VC * SZ + ((int64_t)(v_slot / kVBlock) * (VC * kVBlock) + in16) * SZ;
+    float vx[VN];
+    uint32_t vb[TYPE == kKvQ4 ? VN : 1];
+    uint16_t vd[TYPE == kKvQ4 ? VN : 1];
+#pragma unroll
+    for (int i = 0; i < VN; i++) {
+        const int d = tid / kReadRows + 256 / kReadRows * i;
         if constexpr (TYPE == kKvQ4) {
-            const int b = d / 16, col = 32 * b + d % 16;
-            float x = 0.f, y = 0.f;
-            if (page >= 0) {
-                const uint32_t byte = codes[block + kv_place4(slot % kVBlock)];
-                const uint16_t *sc = reinterpret_cast<const uint16_t *>(head + page_size * HD);
-                const float f = half_bits_to_float(sc[page_size * NB + b * page_size + slot]);
-                x = f * (float)((int)(byte & 15) - 8), y = f * (float)((int)(byte >> 4) - 8);
-            }
-            s_v[r][col] = x, s_v[r][col + 16] = y;
+            vb[i] = v_codes[d * kVBlock];
+            vd[i] = reinterpret_cast<const uint16_t *>(v_head + page_size * HD)[page_size * NB + d / 16 * page_size + v_slot];
         } else {
-            float x = 0.f;
-            if (page >= 0) {
-                x = kv_value<TYPE>(codes, block + slot % kVBlock);
-                if constexpr (TYPE == kKvI8)
-                    x *= reinterpret_cast<const float *>(head + 2 * page_size * HD)[page_size + slot];
-            }
-            s_v[r][d] = x;
+            vx[i] = kv_value<TYPE>(v_codes, d * kVBlock);
         }
     }
-    for (int e = tid; e < kReadRows * HD; e += 256) {
-        const int r = e / HD, d = e % HD, page = s_page[r], slot = s_slot[r];
+    float v_scale = 1.f;
+    if constexpr (TYPE == kKvI8) v_scale = reinterpret_cast<const float *>(v_head + 2 * page_size * HD)[page_size + v_slot];
+#pragma unroll
+    for (int i = 0; i < N4; i++) {
+        const int e = tid + 256 * i, r = e / (HD / 4), d = e % (HD / 4) * 4, page = s_page[r], slot = s_slot[r];
         if (s_pos[r] < 0) continue;
         const uint8_t *head = kv_head(c, page < 0 ? 0 : page, h);
-        float x = 0.f;
-        if (page >= 0) {
-            if constexpr (TYPE == kKvQ4) {
-                const int b = d / 32;
-                const uint32_t byte = head[(int64_t)slot * VC + 16 * b + d % 16];
-                x = half_bits_to_float(reinterpret_cast<const uint16_t *>(head + page_size * HD)[(int64_t)slot * NB + b]) *
-                    (float)((int)(byte >> (d % 32 / 16 * 4) & 15) - 8);
-            } else {
-                x = kv_value<TYPE>(head, (int64_t)slot * HD + d);
-                if constexpr (TYPE == kKvI8) x *= reinterpret_cast<const float *>(head + 2 * page_size * HD)[slot];
+        float x[4];
+        if constexpr (TYPE == kKvQ4) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(head + (int64_t)slot * VC + 16 * (d / 32) + d % 16) >> (d % 32 / 16 * 4);
+            const float f = half_bits_to_float(reinterpret_cast<const uint16_t *>(head + page_size * HD)[(int64_t)slot * NB + d / 32]);
+#pragma unroll
+            for (int j = 0; j < 4; j++) x[j] = f * (float)((int)(w >> (8 * j) & 15) - 8);
+        } else {
+            float f = 1.f;
+            if constexpr (TYPE == kKvI8) f = reinterpret_cast<const float *>(head + 2 * page_size * HD)[slot];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                x[j] = kv_value<TYPE>(head, (int64_t)slot * HD + d + j);
+                if constexpr (TYPE == kKvI8) x[j] *= f;
             }
         }
-        k[(row0 + r) * ldk + (int64_t)h * HD + d] = x;
+        const float4 y = page < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x[0], x[1], x[2], x[3]);
+        __builtin_memcpy(k + (row0 + r) * ldk + (int64_t)h * HD + d, &y, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < VN; i++) {
+        const int d = tid / kReadRows + 256 / kReadRows * i;
+        if constexpr (TYPE == kKvQ4) {
+            const int col = 32 * (d / 16) + d % 16;
+            const float f = half_bits_to_float(vd[i]);
+            s_v[rv * VROW + col] = v_page < 0 ? 0.f : f * (float)((int)(vb[i] & 15) - 8);
+            s_v[rv * VROW + col + 16] = v_page < 0 ? 0.f : f * (float)((int)(vb[i] >> 4) - 8);
+        } else {
+            s_v[rv * VROW + d] = v_page < 0 ? 0.f : TYPE == kKvI8 ? vx[i] * v_scale : vx[i];
+        }
     }
     __syncthreads();
-    for (int e = tid; e < kReadRows * HD; e += 256) {
-        const int r = e / HD, d = e % HD;
-        if (s_pos[r] >= 0) v[(row0 + r) * ldv + (int64_t)h * HD + d] = s_v[r][d];
+#pragma unroll
+    for (int i = 0; i < N4; i++) {
+        const int e = tid + 256 * i, r = e / (HD / 4), d = e % (HD / 4) * 4;
+        if (s_pos[r] < 0) continue;
+        const float4 y = *reinterpret_cast<const float4 *>(s_v + r * VROW + d);
+        __builtin_memcpy(v + (row0 + r) * ldv + (int64_t)h * HD + d, &y, 16);
     }
 }
 
@@ -779,10 +828,11 @@ hipError_t append_rows(const AppendCall &a) {
 template <int HD>
 hipError_t append_hd(const AppendCall &a, bool rope) {
     // 32 rows once that still gives two workgroups per compute unit (6808 rows
-    // of 8 heads of 128: 20.8 us, with 16 rows 23.5, with 64 rows 23.6)
+    // of 8 heads of 128: 20.8 us, with 16 rows 23.5, with 64 rows 23.6; 4 bits, which
+    // compute longer between reading and writing, 24.2 us and with 16 rows 21.5)
     const bool many = a.n * a.c.n_kv >= 32 * 512;
-    if (rope) return many ? append_rows<HD, 32, 4>(a) : append_rows<HD, 16, 1>(a);
-    return many ? append_rows<HD, 32, 0>(a) : append_rows<HD, 16, 0>(a);
+    if (rope) return many ? append_rows<HD, 32, 2>(a) : append_rows<HD, 16, 1>(a);
+    return many && a.type != kKvQ4 ? append_rows<HD, 32, 0>(a) : append_rows<HD, 16, 0>(a);
 }
 
 hipError_t append_call(const AppendCall &a, bool rope) {

@@ -139,24 +139,29 @@ __device__ __forceinline__ Cols8 rope_apply(const RopeArgs &a, const RopeLane &l
     return y;
 }
 
-// Heads h0 .. h0 + HB - 1 of one row, by the row's lanes, all of them read before
-// the first is done.  A lane writes only what it has read, and a norm's sum
-// comes before the row is written, so rows may be turned in place.
+// Heads h0 .. h0 + HB - 1 of one row, by the row's lanes: all of them are read
+// first, while the row's position is still looked up.  A lane writes only what it
+// has read, and a norm's sum comes before the row is written, so rows may be
+// turned in place.
 template <int HD, int HB>
-__device__ __forceinline__ void rope_heads(const RopeArgs &a, const HeadRows &x, const float *w, int64_t row, int pos,
-                                           int p, int h0) {
-    const RopeLane l = rope_lane<HD>(a, p);
-    const float *in = x.in + row * x.ld_in;
-    float *out = x.out + row * x.ld_out;
+struct RopeHeads {
     Cols8 v[HB];
+
+    __device__ __forceinline__ void load(const HeadRows &x, const RopeLane &l, int64_t row, int h0) {
+        const float *in = x.in + row * x.ld_in;
 #pragma unroll
-    for (int i = 0; i < HB; i++) v[i] = rope_load(in + (int64_t)(h0 + i < x.heads ? h0 + i : h0) * HD, l);
-    const Turn t = rope_turn(a, l, p, pos);
-#pragma unroll
-    for (int i = 0; i < HB; i++) {
-        const Cols8 y = rope_apply<HD>(a, l, t, v[i], w);
-        if (h0 + i < x.heads && l.live) rope_store(out + (int64_t)(h0 + i) * HD, l, y);
+        for (int i = 0; i < HB; i++) v[i] = rope_load(in + (int64_t)(h0 + i < x.heads ? h0 + i : h0) * HD, l);
     }
-}
+    __device__ __forceinline__ void finish(const RopeArgs &a, const HeadRows &x, const float *w, const RopeLane &l,
+                                           int64_t row, int pos, int p, int h0) const {
+        float *out = x.out + row * x.ld_out;
+        const Turn t = rope_turn(a, l, p, pos);
+#pragma unroll
+        for (int i = 0; i < HB; i++) {
+            const Cols8 y = rope_apply<HD>(a, l, t, v[i], w);
+            if (h0 + i < x.heads && l.live) rope_store(out + (int64_t)(h0 + i) * HD, l, y);
+        }
+    }
+};
 
 }  // namespace qmv

@@ -19,16 +19,26 @@ constexpr int kRopeRows = HD == 64 ? 32 : 16;
 template <int HD, int HB>
 __global__ __launch_bounds__(256) void qk_norm_rope(RopeArgs a, int64_t n, const int32_t *pos, HeadRows q, HeadRows k) {
     constexpr int L = kRopeLanes<HD>, R = 256 / L;
-    const int p = threadIdx.x % L, q_chunks = (q.heads + HB - 1) / HB, chunk = blockIdx.y;
+    const int p = threadIdx.x % L, q_chunks = (q.heads + HB - 1) / HB;
+    int chunk = blockIdx.y;
+    int64_t tile = blockIdx.x;
+    if constexpr (HB > 1) {  // neighbouring workgroups: neighbouring heads of the same rows
+        const int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+        chunk = (int)(id % gridDim.y);
+        tile = id / gridDim.y;
+    }
+    const bool is_q = chunk < q_chunks;
+    const HeadRows &x = is_q ? q : k;
+    const int h0 = (is_q ? chunk : chunk - q_chunks) * HB;
+    const RopeLane l = rope_lane<HD>(a, p);
 #pragma unroll
     for (int i = 0; i < kRopeRows<HD>; i += R) {
-        const int64_t row = (int64_t)blockIdx.x * kRopeRows<HD> + i + threadIdx.x / L;
-        const int at = row < n ? pos[row] : -1;
-        if (at < 0) continue;
-        if (chunk < q_chunks)
-            rope_heads<HD, HB>(a, q, a.q_norm, row, at, p, chunk * HB);
-        else
-            rope_heads<HD, HB>(a, k, a.k_norm, row, at, p, (chunk - q_chunks) * HB);
+        const int64_t row = tile * kRopeRows<HD> + i + threadIdx.x / L;
+        if (row >= n) continue;
+        RopeHeads<HD, HB> heads;
+        heads.load(x, l, row, h0);
+        const int at = pos[row];
+        if (at >= 0) heads.finish(a, x, is_q ? a.q_norm : a.k_norm, l, row, at, p, h0);
     }
 }
 
