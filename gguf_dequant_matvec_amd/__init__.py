@@ -448,6 +448,11 @@ def _f32_rows(name, a, ld, n, width):
         return width if ld is None else ld
     if a.dtype is not _torch().float32:
         raise ValueError(f"{name} must be float32")
+    if ld is None and a.dim() == 2:      # the usual rows, without the loop below
+        rows, cols = a.shape
+        step, inner = a.stride()
+        if rows >= n and cols == width and inner == 1:
+            return step if n > 1 else width
     if ld is not None:
         have = a.untyped_storage().nbytes() // 4 - a.storage_offset()
         if (n - 1) * ld + width > have:
@@ -569,23 +574,33 @@ def qmv_kv_append_rope(cache, rope, n, n_heads, q, q_out, k, v, start=None, ldq=
           ldqo, _ptr(k), ldk, _ptr(v), ldv, _cache_stream(cache, stream, start, q, q_out, k, v))
 
 
+def _dense_ptr(name, a, dtype, numel, on):
+    """Address of `numel` contiguous values of a torch dtype on GPU `on` (None: any), all checks
+    in one pass: these calls are as short as their checks."""
+    if a is None:
+        return 0
+    if a.__class__ is int:
+        return a
+    if a.dtype is not dtype or a.numel() < numel or not a.is_contiguous():
+        raise ValueError(f"{name} must hold {numel} contiguous {dtype} values")
+    if on is not None and a.get_device() != on:
+        raise ValueError(f"{name} is on {a.device}, the cache on GPU {on}")
+    return a.data_ptr()
+
+
 def qmv_kv_reserve(cache, add, free_pages, free_count, n, granted, start, pos=None, slot=None, stream=None):
-    for name, a, dtype, numel in (("add", add, "int32", cache.n_seq), ("free_pages", free_pages, "int32", cache.n_pages),
-                                  ("free_count", free_count, "int32", 1), ("granted", granted, "int32", cache.n_seq),
-                                  ("pos", pos, "int32", n), ("slot", slot, "int64", n)):
-        _check_dense(name, a, dtype, numel)
-    _check_start(cache, start)
-    _call("qmv_kv_reserve", cache._address, _ptr(add), _ptr(free_pages), _ptr(free_count), n, _ptr(granted),
-          _ptr(start), _ptr(pos), _ptr(slot),
-          _cache_stream(cache, stream, add, free_pages, free_count, granted, start, pos, slot))
+    on, n_seq, i32 = cache.device, cache.n_seq, _torch().int32
+    _call("qmv_kv_reserve", cache._address, _dense_ptr("add", add, i32, n_seq, on),
+          _dense_ptr("free_pages", free_pages, i32, cache.n_pages, on), _dense_ptr("free_count", free_count, i32, 1, on),
+          n, _dense_ptr("granted", granted, i32, n_seq, on), _dense_ptr("start", start, i32, n_seq + 1, on),
+          _dense_ptr("pos", pos, i32, n, on), _dense_ptr("slot", slot, _torch().int64, n, on), _cache_stream(cache, stream))
 
 
 def qmv_kv_release(cache, new_len, free_pages, free_count, stream=None):
-    for name, a, numel in (("new_len", new_len, cache.n_seq), ("free_pages", free_pages, cache.n_pages),
-                           ("free_count", free_count, 1)):
-        _check_dense(name, a, "int32", numel)
-    _call("qmv_kv_release", cache._address, _ptr(new_len), _ptr(free_pages), _ptr(free_count),
-          _cache_stream(cache, stream, new_len, free_pages, free_count))
+    on, i32 = cache.device, _torch().int32
+    _call("qmv_kv_release", cache._address, _dense_ptr("new_len", new_len, i32, cache.n_seq, on),
+          _dense_ptr("free_pages", free_pages, i32, cache.n_pages, on), _dense_ptr("free_count", free_count, i32, 1, on),
+          _cache_stream(cache, stream))
 
 
 def qmv_attn_decode_workspace(cache, n, n_heads, max_len, window=0, sinks=0, with_acc=False) -> int:
