@@ -88,8 +88,8 @@ __device__ __forceinline__ Place kv_place(const KvArgs &c, int64_t r, int64_t n,
         first = start[seq];
         next = start[seq + 1];
     } else {
-        const int64_t each = n / c.n_seq;
-        seq = (int)(r / each);
+        const uint32_t each = (uint32_t)n / (uint32_t)c.n_seq;  // (n is at most 2^27)
+        seq = (int)((uint32_t)r / each);
         first = (int64_t)seq * each;
         next = first + each;
     }
@@ -147,30 +147,43 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRo
     }
     const int rows = n - row0 < ROWS ? (int)(n - row0) : ROWS;
 
+    const RopeLane rl = rope_lane<HD>(rope, tid % L);  // (L divides 256: the same for all of a thread's rows)
     if constexpr (ROPE > 0) {
         if (h >= c.n_kv) {
             const int h0 = (h - c.n_kv) * ROPE;
+            const RopeWith with = rope_with(rope, rl, tid % L, rope.q_norm);
+            // (few rows: everything is asked for at once; with many, rows held while
+            // positions are looked up cost more registers than that gains)
+            constexpr bool EARLY = ROPE == 1;
+            RopeHeads<HD, ROPE> early[EARLY ? RN : 1];
+            if constexpr (EARLY) {
+#pragma unroll
+                for (int i = 0; i < RN; i++) {
+                    const int r = (tid + 256 * i) / L;
+                    early[i].load(q, rl, row0 + (r < rows ? r : 0), h0);
+                }
+            }
             if (tid < ROWS) s_pos[tid] = kv_place(c, row0 + tid, n, start).pos;
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < RN; i++) {
-                const int e = tid + 256 * i, r = e / L;
+                const int r = (tid + 256 * i) / L;
                 if (r >= ROWS || s_pos[r] < 0) continue;
-                const RopeLane l = rope_lane<HD>(rope, e % L);
-                RopeHeads<HD, ROPE> heads;
-                heads.load(q, l, row0 + r, h0);
-                heads.finish(rope, q, rope.q_norm, l, row0 + r, s_pos[r], e % L, h0);
+                if constexpr (!EARLY) early[0].load(q, rl, row0 + r, h0);
+                early[EARLY ? i : 0].finish(rope, q, rl, with, row0 + r, s_pos[r], h0);
             }
             return;
         }
     }
     float kf[N][8], vf[N][8];
     Cols8 kx[ROPE ? RN : 1];
+    RopeWith with;
     if constexpr (ROPE > 0) {
+        with = rope_with(rope, rl, tid % L, rope.k_norm);
 #pragma unroll
         for (int i = 0; i < RN; i++) {
-            const int e = tid + 256 * i, r = e / L;
-            kx[i] = rope_load(k + (row0 + (r < rows ? r : 0)) * ldk + (int64_t)h * HD, rope_lane<HD>(rope, e % L));
+            const int r = (tid + 256 * i) / L;
+            kx[i] = rope_load(k + (row0 + (r < rows ? r : 0)) * ldk + (int64_t)h * HD, rl);
         }
     }
 #pragma unroll
@@ -194,11 +207,10 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRo
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < RN; i++) {
-            const int e = tid + 256 * i, r = e / L, p = e % L;
+            const int r = (tid + 256 * i) / L;
             if (r >= ROWS) continue;
-            const RopeLane l = rope_lane<HD>(rope, p);
-            const Cols8 y = rope_apply<HD>(rope, l, rope_turn(rope, l, p, s_pos[r]), kx[i], rope.k_norm);
-            if (l.live) rope_store(s_k + r * KROW, l, y);
+            const Cols8 y = rope_apply<HD>(rope, rl, with, rope_turn(rl, with, s_pos[r]), kx[i]);
+            if (rl.live) rope_store(s_k + r * KROW, rl, y);
         }
         __syncthreads();
 #pragma unroll

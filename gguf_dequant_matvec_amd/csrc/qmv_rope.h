@@ -79,20 +79,6 @@ __device__ __forceinline__ void cos_sin(int pos, double freq, float &c, float &s
     s = k & 2 ? -s : s;
 }
 
-// The four rotations of a lane at one position.
-struct Turn {
-    float c[4], s[4];
-};
-__device__ __forceinline__ Turn rope_turn(const RopeArgs &a, const RopeLane &l, int p, int pos) {
-    Turn t;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        t.c[j] = 1.f, t.s[j] = 0.f;
-        if (l.turns) cos_sin(pos, a.freq[4 * p + j], t.c[j], t.s[j]);
-    }
-    return t;
-}
-
 struct Cols8 {
     float4 a, b;  // columns first .. first + 3 and second .. second + 3
 };
@@ -107,11 +93,39 @@ __device__ __forceinline__ void rope_store(float *row, const RopeLane &l, const 
     __builtin_memcpy(row + l.second, &x.b, 16);
 }
 
-// x normed by w (if there is one) and turned.  All lanes of a row take part.
+// What a lane needs besides its row: loaded before anything is waited for.
+struct RopeWith {
+    double freq[4];  // of its four pairs
+    Cols8 norm;
+    bool normed;
+};
+__device__ __forceinline__ RopeWith rope_with(const RopeArgs &a, const RopeLane &l, int p, const float *w) {
+    RopeWith r;
+#pragma unroll
+    for (int j = 0; j < 4; j++) r.freq[j] = l.turns ? a.freq[4 * p + j] : 0.;
+    r.normed = w != nullptr;
+    if (w) r.norm = rope_load(w, l);
+    return r;
+}
+
+// The four rotations of a lane at one position.
+struct Turn {
+    float c[4], s[4];
+};
+__device__ __forceinline__ Turn rope_turn(const RopeLane &l, const RopeWith &with, int pos) {
+    Turn t;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        t.c[j] = 1.f, t.s[j] = 0.f;
+        if (l.turns) cos_sin(pos, with.freq[j], t.c[j], t.s[j]);
+    }
+    return t;
+}
+
+// x normed (if it is to be) and turned.  All lanes of a row take part.
 template <int HD>
-__device__ __forceinline__ Cols8 rope_apply(const RopeArgs &a, const RopeLane &l, const Turn &t, Cols8 x,
-                                            const float *w) {
-    if (w) {
+__device__ __forceinline__ Cols8 rope_apply(const RopeArgs &a, const RopeLane &l, const RopeWith &with, const Turn &t, Cols8 x) {
+    if (with.normed) {
         float ss = x.a.x * x.a.x;
         ss = fmaf(x.a.y, x.a.y, ss), ss = fmaf(x.a.z, x.a.z, ss), ss = fmaf(x.a.w, x.a.w, ss);
         ss = fmaf(x.b.x, x.b.x, ss), ss = fmaf(x.b.y, x.b.y, ss), ss = fmaf(x.b.z, x.b.z, ss), ss = fmaf(x.b.w, x.b.w, ss);
@@ -119,7 +133,7 @@ __device__ __forceinline__ Cols8 rope_apply(const RopeArgs &a, const RopeLane &l
 #pragma unroll
         for (int off = kRopeLanes<HD> / 2; off; off >>= 1) ss += __shfl_xor(ss, off);
         const float inv = 1.f / sqrtf(ss * (1.f / HD) + a.eps);
-        const Cols8 n = rope_load(w, l);
+        const Cols8 &n = with.norm;
         x.a.x *= inv * n.a.x, x.a.y *= inv * n.a.y, x.a.z *= inv * n.a.z, x.a.w *= inv * n.a.w;
         x.b.x *= inv * n.b.x, x.b.y *= inv * n.b.y, x.b.z *= inv * n.b.z, x.b.w *= inv * n.b.w;
     }
@@ -140,7 +154,7 @@ __device__ __forceinline__ Cols8 rope_apply(const RopeArgs &a, const RopeLane &l
 }
 
 // Heads h0 .. h0 + HB - 1 of one row, by the row's lanes: all of them are read
-// first, while the row's position is still looked up.  A lane writes only what it
+// first.  A lane writes only what it
 // has read, and a norm's sum comes before the row is written, so rows may be
 // turned in place.
 template <int HD, int HB>
@@ -152,13 +166,13 @@ struct RopeHeads {
 #pragma unroll
         for (int i = 0; i < HB; i++) v[i] = rope_load(in + (int64_t)(h0 + i < x.heads ? h0 + i : h0) * HD, l);
     }
-    __device__ __forceinline__ void finish(const RopeArgs &a, const HeadRows &x, const float *w, const RopeLane &l,
-                                           int64_t row, int pos, int p, int h0) const {
+    __device__ __forceinline__ void finish(const RopeArgs &a, const HeadRows &x, const RopeLane &l, const RopeWith &with,
+                                           int64_t row, int pos, int h0) const {
         float *out = x.out + row * x.ld_out;
-        const Turn t = rope_turn(a, l, p, pos);
+        const Turn t = rope_turn(l, with, pos);
 #pragma unroll
         for (int i = 0; i < HB; i++) {
-            const Cols8 y = rope_apply<HD>(a, l, t, v[i], w);
+            const Cols8 y = rope_apply<HD>(a, l, with, t, v[i]);
             if (h0 + i < x.heads && l.live) rope_store(out + (int64_t)(h0 + i) * HD, l, y);
         }
     }

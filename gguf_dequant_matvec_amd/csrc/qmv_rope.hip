@@ -31,6 +31,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope(RopeArgs a, int64_t n, const
     const HeadRows &x = is_q ? q : k;
     const int h0 = (is_q ? chunk : chunk - q_chunks) * HB;
     const RopeLane l = rope_lane<HD>(a, p);
+    const RopeWith with = rope_with(a, l, p, is_q ? a.q_norm : a.k_norm);
 #pragma unroll
     for (int i = 0; i < kRopeRows<HD>; i += R) {
         const int64_t row = tile * kRopeRows<HD> + i + threadIdx.x / L;
@@ -38,7 +39,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope(RopeArgs a, int64_t n, const
         RopeHeads<HD, HB> heads;
         heads.load(x, l, row, h0);
         const int at = pos[row];
-        if (at >= 0) heads.finish(a, x, is_q ? a.q_norm : a.k_norm, l, row, at, p, h0);
+        if (at >= 0) heads.finish(a, x, l, with, row, at, h0);
     }
 }
 
