@@ -429,7 +429,12 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD == 64 ? 3 : 2) void attn_pr
             // us for 4096 tokens; 64 columns lose 1%).
             if constexpr (HD >= 128) __builtin_amdgcn_s_setprio(1);
             // V's operands fly during the softmax where there are registers for them
-            constexpr int EARLY = HD == 256 ? 0 : TYPE == kKvF16 ? 2 : HD == 64 && TYPE == kKvBF16 ? 1 : 0;
+            // (4 bits, 4096 tokens, none early and as here: 64 columns 196 -> 191 us, 96
+            // 174 -> 167, 128 323 -> 322)
+            constexpr int EARLY = HD == 256                                          ? 0
+                                  : TYPE == kKvF16 || (TYPE == kKvQ4 && HD < 128)    ? 2
+                                  : TYPE == kKvQ4 || (HD == 64 && TYPE == kKvBF16)   ? 1
+                                                                                     : 0;
             Vec vx[2][DT];
             const uint8_t *vp = buf + Lds<HD>::kV + 2 * half * HD * 32 + vslot(col, hh) * 16;
             auto read_v = [&](int u) {
