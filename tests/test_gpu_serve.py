@@ -268,6 +268,22 @@ def test_decode_q4_ragged(hd, kv, heads, n, window, sinks):
     decode(c, n, heads, window=window, sinks=sinks, with_acc=n in (3, 5))
 
 
+EVERY = [200, 0, 5200, 33, 64, 700] + [(53 * i) % 130 for i in range(34)]
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128, 256])
+@pytest.mark.parametrize("rows", [3, 4, 5, 8, 9, 16, 20])
+@pytest.mark.parametrize("shape", ["short", "split", "ranges"])
+def test_decode_q4_every_kernel(hd, rows, shape):
+    """Each way a call is cut (eight waves, pieces of one sequence, even ranges) with each packing of rows
+    into the operand's columns, with and without weights."""
+    n, group = (rows, 1) if rows <= 16 else (10, 2)
+    lens, kv, cap = {"short": ([70, 300], 2, 5), "split": ([4100], 1, 70), "ranges": (EVERY, 8, 82)}[shape]
+    c, _ = make4(kv, hd, 64, lens, 81, cap_pages=cap)
+    for with_acc in (False, True):
+        decode(c, n, kv * group, with_acc=with_acc)
+
+
 def test_decode_q4_holes():
     c, _ = make4(1, 64, 16, [300, 300, 40], 25)
     c.table[0, 2:14] = -1
@@ -421,6 +437,58 @@ def test_evict_q4(hd, kv, page, keep, first, recent):
                 v1[at[1] // 16, :, PLACE[at[1] % 16]] = v0[src[1] // 16, :, PLACE[src[1] % 16]]
     assert host(len_out).tolist() == [min(x, keep) for x in lens]
     assert np.array_equal(d.pool(), c.pool)
+
+
+def test_q4_captured():
+    """Append, decode, prompt and read captured once; replays follow lengths and pages changed in place."""
+    kv, hd, page, heads = 2, 128, 16, 8
+    c, rng = make4(kv, hd, page, [200, 90], 91, cap_pages=16)
+    d = Dev(c)
+    k, v, x = (torch.zeros(2, w, device="cuda") for w in (kv * hd, kv * hd, heads * hd))
+    ko, vo, out = torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(x)
+    ws = workspace(q.qmv_attn_decode_workspace(d.h, 1, heads, c.cap))
+    pout = torch.zeros(2, heads * hd, device="cuda")
+    pws = workspace(q.qmv_attn_prefill_workspace(d.h, 2, heads, c.cap))
+
+    def step():
+        q.qmv_kv_append(d.h, 2, k, v)
+        q.qmv_attn_decode(d.h, 1, heads, x, hd ** -0.5, out, c.cap, workspace=ws)
+        q.qmv_attn_prefill(d.h, 2, heads, x, hd ** -0.5, pout, c.cap, workspace=pws)
+        q.qmv_kv_read(d.h, 2, ko, vo)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for rep in range(4):
+        lens = np.array([[200, 90], [201, 1], [17, 256], [0, 33]][rep], np.int32)
+        d.lens.copy_(dev(lens))
+        c.seq_len[:] = lens
+        kh, vh, xh = (rng.standard_normal(tuple(t.shape), dtype=np.float32) for t in (k, v, x))
+        c.pool[:] = d.pool()
+        for t, h in ((k, kh), (v, vh), (x, xh)):
+            t.copy_(dev(h))
+        g.replay()
+        torch.cuda.synchronize()
+        c.append([0, 1, 2], kh.reshape(2, kv, hd), vh.reshape(2, kv, hd))
+        assert np.array_equal(d.pool(), c.pool), rep
+        want, tol, _, _ = ref.attention(c, [0, 1, 2], xh.reshape(2, heads, hd), hd ** -0.5, c.cap)
+        # (positions behind the first lengths hold NaN scales: a longer one sees them, and is NaN)
+        nan = np.isnan(want)
+        assert nan.any() == (rep == 2)
+        for got, what in ((out, "decode"), (pout, "prompt")):
+            got = host(got).reshape(want.shape)
+            assert np.isnan(got[nan]).all()
+            close(np.where(nan, 0, got), np.where(nan, 0, want), np.where(nan, 1, tol), f"replay {rep}, {what}")
+        eager = [t.clone() for t in (out, pout, ko, vo)]
+        step()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(host(a), host(b), equal_nan=True) for a, b in zip(eager, (out, pout, ko, vo)))
 
 
 # ---- norms and rotation -----------------------------------------------------------
