@@ -299,8 +299,8 @@ __device__ __forceinline__ Range find_range(const AttnArgs &a, int p, int lane) 
 }
 
 // 4-bit rows take more instructions a byte than others, so that more waves are
-// wanted; the operands of their queries, which every chunk needs once and in the
-// same order, lie in LDS, where each lane finds its own, and not in registers.
+// wanted; the operands of their queries lie in LDS and not in registers, and each
+// wave makes one step's of them for all four.
 constexpr bool queries_in_lds(int type, int hd, int rt, int nw) {
     return type == kKvQ4 && hd <= 128 && rt == 1 && nw == 4;
 }
@@ -346,7 +346,9 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
     // with two workgroups a unit: 116 against 113).
     constexpr bool NT = RT == 1 && HD <= 128;
     constexpr bool QL = queries_in_lds(TYPE, HD, RT, NW);
-    __shared__ U128 s_q[QL ? NW : 1][QL ? KS * NP : 1][QL ? 64 : 1];
+    __shared__ U128 s_q[QL ? KS * NP : 1][QL ? 64 : 1];
+    __shared__ float s_big[QL ? NW : 1][16];
+    static_assert(!QL || KS <= NW, "a wave for every step");
     __shared__ __align__(16) uint32_t s_d4[TYPE == kKvQ4 ? NW : 1][4][TYPE == kKvQ4 ? HD / 4 : 1];  // scales of a chunk's V
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.y / a.tiles, tile = blockIdx.y % a.tiles;
@@ -431,7 +433,8 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
             for (int t = 0; t < DT; t++) o[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 
-        if (begin + wave < end) {
+        // (with queries in LDS the waves without a chunk make some of them, and read page 0)
+        if (QL || begin + wave < end) {
             int i = begin + wave;
             int kentry = entry_of(i, m >> 2), ventry = entry_of(i, g);
             const int kpage = page_of(i, m >> 2, kentry), vpage = page_of(i, g, ventry);
@@ -453,10 +456,12 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                 const int j = live ? rr / a.group : 0, hg = live ? rr % a.group : 0;
                 pos[rt] = live ? len - n + j : -1;
                 const float *qp = a.q + ((int64_t)s * n + j) * a.ldq + (int64_t)(h * a.group + hg) * HD;
-                float f[KS][8];
+                constexpr int KP = QL ? 1 : KS;  // steps that the wave makes
+                float f[KP][8];
                 float big = 0.f;
 #pragma unroll
-                for (int t = 0; t < KS; t++) {
+                for (int tp = 0; tp < KP; tp++) {
+                    const int t = QL ? (wave < KS ? wave : 0) : tp;
                     float w[8];
                     if constexpr (TYPE == kKvQ4) {
                         q4_cols(qp, KS * g + t, w);
@@ -467,8 +472,8 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                     }
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        f[t][e] = live ? w[e] * a.q_sign : 0.f;
-                        big = fmaxf(big, fabsf(f[t][e]));
+                        f[tp][e] = live ? w[e] * a.q_sign : 0.f;
+                        big = fmaxf(big, fabsf(f[tp][e]));
                     }
                 }
                 // f16 pieces: scale the row by a power of two so that its largest
@@ -477,6 +482,12 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                 if constexpr (TYPE != kKvBF16) {
                     big = fmaxf(big, __shfl_xor(big, 16));
                     big = fmaxf(big, __shfl_xor(big, 32));
+                    if constexpr (QL) {
+                        if (g == 0) s_big[wave][m] = big;
+                        lds_barrier();
+#pragma unroll
+                        for (int w = 0; w < NW; w++) big = fmaxf(big, s_big[w][m]);
+                    }
                     if (big > 0.f && big < __builtin_inff()) {
                         sh = 15 - __builtin_amdgcn_frexp_expf(big);
                         sh = sh > 100 ? 100 : sh;
@@ -484,25 +495,28 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                 }
                 qscale[rt] = logit_factor(a.scale_log2, sh);
 #pragma unroll
-                for (int t = 0; t < KS; t++) {
+                for (int t = 0; t < KP; t++) {
 #pragma unroll
                     for (int e = 0; e < 8; e++) f[t][e] = ldexpf(f[t][e], sh);
                     if constexpr (PACK > 0) {
                         U128 both[Op::kPieces];
                         split8<Op>(f[t], both);
 #pragma unroll
-                        for (int j = 0; j < 4; j++) qf[0][QL ? 0 : t][0].w[j] = pack_piece<PACK>(m) ? both[1].w[j] : both[0].w[j];
+                        for (int j = 0; j < 4; j++) qf[0][t][0].w[j] = pack_piece<PACK>(m) ? both[1].w[j] : both[0].w[j];
                     } else {
-                        split8<Op>(f[t], qf[rt][QL ? 0 : t]);
+                        split8<Op>(f[t], qf[rt][t]);
                     }
-                    if constexpr (QL) {
+                }
+                if constexpr (QL) {
+                    if (wave < KS) {
 #pragma unroll
-                        for (int p = 0; p < NP; p++) s_q[wave][t * NP + p][lane] = qf[0][0][p];
+                        for (int p = 0; p < NP; p++) s_q[wave * NP + p][lane] = qf[0][0][p];
                     }
+                    lds_barrier();
                 }
             }
 
-            for (;;) {
+            if (!QL || i < end) for (;;) {
                 const bool more = i + NW < end;
                 const int kentry2 = entry_of(i + 2 * NW, m >> 2), ventry2 = entry_of(i + 2 * NW, g);
                 f32x4 sacc[RT][2 * SUB];
@@ -514,7 +528,7 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                 for (int t = 0; t < KS; t++) {
                     if constexpr (QL) {
 #pragma unroll
-                        for (int p = 0; p < NP; p++) qf[0][0][p] = s_q[wave][t * NP + p][lane];
+                        for (int p = 0; p < NP; p++) qf[0][0][p] = s_q[t * NP + p][lane];
                     }
 #pragma unroll
                     for (int ub = 0; ub < 2 * SUB; ub++) {

@@ -137,6 +137,14 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
+// A workgroup's barrier for what is in LDS alone: what is on its way from or to
+// memory is not waited for (__syncthreads does, about 1 us for a store).
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Order-preserving map of an f32 to u32 (larger float -> larger key).
 __device__ __forceinline__ uint32_t float_key(float v) {
     uint32_t b = __builtin_bit_cast(uint32_t, v);

@@ -42,14 +42,6 @@ __device__ __forceinline__ uint32_t wave_upto(uint32_t x) {
     return x;
 }
 
-// A barrier for what is in LDS alone.  Nothing that the workgroup has written to
-// memory is read again in its launch, and waiting for such writes costs about 1 us.
-__device__ __forceinline__ void lds_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 struct Sums {
     uint32_t before, all;
 };
@@ -59,7 +51,7 @@ __device__ __forceinline__ void block_sums(uint32_t x, uint32_t y, uint32_t (*tm
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t ux = wave_upto(x), uy = wave_upto(y);
     if (lane == 63) tmp[0][wave] = ux, tmp[1][wave] = uy;
-    lds_barrier();
+    lds_barrier();  // (nothing that a launch writes to memory is read again in it)
     sx = sy = Sums{0, 0};
 #pragma unroll
     for (int w = 0; w < W; w++) {
