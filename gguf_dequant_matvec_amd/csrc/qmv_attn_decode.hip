@@ -752,90 +752,119 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
             }
         }
 
+        // where row rr's sums go: to the outputs, divided, or, where the sequence has
+        // other pieces, as a piece, with its maximum and sum (written by `first`)
+        const bool direct = opens && closes && !ACC;
+        auto row_of = [&](int rr, bool first, float mx, float l, float &mul) {
+            mul = direct ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // a row that sees nothing: zeros
+            const int64_t row = (int64_t)(direct ? s : slot) * n + rr / a.group;
+            const int64_t at = row * a.n_heads + h * a.group + rr % a.group;
+            if (!direct && first) a.part_ml[at] = make_float2(mx, l);
+            return (direct ? a.out : a.part_o) + at * HD;
+        };
+        if (RANGES && blockIdx.y == 0 && tid == 0) {
+            if (opens) a.share[s].x = slot;
+            if (closes) a.share[s].y = slot;
+        }
         if constexpr (PACK > 0) {
+            // join the waves: their few rows' sums side by side in LDS, four columns a
+            // thread after one barrier
+            constexpr int ROWS = PACK == 4 ? 4 : 8, RS = HD / 4 + 1;
+            __shared__ float s_m[NW][ROWS], s_l[NW][ROWS];
+            __shared__ f32x4 s_o[NW][ROWS][RS];
             if constexpr (PACK == 4) lrun[0] += dpp_f32<kDppRowRor8>(lrun[0]);
+            lrun[0] += __shfl_xor(lrun[0], 16);
+            lrun[0] += __shfl_xor(lrun[0], 32);
+            if (mrun[0] != kNoMax) mrun[0] *= qscale[0];
 #pragma unroll
-            for (int t = 0; t < DT; t++)
+            for (int t = 0; t < DT; t++) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     o[0][t][e] = pack_add<PACK>(o[0][t][e]);
                     if constexpr (PACK == 4) o[0][t][e] += dpp_f32<kDppRowRor8>(o[0][t][e]);
                 }
-        }
-        // join the waves: a common maximum, then the partial sums two by two
-        __shared__ float s_m[NW][RT * 16], s_l[NW][RT * 16];
-        __shared__ f32x4 s_o[2][RT * DT * 64];
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            lrun[rt] += __shfl_xor(lrun[rt], 16);
-            lrun[rt] += __shfl_xor(lrun[rt], 32);
-            if (mrun[rt] != kNoMax) mrun[rt] *= qscale[rt];
-            if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int rt = 0; rt < RT; rt++) {
-            float mm = kNoMax;
-            for (int w = 0; w < NW; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
-            // (a NaN maximum cannot be: fmaxf drops NaN; a NaN sum stays)
-            const float r = exp2_fast(mrun[rt] - mm);
-            mrun[rt] = mm;
-            lrun[rt] *= r;
-            if constexpr (TYPE == kKvI8) {
-                lrun[rt] *= a.unit;
-                const float back = vback * a.unit;  // a power of two (with r it might be subnormal and lose bits)
-#pragma unroll
-                for (int t = 0; t < DT; t++) o[rt][t] *= back;
+                if (m < ROWS) s_o[wave][m][4 * t + g] = o[0][t];
             }
-            if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
+            if (m < ROWS && g == 0) s_m[wave][m] = mrun[0], s_l[wave][m] = lrun[0];
+            lds_barrier();
+            for (int e = tid; e < nrows * (HD / 4); e += NW * 64) {
+                const int rr = e / (HD / 4), d = e % (HD / 4);
+                float mm = kNoMax, l = 0.f, mul;
 #pragma unroll
-            for (int t = 0; t < DT; t++) o[rt][t] *= r;
-        }
-        for (int from = NW - 2; from >= 0; from -= 2) {
-            // waves from, from + 1 add to the two before them; last 1 to 0
-            const int w0 = from > 0 ? from : 1, n_from = from > 0 ? 2 : 1, to = from > 0 ? from - 2 : 0;
-            if (wave >= w0 && wave < w0 + n_from) {
+                for (int w = 0; w < NW; w++) mm = fmaxf(mm, s_m[w][rr]);
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                    for (int t = 0; t < DT; t++) s_o[wave - w0][(rt * DT + t) * 64 + lane] = o[rt][t];
+                for (int w = 0; w < NW; w++) {
+                    const float r = exp2_fast(s_m[w][rr] - mm);
+                    l += s_l[w][rr] * r;
+                    v += s_o[w][rr][d] * r;
+                }
+                float *dst = row_of(rr, d == 0, mm, l, mul);
+                v *= mul;
+                __builtin_memcpy(dst + 4 * d, &v, 16);
             }
-            __syncthreads();
-            if (wave >= to && wave < to + n_from) {
-#pragma unroll
-                for (int rt = 0; rt < RT; rt++)
-#pragma unroll
-                    for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave - to][(rt * DT + t) * 64 + lane];
-            }
-            __syncthreads();
-        }
-        const bool direct = opens && closes && !ACC;
-        if (wave == 0) {
-            if (RANGES && blockIdx.y == 0 && lane == 0) {
-                if (opens) a.share[s].x = slot;
-                if (closes) a.share[s].y = slot;
-            }
+        } else {
+            // join the waves: a common maximum, then the partial sums two by two
+            __shared__ float s_m[NW][RT * 16], s_l[NW][RT * 16];
+            __shared__ f32x4 s_o[2][RT * DT * 64];
 #pragma unroll
             for (int rt = 0; rt < RT; rt++) {
-                const int rr = r0 + rt * 16 + m;
-                if (rr >= nrows) continue;
-                float l = 0.f;
-                for (int w = 0; w < NW; w++) l += s_l[w][rt * 16 + m];
-                float *dst;
-                float mul = 1.f;
-                if (direct) {
-                    const int j = rr / a.group, hg = rr % a.group;
-                    dst = a.out + (((int64_t)s * n + j) * a.n_heads + h * a.group + hg) * HD;
-                    mul = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing: zeros
-                } else {
-                    const int64_t at = ((int64_t)slot * n + rr / a.group) * a.n_heads + h * a.group + rr % a.group;
-                    if (g == 0) a.part_ml[at] = make_float2(mrun[rt], l);
-                    dst = a.part_o + at * HD;
-                }
+                lrun[rt] += __shfl_xor(lrun[rt], 16);
+                lrun[rt] += __shfl_xor(lrun[rt], 32);
+                if (mrun[rt] != kNoMax) mrun[rt] *= qscale[rt];
+                if (g == 0) s_m[wave][rt * 16 + m] = mrun[rt];
+            }
+            __syncthreads();
 #pragma unroll
-                for (int t = 0; t < DT; t++) {
-                    const f32x4 v = o[rt][t] * mul;
-                    __builtin_memcpy(dst + 16 * t + 4 * g, &v, 16);
+            for (int rt = 0; rt < RT; rt++) {
+                float mm = kNoMax;
+                for (int w = 0; w < NW; w++) mm = fmaxf(mm, s_m[w][rt * 16 + m]);
+                // (a NaN maximum cannot be: fmaxf drops NaN; a NaN sum stays)
+                const float r = exp2_fast(mrun[rt] - mm);
+                mrun[rt] = mm;
+                lrun[rt] *= r;
+                if constexpr (TYPE == kKvI8) {
+                    lrun[rt] *= a.unit;
+                    const float back = vback * a.unit;  // a power of two (with r it might be subnormal and lose bits)
+#pragma unroll
+                    for (int t = 0; t < DT; t++) o[rt][t] *= back;
+                }
+                if (g == 0) s_l[wave][rt * 16 + m] = lrun[rt];
+#pragma unroll
+                for (int t = 0; t < DT; t++) o[rt][t] *= r;
+            }
+            for (int from = NW - 2; from >= 0; from -= 2) {
+                // waves from, from + 1 add to the two before them; last 1 to 0
+                const int w0 = from > 0 ? from : 1, n_from = from > 0 ? 2 : 1, to = from > 0 ? from - 2 : 0;
+                if (wave >= w0 && wave < w0 + n_from) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                        for (int t = 0; t < DT; t++) s_o[wave - w0][(rt * DT + t) * 64 + lane] = o[rt][t];
+                }
+                __syncthreads();
+                if (wave >= to && wave < to + n_from) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; rt++)
+#pragma unroll
+                        for (int t = 0; t < DT; t++) o[rt][t] += s_o[wave - to][(rt * DT + t) * 64 + lane];
+                }
+                __syncthreads();
+            }
+            if (wave == 0) {
+#pragma unroll
+                for (int rt = 0; rt < RT; rt++) {
+                    const int rr = r0 + rt * 16 + m;
+                    if (rr >= nrows) continue;
+                    float l = 0.f;
+                    for (int w = 0; w < NW; w++) l += s_l[w][rt * 16 + m];
+                    float mul;
+                    float *dst = row_of(rr, g == 0, mrun[rt], l, mul);
+#pragma unroll
+                    for (int t = 0; t < DT; t++) {
+                        const f32x4 v = o[rt][t] * mul;
+                        __builtin_memcpy(dst + 16 * t + 4 * g, &v, 16);
+                    }
                 }
             }
         }
