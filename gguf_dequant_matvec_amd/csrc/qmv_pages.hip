@@ -26,7 +26,7 @@ constexpr int kItems = 4096 / T;
 // 3.7 to reserve, with 1024 threads 3.2 and 4.9), many: 1024 (10500 pages of 96
 // sequences: 8.9 and 9.3 us, with 256 threads 20 and 19).
 constexpr int kSmall = 256, kLarge = 1024;
-// Sums stop here, above any row or page count that a call can be given.
+// Sums stop here: no call can be given more rows, or give back more pages.
 constexpr uint32_t kSat = 1u << 30;
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return a + b < kSat ? a + b : kSat; }

@@ -154,9 +154,8 @@ __device__ __forceinline__ Cols8 rope_apply(const RopeArgs &a, const RopeLane &l
 }
 
 // Heads h0 .. h0 + HB - 1 of one row, by the row's lanes: all of them are read
-// first.  A lane writes only what it
-// has read, and a norm's sum comes before the row is written, so rows may be
-// turned in place.
+// first.  A lane writes only what it has read, and a norm's sum comes before the
+// row is written, so rows may be turned in place.
 template <int HD, int HB>
 struct RopeHeads {
     Cols8 v[HB];

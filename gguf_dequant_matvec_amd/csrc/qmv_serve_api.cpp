@@ -116,6 +116,7 @@ qmv_status qmv_kv_release(const qmv_kv_cache *cache, const int32_t *new_len, int
     KvArgs c;
     qmv_status st = check_cache(cache, c);
     if (st != QMV_OK) return st;
+    if (c.n_seq * c.table_ld > 1ll << 30) return QMV_ESHAPE;  // the sums of pages end there
     if (!new_len || !free_pages || !free_count) return QMV_EINVAL;
     if (!aligned(new_len, 4) || !aligned(free_pages, 4) || !aligned(free_count, 4)) return QMV_EALIGN;
     return from_hip(launch_kv_release(c, const_cast<int32_t *>(c.table), const_cast<int32_t *>(c.seq_len), new_len,

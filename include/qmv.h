@@ -522,7 +522,8 @@ qmv_status qmv_kv_append_rope(const qmv_kv_cache *cache, const qmv_qk_rope *rope
  * entries behind the page of its last token -1, and the pages that they named
  * (holes none) go back on the stack, so that the first of the first sequence is
  * on top: reserving the same again enters the same pages.  The stack holds at
- * most n_pages; what would go beyond is lost.  One launch. */
+ * most n_pages; what would go beyond is lost.  n_seq * table_ld <= 2^30.  One
+ * launch. */
 qmv_status qmv_kv_reserve(const qmv_kv_cache *cache, const int32_t *add, const int32_t *free_pages,
                           int32_t *free_count, int64_t n, int32_t *granted, int32_t *start, int32_t *pos,
                           int64_t *slot, hipStream_t stream);

@@ -130,6 +130,9 @@ def test_pages_refusals():
     for kw, want in ((dict(new_len=0), "QMV_EINVAL"), (dict(free=0), "QMV_EINVAL"), (dict(count=0), "QMV_EINVAL"),
                      (dict(new_len=A16 + 2), "QMV_EALIGN"), (dict(free=A16 + 1), "QMV_EALIGN")):
         assert status_of(release, c, **kw) == want, kw
+    # more table entries than the sums of pages count (n_seq table_ld above 2^30; then the other checks go on)
+    assert status_of(release, cache(n_seq=17, table_ld=1 << 26)) == "QMV_ESHAPE"
+    assert status_of(release, cache(n_seq=16, table_ld=1 << 26), new_len=0) == "QMV_EINVAL"
 
 
 def test_binding_checks():
