@@ -216,6 +216,14 @@ __device__ __forceinline__ void q4_cols(const float *row, int D, float *f) {
     f[0] = x.x, f[1] = x.z, f[2] = y.x, f[3] = y.z, f[4] = x.y, f[5] = x.w, f[6] = y.y, f[7] = y.w;
 }
 
+// Bits 0 and 16: which of two scales make values that are not finite.  That is
+// those from 2730 (0x6955) on, infinities and NaN among them: 24 times that is
+// past f16, and so the addend, and with it every value of the block, infinite or
+// NaN whatever the code.  (The addition carries into the sign bit from there on.)
+__device__ __forceinline__ uint32_t q4_not_finite(uint32_t d2) {
+    return (((d2 & 0x7FFF7FFFu) + (0x8000u - 0x6955u) * 0x10001u) & 0x80008000u) >> 15;
+}
+
 // The chunks of `ck` positions that hold every position some query with
 // pmin <= p <= pmax sees: first those of the sinks, then those of the window.
 struct Chunks {

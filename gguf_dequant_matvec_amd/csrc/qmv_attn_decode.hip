@@ -659,11 +659,11 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                         for (int u = 0; u < SUB; u++) split8<Op>(x + 8 * u, pf[rt][u]);
                     }
                 }
-                if constexpr (TYPE == kKvQ4) {  // a 4-bit value is not finite where its block's scale is not
+                if constexpr (TYPE == kKvQ4) {  // a 4-bit value is not finite where its block's scale is too large
                     if (!whole) {
                         uint32_t bad = 0;
 #pragma unroll
-                        for (int j = 0; j < VTile<TYPE, HD>::W; j++) bad |= not_finite<Op>(vt.d[j]);
+                        for (int j = 0; j < VTile<TYPE, HD>::W; j++) bad |= q4_not_finite(vt.d[j]);
                         if (__any(bad != 0)) {
                             vt.share(s_d4[wave][g], m);
                             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -676,7 +676,7 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                                 for (int b = 0; b < HD / 32; b++) {
                                     U128 marks = *reinterpret_cast<const U128 *>(&s_d4[wave][g][8 * b + 4 * u]);
 #pragma unroll
-                                    for (int j = 0; j < 4; j++) marks.w[j] = not_finite<Op>(marks.w[j]) * kHuge;
+                                    for (int j = 0; j < 4; j++) marks.w[j] = q4_not_finite(marks.w[j]) * kHuge;
 #pragma unroll
                                     for (int rt = 0; rt < RT; rt++) {
                                         o[rt][2 * b] = OpBF16::mfma16(as_vec<bf16x8>(marks), as_vec<bf16x8>(seen[rt]), o[rt][2 * b]);
@@ -686,7 +686,7 @@ __global__ __launch_bounds__(NW * 64, (RANGES && RT == 1) || queries_in_lds(TYPE
                             }
                             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-                            for (int j = 0; j < VTile<TYPE, HD>::W; j++) vt.d[j] &= ~(not_finite<Op>(vt.d[j]) * 0xFFFFu);
+                            for (int j = 0; j < VTile<TYPE, HD>::W; j++) vt.d[j] &= ~(q4_not_finite(vt.d[j]) * 0xFFFFu);
                         }
                     }
                     vt.share(s_d4[wave][g], m);

@@ -138,7 +138,7 @@ struct Stage {
                         uint32_t bits = 0;
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const uint32_t bad = not_finite<OpF16>(sc4[j]);
+                            const uint32_t bad = q4_not_finite(sc4[j]);
                             sc4[j] &= ~(bad * 0xFFFFu);
                             bits |= ((bad & 1) | (bad >> 15)) << (2 * j);
                         }

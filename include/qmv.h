@@ -359,8 +359,10 @@ qmv_status qmv_quantize(qmv_type t, const float *w, int64_t M, int64_t K, void *
  *     the f32 quotient), within -8 .. 7, 0 if d is 0; value = d * code.  Values
  *     beyond 7 * 2720 (8 * 2720 where d's sign is the other) and infinities
  *     saturate; a NaN makes its block's scale, and so the block, NaN.  Scales
- *     that a caller writes into pages have to keep the two limits (8 bits of
- *     significand, 2720), or values are rounded.
+ *     that a caller writes into pages have to keep the two limits: with more
+ *     than 8 bits of significand attention rounds the values to f16; a scale
+ *     past 2728 it takes for one that is not finite (qmv_kv_read gives scale *
+ *     code as it is).
  *
  * A page holds, for each key-value head in turn, the bytes
  *   K  [page_size][head_dim]            rows of the positions,

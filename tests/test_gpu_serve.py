@@ -338,6 +338,113 @@ def test_q4_hidden_nan(hd, what):
             close(got[blind:][..., rest], clean[blind:][..., rest], tol[blind:][..., rest], f"{call} other columns")
 
 
+# the f16 scales whose 24-fold is infinite, of which the readers make infinite or NaN values
+LARGE = np.arange(0x6955, 0x7C00, dtype=np.uint16)
+
+
+def leave_scales(c, rng, hidden=lambda s, p: False):
+    """Any codes and finite scales past what the writer gives in every slot that no row sees: behind the
+    lengths, in pages of no sequence (page 0 among them, which is read in place of a hole) and where
+    hidden(s, positions) says so."""
+    old = np.flatnonzero(c.table.reshape(-1) == 0)
+    if old.size:                                  # page 0 into no sequence's table
+        spare = next(p for p in range(c.n_pages) if p not in set(c.table.reshape(-1).tolist()))
+        c.pool[[0, spare]] = c.pool[[spare, 0]]
+        c.table.reshape(-1)[old] = spare
+    owner = {int(c.table[s, j]): (s, j) for s in range(c.table.shape[0]) for j in range(c.table.shape[1])}
+    for pg in range(c.n_pages):
+        s, j = owner.get(pg, (None, 0))
+        at = np.arange(c.page)
+        if s is not None:
+            at = at[(j * c.page + at >= c.seq_len[s]) | hidden(s, j * c.page + at)]
+        for h in range(c.kv):
+            k, v, ks, vs = c.parts4(pg, h)
+            k[at] = rng.integers(0, 256, (len(at), c.hd // 2))
+            if s is None:
+                v[:] = rng.integers(0, 256, v.shape)
+            for d in (ks.view(np.uint16).T, vs.view(np.uint16)):
+                d[:, at] = rng.choice(LARGE, (c.hd // 32, len(at))) | rng.choice([0, 0x8000], (c.hd // 32, len(at))).astype(np.uint16)
+    assert not (c.table == 0).any()
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128, 256])
+@pytest.mark.parametrize("rows", [1, 4, 6, 9, 20])
+@pytest.mark.parametrize("shape", ["short", "split", "ranges"])
+def test_decode_q4_leftover_scales(hd, rows, shape):
+    """What slots that no row sees hold does not matter: scales that are finite but too large for attention."""
+    n, group = {1: (1, 1), 4: (2, 2), 6: (6, 1), 9: (3, 3), 20: (10, 2)}[rows]
+    lens, kv, cap = {"short": ([70, 301, 0, 1], 2, 5), "split": ([4133], 1, 70), "ranges": (EVERY, 8, 82)}[shape]
+    c, rng = make4(kv, hd, 64, lens, 82, cap_pages=cap)
+    leave_scales(c, rng)
+    for with_acc in (False, True):
+        decode(c, n, kv * group, with_acc=with_acc)
+
+
+@pytest.mark.parametrize("hd", [64, 96, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(33, 0), (100, 21)])
+def test_q4_leftover_scales_outside_windows(hd, window, sinks):
+    """... in holes, and in positions between the sinks and every row's window."""
+    lens, news = [600, 333, 41], [1, 1, 1]
+    for n in (1, 5):
+        c, rng = make4(2, hd, 16, lens, 83)
+        leave_scales(c, rng, lambda s, p: (p >= sinks) & (p <= c.seq_len[s] - n - window))
+        c.table[0, 35] = -1                       # a hole inside the window, another behind it
+        c.table[1, 3] = c.n_pages
+        decode(c, n, 6, window=window, sinks=sinks, with_acc=True)
+        prefill(c, [n] * 3, 6, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("hd,heads,kv,page", [(64, 9, 3, 16), (96, 4, 2, 32), (128, 8, 2, 64), (256, 5, 1, 16)])
+def test_prefill_q4_leftover_scales(hd, heads, kv, page):
+    c, rng = make4(kv, hd, page, [0, 1, 33, 64, 130, 203], 84)
+    leave_scales(c, rng)
+    c.table[5, 64 // page] = -1
+    prefill(c, [0, 1, 33, 20, 130, 97], heads, before=3, after=4)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("bits", [0x6954, 0xE954, 0x6955, 0xE955, 0x7BFF, 0xFBFF])
+def test_q4_scale_too_large(hd, bits):
+    """A V scale past 2728 counts as not finite for the rows that see it, in chunks that all rows see and
+    in others, and changes nothing for other rows and columns; one of 2728 is a scale like others."""
+    n, length, group = 70, 300, 2
+    finite = bits & 0x7FFF < 0x6955
+    for bad in (40, 271, 294, 299):              # seen by all rows; by the last 29, 6, 1
+        c, _ = make4(1, hd, 16, [length], 85)
+        pg, slot = c.where(0, bad)
+        _, _, _, vs = c.parts4(pg, 0)
+        qh = synth.normal(5, synth.T_X, (n, group, hd), 1.5)
+        clean, tol, _, _ = ref.attention(c, [0, n], qh, hd ** -0.5, 304)
+        vs.view(np.uint16)[1, slot] = bits
+        want, wtol, _, _ = ref.attention(c, [0, n], qh, hd ** -0.5, 304)
+        # (24 * 2728 is an f16 value; scale * code, below 2^15 and of more bits than f16 has, is rounded once, to
+        # steps of 16: off by 8, times a weight of at most 1)
+        wtol = wtol + np.where(np.arange(hd) // 32 == 1, 8.0, 0.0)
+        blind = max(0, bad - (length - n))
+        for call, m in (("decode", 2), ("decode", 4), ("decode", 12), ("prefill", n)):
+            d = Dev(c)
+            rows = dev(qh[-m:].reshape(m, -1))
+            out = torch.empty(m, group, hd, device="cuda")
+            if call == "decode":
+                q.qmv_attn_decode(d.h, m, group, rows, hd ** -0.5, out, 304,
+                                  workspace=workspace(q.qmv_attn_decode_workspace(d.h, m, group, 304)))
+            else:
+                q.qmv_attn_prefill(d.h, m, group, rows, hd ** -0.5, out, 304,
+                                   workspace=workspace(q.qmv_attn_prefill_workspace(d.h, m, group, 304)))
+            got = np.full((n, group, hd), np.nan, np.float32)
+            got[n - m:] = host(out)
+            what = f"{call} of {m} {bits:#x} at {bad}"
+            first = max(blind, n - m)
+            if finite:
+                close(got[n - m:], want[n - m:], wtol[n - m:], what)
+                continue
+            if blind > n - m:
+                close(got[n - m:blind], clean[n - m:blind], tol[n - m:blind], what + ", rows that do not see it")
+            assert not np.isfinite(got[first:, :, 32:64]).any(), what
+            rest = np.r_[0:32, 64:hd]
+            close(got[first:][..., rest], clean[first:][..., rest], tol[first:][..., rest], what + ", other columns")
+
+
 @pytest.mark.parametrize("hd,heads,kv,page", [(64, 9, 3, 16), (96, 4, 2, 32), (128, 8, 2, 64), (256, 5, 1, 16), (64, 17, 1, 128)])
 def test_prefill_q4_ragged(hd, heads, kv, page):
     c, _ = make4(kv, hd, page, [0, 1, 33, 64, 130, 200], 31)
