@@ -202,18 +202,30 @@ def _cache_stream(cache, stream, *tensors) -> int:
     """The stream of a call over a cache of tensors, all of whose tensors must
     be on the pages' GPU, the current one: a kernel cannot tell, it would fault.
     Raw addresses are taken as they are."""
-    on = cache.device
+    return _stream_on(cache.device, "the cache", stream, tensors)
+
+
+def _rope_stream(rope, stream, *tensors) -> int:
+    """The same for rows of queries and keys beside a rotation, which may have no
+    tensors itself: then the rows' first one says which GPU it is."""
+    on = rope.device
+    if on is None:
+        on = next((a.get_device() for a in tensors if a is not None and a.__class__ is not int), None)
+    return _stream_on(on, "the rotation" if rope.device is not None else "another", stream, tensors)
+
+
+def _stream_on(on, what, stream, tensors) -> int:
     if on is None:
         return _stream(stream)
     if on < 0:
-        raise ValueError("the cache's tensors are not on a GPU")
+        raise ValueError("the call's tensors are not on a GPU")
     for a in tensors:
         if a is not None and a.__class__ is not int and a.get_device() != on:
-            raise ValueError(f"a tensor on {a.device}, the cache on GPU {on}")
+            raise ValueError(f"a tensor on {a.device}, {what} on GPU {on}")
     if _torch().cuda.current_device() != on:
-        raise ValueError(f"the cache is on GPU {on}, which is not the current one")
+        raise ValueError(f"the call's tensors are on GPU {on}, which is not the current one")
     if stream is not None and not isinstance(stream, int) and stream.device_index != on:
-        raise ValueError(f"a stream of GPU {stream.device_index}, the cache on GPU {on}")
+        raise ValueError(f"a stream of GPU {stream.device_index}, the call's tensors on GPU {on}")
     return _raw_stream_on(on) if stream is None and _raw_stream_on is not None else _stream(stream)
 
 
@@ -557,7 +569,7 @@ def qmv_qk_norm_rope(rope, head_dim, n, pos, n_heads=0, q=None, q_out=None, n_kv
            (("q", q, ldq, n_heads), ("q_out", q_out, ldqo, n_heads), ("k", k, ldk, n_kv_heads),
             ("k_out", k_out, ldko, n_kv_heads))]
     _call("qmv_qk_norm_rope", rope._address, head_dim, n, _ptr(pos), n_heads, _ptr(q), lds[0], _ptr(q_out), lds[1],
-          n_kv_heads, _ptr(k), lds[2], _ptr(k_out), lds[3], _cache_stream(rope, stream, pos, q, q_out, k, k_out))
+          n_kv_heads, _ptr(k), lds[2], _ptr(k_out), lds[3], _rope_stream(rope, stream, pos, q, q_out, k, k_out))
 
 
 def qmv_kv_append_rope(cache, rope, n, n_heads, q, q_out, k, v, start=None, ldq=None, ldqo=None, ldk=None, ldv=None,

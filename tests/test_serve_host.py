@@ -175,6 +175,20 @@ def test_binding_checks():
         release(c, new_len=f(2, dtype=torch.int64))
 
 
+@pytest.mark.parametrize("r", [q.QkRope(None, 0), q.QkRope(0, 0, "adjacent")])
+def test_rows_beside_a_rotation_without_tensors(r):
+    """Neither frequencies nor norms: the rows' own tensors say which GPU the call is for, and that they are
+    on one (a kernel that got host memory would fault)."""
+    f, n = torch.zeros, 2
+    rows = dict(pos=f(n, dtype=torch.int32), n_heads=1, q=f(n, 64), q_out=f(n, 64))
+    for kw in (rows, dict(rows, pos=A16), dict(rows, pos=A16, q=A16),
+               dict(pos=A16, n_kv_heads=1, k=f(n, 64), k_out=B16), dict(pos=A16, n_kv_heads=1, k=A16, k_out=f(n, 64))):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            q.qmv_qk_norm_rope(r, 64, n, **kw)
+    # addresses alone are taken as they are
+    assert status_of(q.qmv_qk_norm_rope, r, 64, n, 0, 1, A16, B16, stream=0) == "QMV_EINVAL"
+
+
 # ---- the references ---------------------------------------------------------
 
 def test_encode4_is_near():
