@@ -31,11 +31,15 @@ ROW_FORMATS = ["Q2K", "Q3K", "Q4K", "Q5K", "Q6K", "Q40", "Q41", "Q50", "Q51", "Q
 ROW_MODES = ["kModeStore", "kModeArgmax", "kModeMoeGateUp", "kModeMoeDown", "kModeSiluUp",
              "kModeShortConv"]
 INST_SRC = "qmv_rows_inst.hip"
-# Bundles of neighbouring loads are off here: with a load's registers changed one
-# by one in a branch (scales that are not finite are cleared), the pass that
-# forms them loses track of the other ones, and a kernel read registers that were
-# in use for something else (-verify-machineinstrs reports it).
-EXTRA = {"qmv_attn_decode.hip": ["-mllvm", "-amdgpu-max-memory-clause=1"]}
+# The compiler checks its own machine code of the attention kernels, and where it
+# finds a fault (a register read that nothing wrote) the build ends.  It has:
+# before 4-bit V scales went through LDS, the pass that bundles neighbouring loads
+# lost track of registers that a branch changes one by one (scales that are not
+# finite are cleared), in two decode kernels of 64 columns with weights.  Decode is
+# still built without such bundles, as a precaution; times are the same.
+VERIFY = ["-mllvm", "-verify-machineinstrs"]
+EXTRA = {"qmv_attn_decode.hip": [*VERIFY, "-mllvm", "-amdgpu-max-memory-clause=1"],
+         "qmv_attn_prefill.hip": VERIFY}
 
 
 def hipcc() -> str:

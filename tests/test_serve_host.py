@@ -189,6 +189,16 @@ def test_rows_beside_a_rotation_without_tensors(r):
     assert status_of(q.qmv_qk_norm_rope, r, 64, n, 0, 1, A16, B16, stream=0) == "QMV_EINVAL"
 
 
+def test_attention_units_are_built_with_the_machine_verifier():
+    """The compiler once made an attention kernel that read registers which nothing had written; built with
+    its own verifier, such a unit ends the build."""
+    from gguf_dequant_matvec_amd import build
+    flags = {os.path.basename(src): extra for src, _, extra in build.units()}
+    for unit in ("qmv_attn_decode.hip", "qmv_attn_prefill.hip"):
+        at = flags[unit].index("-verify-machineinstrs")
+        assert flags[unit][at - 1] == "-mllvm"
+
+
 # ---- the references ---------------------------------------------------------
 
 def test_encode4_is_near():
