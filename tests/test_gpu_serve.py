@@ -927,6 +927,54 @@ def test_serving_steps_in_a_graph(t):
         close(host(p["out"]).reshape(want.shape), want, tol, f"step {rep}")
 
 
+@pytest.mark.parametrize("t", ["q4", "f16"])
+def test_evicted_and_appended_at_the_callers_positions(t):
+    """After an eviction a sequence's lengths are less than its tokens were, and kept keys stay turned by their
+    old positions: the next tokens are turned to their own by qmv_qk_norm_rope and appended as they are."""
+    rng = np.random.default_rng(12)
+    kv, heads, hd, page, n, keep, m = 2, 6, 64, 16, 90, 40, 3
+    per = 8
+    c = (sref.Cache4(kv, hd, page, 2 * per, np.arange(per)[None], [n], fill=0) if t == "q4" else
+         ref.Cache(t, kv, hd, page, 2 * per, np.arange(per)[None], [n], fill=0))
+    d = Dev(c)
+    h, freq, wq, wk, eps = make_rope(hd, hd, "halves", True, rng)
+    x = rng.standard_normal((n, (heads + 2 * kv) * hd), dtype=np.float32)
+    xd, w = dev(x), heads * hd
+    qo = torch.empty(n, w, device="cuda")
+    q.qmv_kv_append_rope(d.h, h, n, heads, xd[:, :w], qo, xd[:, w:w + kv * hd], xd[:, w + kv * hd:])
+    acc = dev(rng.random((1, kv, n), dtype=np.float32))
+    dst = dev((per + np.arange(per, dtype=np.int32))[None])
+    kept, acc_out = torch.empty(1, kv, keep, dtype=torch.int32, device="cuda"), torch.empty(1, kv, keep, device="cuda")
+    q.qmv_kv_evict(d.h, dst, keep, 4, 8, acc, kept, acc_out, d.lens)
+    assert int(host(d.lens)[0]) == keep
+    after = q.KvCache(t, kv, hd, page, d.pages, dst, d.lens)
+    d.lens.add_(m)
+    # tokens n, n + 1, n + 2 of the sequence at the cache's positions keep, keep + 1, keep + 2
+    y = rng.standard_normal((m, (heads + 2 * kv) * hd), dtype=np.float32)
+    yd, pos = dev(y), np.arange(n, n + m, dtype=np.int32)
+    yq, yk = torch.empty(m, w, device="cuda"), torch.empty(m, kv * hd, device="cuda")
+    q.qmv_qk_norm_rope(h, hd, m, dev(pos), heads, yd[:, :w], yq, kv, yd[:, w:w + kv * hd], yk)
+    q.qmv_kv_append(after, m, yk, yd[:, w + kv * hd:])
+    out = torch.empty(m, heads, hd, device="cuda")
+    q.qmv_attn_decode(after, m, heads, yq, hd ** -0.5, out, per * page,
+                      workspace=workspace(q.qmv_attn_decode_workspace(after, m, heads, per * page)))
+    want_k, tol_k = sref.rope(y[:, w:w + kv * hd].reshape(m, kv, hd), wk, pos, freq, hd, "halves", eps)
+    close(host(yk).reshape(want_k.shape), want_k, tol_k, "keys at their positions")
+    c.pool[:], c.seq_len[:], c.table[:] = d.pool(), keep + m, host(dst)
+    # the kept keys as they were turned, the new ones behind them
+    for hh in range(kv):
+        K, V, _ = c.rows(0, hh, keep + m)
+        old = sref.rope(x[:, w:w + kv * hd].reshape(n, kv, hd), wk, np.arange(n), freq, hd, "halves", eps)[0][:, hh]
+        rows = np.concatenate([old[host(kept)[0, hh]], want_k[:, hh]])
+        # f16: half a step relative, or of its smallest; 4 bits: a step and 8 2^-8 of one (1% more: f32), of an eighth
+        # of the block's largest, which the scale's rounding changes by 2^-8 relative
+        bound = (np.abs(rows) * (2.0 ** -11 + 1e-4) + 2.0 ** -25 if t == "f16" else
+                 np.repeat(np.abs(rows).reshape(keep + m, -1, 32).max(-1), 32, axis=-1) / 8 * (1 + 2.0 ** -8) * (1 + 8.1 * 2.0 ** -8))
+        close(K.astype(np.float32), rows, bound, "kept and new keys")
+    want, tol, _, _ = ref.attention(c, [0, m], host(yq).reshape(m, heads, hd), hd ** -0.5, per * page)
+    close(host(out), want, tol, "attention after an eviction")
+
+
 def test_two_streams_at_once():
     """Independent caches on two streams, calls interleaved: each as if alone."""
     rng = np.random.default_rng(10)
