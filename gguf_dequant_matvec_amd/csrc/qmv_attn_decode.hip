@@ -22,9 +22,10 @@
 // / 8 heads of 128, f16, 805 MB of cache: 129 - 130 us (6.2 TB/s; a streaming
 // read of the same size reaches 7.1) and 5.0 us for the join; one of 131071 int8
 // positions, 277 MB: 54 - 57 and 4.8 us; 301 positions, 9 / 3 heads of 64: 6.3
-// us, a chain of latencies.  The same with 4 bits: 227 MB, 51 - 56 us; 151 MB,
-// 35 - 38 us (4.0 TB/s), bound by the instructions that make operands of codes,
-// three a pair (with codes taken as they are, wrongly, 43 and 29 us); 6.9 us.
+// us, a chain of latencies.  The same with 4 bits: 227 MB, 56 - 60 us (the least
+// of 60 launches 51); 151 MB, 38 us (the least 35; 4.0 TB/s), bound by the
+// instructions that make operands of codes, three a pair (with codes taken as they
+// are, wrongly, 43 and 29 us at the least); 6.9 us.
 #include "qmv_attn.h"
 #include "qmv_internal.h"
 

@@ -15,7 +15,9 @@ constexpr int decode_chunk(int type) { return type == kKvI8 || type == kKvQ4 ? 6
 constexpr int kMaxPieces = 512;  // pieces of an output row that the join takes
 
 // Workgroups of four waves and 16-row tiles that the registers of a compute
-// unit hold at once (256 columns take more than half of them).
+// unit hold at once (256 columns take more than half of them; 4 bits of 128
+// columns spill one to three registers in even ranges, with more than 8 rows or
+// with weights and more than 4).
 constexpr int resident(int type, int hd) {
     if (hd == 256) return 1;
     return type == kKvQ4 || (hd == 64 && type != kKvI8) ? 3 : 2;

@@ -114,7 +114,9 @@ __device__ __forceinline__ void load_cols8(const float *p, float *f) {
 // the key-value heads do the same to HB heads of the rows' queries.  A K row
 // then goes through LDS, because its pairs are half a row apart and the cache
 // wants eight neighbours.  6808 rows of 32 / 8 heads of 128, bf16, 307 MB: 65 - 67
-// us (4.6 TB/s, a large copy's rate); 16 rows: 5.9 us.
+// us (4.6 TB/s, a large copy's rate); 16 rows: 5.9 us.  With the same rows each
+// time, of which a part stays in the last cache: bf16 60 us, int8 60, 4 bits 58;
+// 16 rows f16 6.4, int8 7.3, 4 bits 6.4.
 template <int TYPE, int HD, int ROWS, int ROPE>
 __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRows q, int64_t n, const int32_t *start,
                                                  const float *__restrict__ k, int64_t ldk,
@@ -367,7 +369,8 @@ __global__ __launch_bounds__(256) void kv_append(KvArgs c, RopeArgs rope, HeadRo
 // A workgroup takes 32 consecutive rows of one key-value head, four columns a
 // thread at a time.  K goes out as it comes.  V's lanes run over the rows first
 // (16 positions of a column are neighbours in a block) and go through LDS.  6808
-// rows of 8 heads of 128, 4 bits, 63.6 MB: 13.0 us (4.9 TB/s).
+// rows of 8 heads of 128, 4 bits, 63.6 MB: 13.0 us (4.9 TB/s); f16 and bf16, 83.7
+// MB, 15 us, int8 13.6 (the same rows each time); 16 rows 4.6 - 4.8 us.
 constexpr int kReadRows = 32;
 
 template <int TYPE>
@@ -844,7 +847,12 @@ template <int HD>
 hipError_t append_hd(const AppendCall &a, bool rope) {
     // 32 rows once that still gives two workgroups per compute unit (6808 rows
     // of 8 heads of 128: 20.8 us, with 16 rows 23.5, with 64 rows 23.6; 4 bits, which
-    // compute longer between reading and writing, 24.2 us and with 16 rows 21.5)
+    // compute longer between reading and writing, 24.2 us and with 16 rows 21.5).
+    // Turned rows take 32, of two heads a lane group, by the same count.  Measured
+    // beside it, 6808 rows of 32 / 8 heads: bf16 60 us and with 16 rows 56, 4 bits 57
+    // and 53, int8 59 and 58.  The count leaves queries out: 6808 rows of 16 / 2 heads
+    // take 16 rows of one head, 28 us, where 32 rows of two heads would take 30 (16 of
+    // two, 24).
     const bool many = a.n * a.c.n_kv >= 32 * 512;
     if (rope) return many ? append_rows<HD, 32, 2>(a) : append_rows<HD, 16, 1>(a);
     return many && a.type != kKvQ4 ? append_rows<HD, 32, 0>(a) : append_rows<HD, 16, 0>(a);

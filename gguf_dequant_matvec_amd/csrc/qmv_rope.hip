@@ -10,9 +10,11 @@ namespace {
 // A lane group takes HB heads of one row: their angles are the same, so cosines
 // and sines are found once for HB.  The first chunks of heads are Q's, the
 // others K's.  Bound by memory, every value read and written once, or for few
-// rows by latency: 6808 rows of 32 / 8 heads of 128, 279 MB, 46 us (a part stays
+// rows by latency.  Means of profiled launches: 6808 rows of 32 / 8 heads of 128,
+// 279 MB, 46 us, four heads a group (the same rows each time, so that a part stays
 // in the last cache; a large copy, 4.7 TB/s, would take 59); 3001 rows of 32 / 8
-// heads of 64, 61 MB, 12.7 - 13.4 us.
+// heads of 64, 61 MB, 13.3 us (one head, below the bound of launch_hd); 16 rows
+// of 32 / 8 heads of 128, 3.6 us.
 // (16 rows at least: the most rows a call may have, in workgroups of eight, would
 // be more threads than a launch takes.)
 template <int HD>

@@ -491,7 +491,12 @@ qmv_status qmv_qk_norm_rope(const qmv_qk_rope *rope, int32_t head_dim, int64_t n
  * its rows take there and stored as qmv_kv_append would store it, V as it is,
  * and Q goes to q_out (which may be q).  n, start, k and v as in qmv_kv_append;
  * the queries of rows that have no place in the cache (positions below 0, rows
- * of no sequence) are left out.  n_heads + n_kv_heads <= 65535.  One launch. */
+ * of no sequence) are left out.  n_heads >= 1, n_heads + n_kv_heads <= 65535.
+ * The angle's position is the row's place in the cache, which is the token's
+ * while every earlier token is cached.  After qmv_kv_evict it no longer is (kept
+ * keys stay turned by their old positions, and lengths are shorter): from then on
+ * take qmv_qk_norm_rope with positions of your own, and qmv_kv_append.  One
+ * launch. */
 qmv_status qmv_kv_append_rope(const qmv_kv_cache *cache, const qmv_qk_rope *rope, int64_t n,
                               const int32_t *start, int32_t n_heads, const float *q, int64_t ldq,
                               float *q_out, int64_t ldqo, const float *k, int64_t ldk, const float *v,
@@ -514,7 +519,7 @@ qmv_status qmv_kv_append_rope(const qmv_kv_cache *cache, const qmv_qk_rope *rope
  * are, and it asks for some; or the tokens asked for up to and with it are more
  * than n.  start int32[n_seq + 1]: sums of granted, the rows as qmv_kv_append,
  * qmv_kv_append_rope and qmv_attn_prefill take them.  pos int32[n], slot
- * int64[n], each may be NULL: the position of row r and its place in the pool,
+ * int64[n], each may be NULL: row r's position in the cache and place in the pool,
  * page * page_size + its slot there (-1 in a hole); -1 for both behind the last
  * row.  n <= QMV_MAX_KV_ROWS.  One launch, a second one for the rows where n is
  * above 4096.
@@ -600,7 +605,8 @@ size_t qmv_attn_prefill_workspace(const qmv_kv_cache *cache, int64_t n, int32_t 
  * later calls see (logit 0, value 0) where they did not see the hole: positions
  * whose pages were given back should not be among the protected ones.  A
  * sequence with seq_len <= keep is copied whole.  Afterwards the caller makes
- * dst_table the cache's table.
+ * dst_table the cache's table; positions in the cache are from then on not the
+ * tokens' own (see qmv_kv_append_rope).
  * acc: f32 [n_seq][n_kv_heads][ld_acc]; seq_len is taken as at most ld_acc.
  * Outputs: kept int32 [n_seq][n_kv_heads][keep], the old positions (-1 past
  * the new length); acc_out f32 [n_seq][n_kv_heads][ld_out], ld_out >= keep,
